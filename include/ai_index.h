@@ -316,6 +316,137 @@ int ai_debug_refine_split(ai_handle h, int32_t split);
  * C outside 1 .. max_budget.                                              */
 int ai_refine_kernel_choice(ai_handle h, int32_t C, int32_t* kernel_out);
 
+/* -------------------------------------------- attention over the keys */
+/* What a layer does with the selection: its queries attend over the keys and
+ * values of the request, which live in a paged cache next to the index.  No
+ * counterpart on the pages, which end at the indices; the formulas are
+ * ordinary softmax attention:
+ *     o = sum_j e^(s_j - m) v_j / sum_j e^(s_j - m),  s_j = scale * (q . k_j),
+ *     lse = m + ln sum_j e^(s_j - m),                 m = max_j s_j,
+ * over the keys j that the row sees.  A row that sees no key, or whose scores
+ * are all -inf, gives zeros and lse = -inf.  Keys and values that a row does
+ * not see have no influence on it, whatever they hold (NaN included).
+ * Forward only: the library selects and serves; it has no training path.
+ * n_heads query heads share n_kv_heads key heads in groups of
+ * n_heads / n_kv_heads consecutive heads.  Queries and outputs are bf16,
+ * sums and statistics float32, weights rounded to bf16 for the product with
+ * v; head_dim is 64 or 128.
+ * The calls are enqueued on cuda_stream, allocate nothing and may be captured;
+ * they need no handle.  Calls whose work may overlap (two streams, two graphs)
+ * need a workspace each.                                                  */
+
+/* A paged cache, all of it device memory of the caller's:
+ *   k, v        [n_layers, n_pages, page_size, n_kv_heads, head_dim] in
+ *               dtype (AI_BF16, or AI_FP8E4M3 codes), 16-byte aligned
+ *   k_scale,    [n_layers, n_pages, page_size, n_kv_heads] float32, one per
+ *   v_scale     token and head (AI_FP8E4M3), else NULL
+ *   tables      [n_seqs, max_pages] int32: page p of a sequence holds its
+ *               tokens [p * page_size, (p + 1) * page_size)
+ *   lens        [n_seqs] int32: tokens of each sequence
+ *   refs        [n_pages] int32: sequences that hold the page, 0 = free (only
+ *               the ai_cache_* calls use it; may be NULL for ai_attend_*)
+ *   status      NULL, or an int32 that collects AI_DEVFLAG_* bits: RANGE for
+ *               an id, sequence or page out of range (skipped, no access),
+ *               CAPACITY where pages ran out (that sequence is unchanged)
+ * n_pages at most 2^20; n_pages * page_size and max_pages * page_size below
+ * 2^31.                                                                   */
+typedef struct ai_cache {
+  void* k;
+  void* v;
+  float* k_scale;
+  float* v_scale;
+  int32_t* tables;
+  int32_t* lens;
+  int32_t* refs;
+  int32_t* status;
+  int32_t dtype, n_layers, n_pages, page_size, n_kv_heads, head_dim;
+  int32_t n_seqs, max_pages;
+} ai_cache;
+
+/* Causal attention over packed prompts.  Sequence b's queries are rows
+ * [cu_q[b], cu_q[b+1]) of q, its keys rows [cu_k[b], cu_k[b+1]) of k and v
+ * (device int32 [n_seqs + 1], ascending, within [0, total]).  The last query
+ * sees the last key: query i of Lq sees keys j <= Lk - Lq + i (so a chunk
+ * whose prefix precedes it in k and v is attended as it stands; with
+ * Lk < Lq the first rows see nothing).  q [total_q, n_heads, head_dim] and
+ * k, v [total_k, n_kv_heads, head_dim] bf16, the last dimension dense; the
+ * strides (in elements) of the first two are given as {token, head} pairs
+ * and are positive multiples of 8, bases 16-byte aligned.  out [total_q, n_heads,
+ * head_dim] bf16 and lse [total_q, n_heads] float32 (nullable) are dense;
+ * rows that belong to no sequence stay as they were.  status_dev: NULL or an
+ * int32 that collects AI_DEVFLAG_* bits (RANGE: cu_q / cu_k not as above;
+ * those sequences are skipped).
+ * Limit: n_heads / n_kv_heads at most 128.                                */
+int ai_attend_prompt(const void* q_dev, const int64_t* q_strides, const void* k_dev,
+                     const int64_t* k_strides, const void* v_dev, const int64_t* v_strides,
+                     const int32_t* cu_q_dev, const int32_t* cu_k_dev, int32_t n_seqs,
+                     int32_t total_q, int32_t total_k, int32_t n_heads, int32_t n_kv_heads,
+                     int32_t head_dim, float scale, void* out_dev, float* lse_dev,
+                     int32_t* status_dev, void* cuda_stream);
+
+/* Bytes of workspace that ai_attend_cached and ai_attend_selected need for
+ * these heads (whatever the lengths).                                     */
+int ai_attend_workspace(int32_t n_heads, int32_t n_kv_heads, int32_t head_dim, int64_t* bytes_out);
+
+/* One new token per sequence (decode): row r of q [n_rows, n_heads,
+ * head_dim] attends over all lens tokens of sequence seqs[r] of the cache.
+ * seqs_dev NULL: row r is sequence r (n_rows = n_seqs).                   */
+int ai_attend_cached(const ai_cache* cache, int32_t layer, const void* q_dev, int32_t n_rows,
+                     int32_t n_heads, const int32_t* seqs_dev, float scale, void* out_dev,
+                     float* lse_dev, void* workspace_dev, int64_t workspace_bytes,
+                     void* cuda_stream);
+
+/* Attention over selected keys: row t of q [T, n_heads, head_dim] attends
+ * over the tokens ids_dev[t, 0..k) (what ai_route_refine writes) of sequence
+ * seqs[t]; negative ids are no keys, an id that occurs twice counts twice.
+ * seqs_dev NULL: every row is the cache's only sequence (n_seqs = 1), or row
+ * t is sequence t (n_seqs = T).                                           */
+int ai_attend_selected(const ai_cache* cache, int32_t layer, const void* q_dev,
+                       const int32_t* ids_dev, int32_t T, int32_t k, int32_t n_heads,
+                       const int32_t* seqs_dev, float scale, void* out_dev, float* lse_dev,
+                       void* workspace_dev, int64_t workspace_bytes, void* cuda_stream);
+
+/* ------------------------------------------------- pages of the cache */
+/* All state is device memory and every change is made in stream order, so
+ * these calls may be captured too.  New pages are the lowest free ones, in
+ * the order of the list.  A sequence with lens = 0 is empty.  What a call
+ * refuses (bad index, a sequence listed twice, pages exhausted) is flagged in
+ * cache->status and left unchanged; the rest of the list is done.         */
+
+/* Bytes of workspace for a call with an n-entry list (ai_cache_compact: 0). */
+int ai_cache_workspace(const ai_cache* cache, int32_t n, int64_t* bytes_out);
+
+/* Lengthen sequence seqs[i] by counts[i] tokens, taking pages as needed.  A
+ * sequence is lengthened if the pages it and the listed ones before it need
+ * are there.  The new tokens' contents come with ai_cache_write, once per
+ * layer.                                                                  */
+int ai_cache_extend(const ai_cache* cache, const int32_t* seqs_dev, const int32_t* counts_dev,
+                    int32_t n, void* workspace_dev, int64_t workspace_bytes, void* cuda_stream);
+
+/* Write the keys and values [n_tokens, n_kv_heads, head_dim] bf16 (dense) of
+ * one layer: rows [cu[i], cu[i+1]) become the last cu[i+1] - cu[i] tokens of
+ * sequence seqs[i] (fp8: quantised as by ai_quantize_fp8, per token and
+ * head).  cu_dev int32 [n + 1], ascending; rows outside are not read.     */
+int ai_cache_write(const ai_cache* cache, int32_t layer, const void* k_dev, const void* v_dev,
+                   const int32_t* seqs_dev, const int32_t* cu_dev, int32_t n, int32_t n_tokens,
+                   void* cuda_stream);
+
+/* Make the empty sequence dst[i] a copy of sequence src[i]: full pages are
+ * shared, the filled slots of a part page are copied to a fresh page.  All
+ * forks of a call see the state before it.                                */
+int ai_cache_fork(const ai_cache* cache, const int32_t* src_dev, const int32_t* dst_dev, int32_t n,
+                  void* workspace_dev, int64_t workspace_bytes, void* cuda_stream);
+
+/* Release sequences: their pages lose one reference each, their table rows
+ * become -1, their lengths 0.                                             */
+int ai_cache_free(const ai_cache* cache, const int32_t* seqs_dev, int32_t n, void* cuda_stream);
+
+/* Move the live pages to the front of the cache: with L live pages, the i-th
+ * live page at or behind L moves to the i-th free page before L (all layers);
+ * tables and refs follow.                                                 */
+int ai_cache_compact(const ai_cache* cache, void* workspace_dev, int64_t workspace_bytes,
+                     void* cuda_stream);
+
 /* ------------------------------------------------- failure-path test hook */
 /* Runs the library's bounded wait against a barrier that nothing completes
  * (the pages have no counterpart: this exists to test failure detection).

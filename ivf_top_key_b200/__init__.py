@@ -14,8 +14,12 @@ import torch
 
 from . import _capi as C
 from ._capi import AiError  # noqa: F401
+from .attention import (PagedCache, attend_cached, attend_prompt, attend_selected, cache_compact, cache_extend,
+                        cache_fork, cache_free, cache_write)
 
-__all__ = ["AttentionIndex", "AiError", "quantize_fp8", "merge_topk", "C"]
+__all__ = ["AttentionIndex", "AiError", "quantize_fp8", "merge_topk", "C", "PagedCache", "attend_prompt",
+           "attend_cached", "attend_selected", "cache_extend", "cache_write", "cache_fork", "cache_free",
+           "cache_compact"]
 
 
 class AttentionIndex:
@@ -89,6 +93,18 @@ class AttentionIndex:
         if out_scores is None:
             out_scores = torch.empty((T, k), dtype=torch.float32, device=q.device)
         return C.ai_route_refine_shard(self.h, q, w, pos0, k, C_budget, shard, n_shards, out, out_scores)
+
+    def attend(self, q_index, w, pos0: int, k: int, C_budget: int, q, cache, seq: int = 0, *, layer: int = 0,
+               scale=None, out=None, out_ids=None, out_lse=None):
+        """route_refine, then attention of the same rows over the selected keys: the layer's step for a chunk.
+
+        q [T, Hq, D] are the attention queries of the rows at pos0 ..; cache is the PagedCache whose sequence
+        `seq` holds the keys and values of the index's keys.  Returns the attention output [T, Hq, D]."""
+        with torch.cuda.stream(self.stream):
+            ids = self.route_refine(q_index, w, pos0, k, C_budget, out=out_ids)
+            return attend_selected(q, ids, cache.k, cache.v, cache.tables[seq:seq + 1], cache.lens[seq:seq + 1],
+                                   layer=layer, k_scale=cache.k_scale, v_scale=cache.v_scale, scale=scale, out=out,
+                                   out_lse=out_lse, status=cache.status)
 
     def select_exhaustive(self, q, w, pos0: int, k: int, out=None, out_scores=None):
         if out is None:

@@ -32,6 +32,9 @@ EXPORTED = [
     "ai_kernel_launches", "ai_select_exhaustive_noalloc", "ai_debug_wait_timeout",
     "ai_route_refine_shard", "ai_merge_topk",
     "ai_debug_refine_kernel", "ai_refine_kernel_choice", "ai_debug_refine_split",
+    "ai_attend_prompt", "ai_attend_workspace", "ai_attend_cached", "ai_attend_selected",
+    "ai_cache_workspace", "ai_cache_extend", "ai_cache_write", "ai_cache_fork", "ai_cache_free",
+    "ai_cache_compact",
 ]
 PHASES = ["route", "refine", "seal", "refit", "publish", "exh_scores", "exh_topk", "order"]
 
@@ -55,6 +58,14 @@ class AiStats(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int64) for n in (
         "n_keys", "n_sealed", "n_clusters", "n_versions", "n_refits", "refit_pending",
         "base_watermark", "last_refit_scanned", "last_refit_rechecked")]
+
+
+class AiCache(ctypes.Structure):
+    """ai_cache: the device arrays of a paged key-value cache."""
+    _fields_ = [(n, ctypes.c_void_p) for n in (
+        "k", "v", "k_scale", "v_scale", "tables", "lens", "refs", "status")] + [
+        (n, ctypes.c_int32) for n in (
+            "dtype", "n_layers", "n_pages", "page_size", "n_kv_heads", "head_dim", "n_seqs", "max_pages")]
 
 
 class AiError(RuntimeError):
@@ -94,6 +105,17 @@ def _load():
         "ai_debug_refine_kernel": [vp, i32],
         "ai_debug_refine_split": [vp, i32],
         "ai_refine_kernel_choice": [vp, i32, ctypes.POINTER(i32)],
+        "ai_attend_prompt": [vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, ctypes.c_float,
+                             vp, vp, vp, vp],
+        "ai_attend_workspace": [i32, i32, i32, ctypes.POINTER(i64)],
+        "ai_attend_cached": [vp, i32, vp, i32, i32, vp, ctypes.c_float, vp, vp, vp, i64, vp],
+        "ai_attend_selected": [vp, i32, vp, vp, i32, i32, i32, vp, ctypes.c_float, vp, vp, vp, i64, vp],
+        "ai_cache_workspace": [vp, i32, ctypes.POINTER(i64)],
+        "ai_cache_extend": [vp, vp, vp, i32, vp, i64, vp],
+        "ai_cache_write": [vp, i32, vp, vp, vp, vp, i32, i32, vp],
+        "ai_cache_fork": [vp, vp, vp, i32, vp, i64, vp],
+        "ai_cache_free": [vp, vp, i32, vp],
+        "ai_cache_compact": [vp, vp, i64, vp],
     }
     for name, args in sig.items():
         f = getattr(lib, name)
@@ -290,6 +312,60 @@ def ai_refine_kernel_choice(h, C: int) -> int:
     v = ctypes.c_int32()
     _check(_lib.ai_refine_kernel_choice(h, C, ctypes.byref(v)))
     return v.value
+
+
+# ---- attention over the keys; tensors are passed as addresses (ints or
+# None) because the callers below check them and strides go separately
+
+def ai_attend_prompt(q, q_strides, k, k_strides, v, v_strides, cu_q, cu_k, n_seqs: int, total_q: int, total_k: int,
+                     n_heads: int, n_kv_heads: int, head_dim: int, scale: float, out, lse, status, stream: int):
+    pair = ctypes.c_int64 * 2
+    _check(_lib.ai_attend_prompt(q, pair(*q_strides), k, pair(*k_strides), v, pair(*v_strides), cu_q, cu_k, n_seqs,
+                                 total_q, total_k, n_heads, n_kv_heads, head_dim, scale, out, lse, status, stream))
+
+
+def ai_attend_workspace(n_heads: int, n_kv_heads: int, head_dim: int) -> int:
+    v = ctypes.c_int64()
+    _check(_lib.ai_attend_workspace(n_heads, n_kv_heads, head_dim, ctypes.byref(v)))
+    return v.value
+
+
+def ai_attend_cached(cache: AiCache, layer: int, q, n_rows: int, n_heads: int, seqs, scale: float, out, lse,
+                     workspace, workspace_bytes: int, stream: int):
+    _check(_lib.ai_attend_cached(ctypes.byref(cache), layer, q, n_rows, n_heads, seqs, scale, out, lse, workspace,
+                                 workspace_bytes, stream))
+
+
+def ai_attend_selected(cache: AiCache, layer: int, q, ids, T: int, k: int, n_heads: int, seqs, scale: float, out, lse,
+                       workspace, workspace_bytes: int, stream: int):
+    _check(_lib.ai_attend_selected(ctypes.byref(cache), layer, q, ids, T, k, n_heads, seqs, scale, out, lse, workspace,
+                                   workspace_bytes, stream))
+
+
+def ai_cache_workspace(cache: AiCache, n: int) -> int:
+    v = ctypes.c_int64()
+    _check(_lib.ai_cache_workspace(ctypes.byref(cache), n, ctypes.byref(v)))
+    return v.value
+
+
+def ai_cache_extend(cache: AiCache, seqs, counts, n: int, workspace, workspace_bytes: int, stream: int):
+    _check(_lib.ai_cache_extend(ctypes.byref(cache), seqs, counts, n, workspace, workspace_bytes, stream))
+
+
+def ai_cache_write(cache: AiCache, layer: int, k, v, seqs, cu, n: int, n_tokens: int, stream: int):
+    _check(_lib.ai_cache_write(ctypes.byref(cache), layer, k, v, seqs, cu, n, n_tokens, stream))
+
+
+def ai_cache_fork(cache: AiCache, src, dst, n: int, workspace, workspace_bytes: int, stream: int):
+    _check(_lib.ai_cache_fork(ctypes.byref(cache), src, dst, n, workspace, workspace_bytes, stream))
+
+
+def ai_cache_free(cache: AiCache, seqs, n: int, stream: int):
+    _check(_lib.ai_cache_free(ctypes.byref(cache), seqs, n, stream))
+
+
+def ai_cache_compact(cache: AiCache, workspace, workspace_bytes: int, stream: int):
+    _check(_lib.ai_cache_compact(ctypes.byref(cache), workspace, workspace_bytes, stream))
 
 
 def ai_last_error() -> str:

@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+struct ai_cache;  // include/ai_index.h
+
 namespace aiidx {
 
 // Kernel launches made by this library (all handles, all streams).
@@ -233,5 +235,10 @@ cudaError_t launch_quantize_fp8(const uint16_t* keys_bf16, int64_t n, int d, uin
                                 float* scales, cudaStream_t st);
 cudaError_t launch_fp8_codes_to_bf16(const uint8_t* codes, int64_t n, int d, uint16_t* out,
                                      cudaStream_t st);
+
+// ------------------------------------------------------ paged cache checks
+// AI_OK, or AI_ERR_ARG with a message: null or misaligned arrays, sizes out
+// of range, scales missing (fp8) or given (bf16).
+int check_cache(const ai_cache* c);
 
 }  // namespace aiidx
