@@ -330,7 +330,7 @@ int ai_refine_kernel_choice(ai_handle h, int32_t C, int32_t* kernel_out);
  * n_heads query heads share n_kv_heads key heads in groups of
  * n_heads / n_kv_heads consecutive heads.  Queries and outputs are bf16,
  * sums and statistics float32, weights rounded to bf16 for the product with
- * v; head_dim is 64 or 128.
+ * v; head_dim is 64 or 128, scale finite and not negative.
  * The calls are enqueued on cuda_stream, allocate nothing and may be captured;
  * they need no handle.  Calls whose work may overlap (two streams, two graphs)
  * need a workspace each.                                                  */
@@ -374,8 +374,8 @@ typedef struct ai_cache {
  * and are positive multiples of 8, bases 16-byte aligned.  out [total_q, n_heads,
  * head_dim] bf16 and lse [total_q, n_heads] float32 (nullable) are dense;
  * rows that belong to no sequence stay as they were.  status_dev: NULL or an
- * int32 that collects AI_DEVFLAG_* bits (RANGE: cu_q / cu_k not as above;
- * those sequences are skipped).
+ * int32 that collects AI_DEVFLAG_* bits (RANGE: cu_q / cu_k not as above,
+ * nothing out of range is touched but the output is not valid).
  * Limit: n_heads / n_kv_heads at most 128.                                */
 int ai_attend_prompt(const void* q_dev, const int64_t* q_strides, const void* k_dev,
                      const int64_t* k_strides, const void* v_dev, const int64_t* v_strides,

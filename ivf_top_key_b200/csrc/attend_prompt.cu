@@ -2,8 +2,30 @@
 //
 //   o_i = sum_{j <= i + Lk - Lq} e^(s_ij - m_i) v_j / sum_j e^(s_ij - m_i)
 //
-// One warp per (query, head): lanes hold 32 keys' scores at a time, the
-// running maximum and sum in fp32, and the output spread over the lanes.
+// One persistent CTA per SM.  A work item is one key head and a block of
+// consecutive queries of one sequence; the G query heads of the key head and
+// the block's tokens are the rows of two 128-row tiles (row = token * G +
+// head), so a short prompt fills a tile with its heads and every key tile is
+// read once for both tiles.  Per 128 keys and tile:
+//   S = Q K^T     tcgen05, operands in shared memory, S fp32 in TMEM
+//   P = e^(S - m) one thread per row, P written as bf16 over S in TMEM
+//   O += P V      tcgen05, P from TMEM, V as it lies in memory (N-major)
+// Warps 0-3 and 4-7 are the rows of tile 0 and 1, warp 8 issues the TMA
+// loads (K and V tiles through one ring), warp 9 the products.  While one
+// tile's exponentials run, the other tile's products do.
+//
+// m is the row maximum when it was last moved: O is rescaled only where the
+// maximum has grown by more than 2^8 (the weights stay far inside bf16's and
+// the sum inside fp32's range, and the quotient is the same), so the rescale
+// through TMEM is rare.
+//
+// Rows that do not see a key must not feel its value, but 0 * NaN is NaN in a
+// matrix product: warps 10-11 look at the V tiles that some row sees in part.
+// Rows behind the sequence's end are zeroed there; if a value before it is not
+// finite, the item is computed again by attend_row, which reads only the keys
+// that each row sees.
+#include <cudaTypedefs.h>
+
 #include <cmath>
 
 #include "../../include/ai_index.h"
@@ -50,12 +72,9 @@ __device__ __forceinline__ bool seq_rows(const PromptArgs& a, int b, int* q0, in
 
 // One query row of one head by one warp, reading only the keys it sees.
 template <int D>
-__device__ void attend_row(const PromptArgs& a, int qi, int h, int k0, int n_keys, float* sq /* [D] of this warp */) {
+__device__ __noinline__ void attend_row(const PromptArgs& a, int qi, int h, int k0, int n_keys) {
   const int lane = threadIdx.x & 31;
   const uint16_t* q = a.q + qi * a.q_tok + h * a.q_head;
-  __syncwarp();
-  for (int d = lane; d < D; d += 32) sq[d] = bf16_bits_to_f32(q[d]);
-  __syncwarp();
   const int kh = h / a.G;
   float m = -INFINITY, l = 0.f, o[D / 32];
 #pragma unroll
@@ -66,15 +85,7 @@ __device__ void attend_row(const PromptArgs& a, int qi, int h, int k0, int n_key
     if (j < n_keys) {
       const uint16_t* k = a.k + static_cast<int64_t>(k0 + j) * a.k_tok + kh * a.k_head;
       float x = 0.f;
-      for (int d = 0; d < D; d += 8) {
-        const uint4 u = *reinterpret_cast<const uint4*>(k + d);
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          x = fmaf(sq[d + 2 * i], __uint_as_float(w[i] << 16), x);
-          x = fmaf(sq[d + 2 * i + 1], __uint_as_float(w[i] & 0xffff0000u), x);
-        }
-      }
+      for (int d = 0; d < D; ++d) x = fmaf(bf16_bits_to_f32(q[d]), bf16_bits_to_f32(k[d]), x);
       s = x * a.c2;
     }
     float mx = s;
@@ -103,19 +114,539 @@ __device__ void attend_row(const PromptArgs& a, int qi, int h, int k0, int n_key
   if (a.lse && lane == 0) a.lse[static_cast<int64_t>(qi) * a.Hq + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
+// ------------------------------------------------------------ tensor cores
+constexpr int kTile = 128;        // rows of a query tile, keys of a key tile
+constexpr int kThreads = 384;
+constexpr float kGrow = 8.f;      // log2 by which the maximum may grow before O is rescaled
+
 template <int D>
-__global__ void __launch_bounds__(256) k_prompt_rows(PromptArgs a) {
-  __shared__ float sq[8][D];
-  const int warp = threadIdx.x >> 5;
-  const int b = blockIdx.y;
-  int q0, lq, k0, lk;
-  if (!seq_rows(a, b, &q0, &lq, &k0, &lk)) return;
-  const int64_t n = static_cast<int64_t>(lq) * a.Hq;
-  for (int64_t i = blockIdx.x * 8ll + warp; i < n; i += gridDim.x * 8ll) {
-    const int row = static_cast<int>(i / a.Hq), h = static_cast<int>(i % a.Hq);
-    const int64_t seen = static_cast<int64_t>(lk) - lq + row + 1;
-    attend_row<D>(a, q0 + row, h, k0, seen < 0 ? 0 : static_cast<int>(seen), sq[warp]);
+struct Smem {
+  static constexpr int kHalves = D / 64;          // 64-element (128-byte) column blocks
+  static constexpr int kTileBytes = kTile * D * 2;
+  static constexpr int kSlots = D == 128 ? 5 : 8; // ring of K and V tiles
+  static constexpr int kBars = 4 + 4 * kSlots + 6;
+  static constexpr int kSick = 8;                 // > items that the ring can be ahead
+  static constexpr int kBytes = 1024 + (2 + kSlots) * kTileBytes + kBars * 8 + 8 + kSick * 4;
+  static_assert(kBytes <= 227 * 1024, "shared memory");
+};
+
+// TMEM columns: the two score tiles (their weights over them), the two outputs.
+constexpr uint32_t kColS = 0, kColO = 256;
+
+// One work item.
+struct Item {
+  int head, qtok, n_tok;      // key head, first query row, queries in the block (0: nothing to do)
+  int k0, lk;                 // first key row, keys of the sequence
+  int see0;                   // keys that the block's first query sees (may be <= 0)
+  int tiles[2];               // key tiles that each query tile needs
+  __device__ int see(int tok) const { return max(0, min(lk, see0 + tok)); }
+  __device__ int n() const { return max(tiles[0], tiles[1]); }
+  // whether some row does not see all of key tile j
+  __device__ bool mixed(int j) const { return (j + 1) * kTile > see(0); }
+};
+
+struct Schedule {
+  int n_slots, qb, tpt;       // slots per key head, queries per block and per tile
+  int64_t n_items;
+};
+
+// Slot s belongs to the last sequence b with cu_q[b] / qb + b <= s: each
+// sequence has at least as many slots as blocks.
+__device__ Item item_at(const PromptArgs& a, const Schedule& sc, int64_t it) {
+  Item x;
+  x.head = static_cast<int>(it / sc.n_slots);
+  const int slot = sc.n_slots - 1 - static_cast<int>(it % sc.n_slots);  // the longest rows first
+  int lo = 0, hi = a.n_seqs;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) / 2;
+    if (a.cu_q[mid] / sc.qb + mid <= slot) lo = mid;
+    else hi = mid;
   }
+  x.n_tok = 0;
+  x.tiles[0] = x.tiles[1] = 0;
+  int q0, lq;
+  if (!seq_rows(a, lo, &q0, &lq, &x.k0, &x.lk)) return x;
+  const int blk = slot - (q0 / sc.qb + lo);
+  const int64_t first = static_cast<int64_t>(blk) * sc.qb;
+  if (blk < 0 || first >= lq) return x;
+  x.qtok = q0 + static_cast<int>(first);
+  x.n_tok = static_cast<int>(min(static_cast<int64_t>(sc.qb), lq - first));
+  x.see0 = static_cast<int>(max(static_cast<int64_t>(x.lk) - lq + first + 1, static_cast<int64_t>(-(1 << 30))));
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int last = min((i + 1) * sc.tpt, x.n_tok) - 1;
+    x.tiles[i] = last >= i * sc.tpt ? (x.see(last) + kTile - 1) / kTile : 0;
+  }
+  return x;
+}
+
+// The r-th item of this CTA; every other round runs backwards, so that costs
+// that fall along the items even out.
+__device__ __forceinline__ int64_t item_of_round(int64_t r) {
+  return r * gridDim.x + ((r & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+}
+
+// Matrix descriptor of an operand that lies N-major (rows of K, 64 elements
+// of N per 128-byte row): 8-row groups 1024 bytes apart along K, 64-element
+// column blocks `block` bytes apart.
+__device__ __forceinline__ uint64_t sdesc_sw128_mn(uint32_t saddr, uint32_t block) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>(block >> 4) << 16;
+  d |= static_cast<uint64_t>(1024 >> 4) << 32;
+  d |= static_cast<uint64_t>(1) << 46;
+  d |= static_cast<uint64_t>(2) << 61;
+  return d;
+}
+// D[tmem] (+)= A[tmem] * B[smem].
+__device__ __forceinline__ void umma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                             uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+          taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&b);
+}
+
+__device__ int g_no_status;  // where flags go when the caller gives no status word
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    k_prompt_tc(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+                const __grid_constant__ CUtensorMap map_v, const PromptArgs a, const Schedule sc) {
+  using L = Smem<D>;
+  constexpr int kSlots = L::kSlots;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sq = base;                              // [2] query tiles
+  uint8_t* ring = base + 2 * L::kTileBytes;        // [kSlots] key / value tiles
+  uint64_t* bars = reinterpret_cast<uint64_t*>(ring + kSlots * L::kTileBytes);
+  uint64_t* q_full = bars;                         // [2] query tile landed
+  uint64_t* q_empty = bars + 2;                    // [2] last product that reads it done
+  uint64_t* kv_full = bars + 4;                    // [kSlots] key tile, or V tile that every row sees whole
+  uint64_t* kv_empty = kv_full + kSlots;
+  uint64_t* mx_full = kv_empty + kSlots;           // [kSlots] V tile that some row sees in part
+  uint64_t* v_clean = mx_full + kSlots;            // [kSlots] and looked at
+  uint64_t* s_full = v_clean + kSlots;             // [2] scores in TMEM
+  uint64_t* p_full = s_full + 2;                   // [2] weights in TMEM
+  uint64_t* o_full = p_full + 2;                   // [2] product with V done
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(o_full + 2);
+  int* abort = reinterpret_cast<int*>(tmem_slot + 1);
+  int* sick = abort + 1;                           // [kSick] by item: its number + 1 where a value is bad
+  int* err = a.status ? a.status : &g_no_status;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&q_full[i], 1);
+      mbar_init(&q_empty[i], 1);
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], 128);
+      mbar_init(&o_full[i], 1);
+    }
+    for (int s = 0; s < kSlots; ++s) {
+      mbar_init(&kv_full[s], 1);
+      mbar_init(&kv_empty[s], 1);
+      mbar_init(&mx_full[s], 1);
+      mbar_init(&v_clean[s], 64);
+    }
+    *abort = 0;
+    for (int i = 0; i < L::kSick; ++i) sick[i] = 0;
+    fence_mbar_init();
+  }
+  if (warp == 9) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 8) {
+    // ---------------------------------------------------------- TMA loads
+    if (lane == 0) {
+      uint32_t g = 0, nq[2] = {0, 0};
+      // by slot: parity of the next phase of its two barriers, and which one
+      // its last load completes on
+      uint32_t kv_next = 0, mx_next = 0, last_mx = 0;
+      bool ok = true;
+      for (int64_t r = 0; ok && item_of_round(r) < sc.n_items; ++r) {
+        const Item x = item_at(a, sc, item_of_round(r));
+        for (int i = 0; ok && i < 2; ++i) {
+          if (x.tiles[i] == 0) continue;
+          if (nq[i] > 0 && !mbar_wait(&q_empty[i], (nq[i] - 1) & 1, err, abort)) {
+            ok = false;
+            break;
+          }
+          mbar_arrive_expect_tx(&q_full[i], sc.tpt * a.G * D * 2);
+          for (int c = 0; c < L::kHalves; ++c)
+            tma_load_3d(sq + i * L::kTileBytes + c * (kTile * 128), &map_q, c * 64, x.head * a.G, x.qtok + i * sc.tpt,
+                        &q_full[i]);
+          ++nq[i];
+        }
+        const int n = x.n();
+        for (int t = 0; ok && t < 2 * n; ++t, ++g) {  // K 0, V 0, K 1, V 1, ..
+          const int s = g % kSlots;
+          if (g >= kSlots && !mbar_wait(&kv_empty[s], (g / kSlots - 1) & 1, err, abort)) {
+            ok = false;
+            break;
+          }
+          const bool mx = (t & 1) && x.mixed(t >> 1);
+          uint64_t* full = mx ? &mx_full[s] : &kv_full[s];
+          if (mx) {
+            mx_next ^= 1u << s;
+            last_mx |= 1u << s;
+          } else {
+            kv_next ^= 1u << s;
+            last_mx &= ~(1u << s);
+          }
+          mbar_arrive_expect_tx(full, L::kTileBytes);
+          for (int c = 0; c < L::kHalves; ++c)
+            tma_load_3d(ring + s * L::kTileBytes + c * (kTile * 128), t & 1 ? &map_v : &map_k, c * 64, x.head,
+                        x.k0 + (t >> 1) * kTile, full);
+        }
+      }
+      if (*abort) {  // copies of this thread may still be landing: bounded waits
+        for (uint32_t s = 0; s < min(g, static_cast<uint32_t>(kSlots)); ++s) {
+          const bool mx = (last_mx >> s) & 1;
+          mbar_drain(mx ? &mx_full[s] : &kv_full[s], (((mx ? mx_next : kv_next) >> s) & 1) ^ 1);
+        }
+        for (int i = 0; i < 2; ++i)
+          if (nq[i] > 0) mbar_drain(&q_full[i], (nq[i] - 1) & 1);
+      }
+    }
+  } else if (warp == 9) {
+    // ----------------------------------------------------------- products
+    if (lane == 0) {
+      constexpr uint32_t id_s = idesc_bf16_f32(kTile, kTile);
+      constexpr uint32_t id_o = idesc_bf16_f32(kTile, D) | (1u << 16);  // B is N-major
+      uint32_t g = 0, nq[2] = {0, 0}, np[2] = {0, 0}, clean = 0, full = 0;  // next parities by slot
+      bool ok = true;
+      auto wait_slot = [&](uint32_t e) {
+        const uint32_t s = e % kSlots, parity = (full >> s) & 1;
+        full ^= 1u << s;
+        return mbar_wait(&kv_full[s], parity, err, abort);
+      };
+      auto scores = [&](int i, uint32_t e) {  // S_i = Q_i K^T
+        const uint32_t qa = smem_u32(sq + i * L::kTileBytes), ka = smem_u32(ring + (e % kSlots) * L::kTileBytes);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = (kk >> 2) * (kTile * 128) + (kk & 3) * 32;
+          umma_bf16(tmem + kColS + i * 128, sdesc_sw128(qa + off), sdesc_sw128(ka + off), id_s, kk > 0);
+        }
+        umma_commit(&s_full[i]);
+      };
+      auto outputs = [&](int i, uint32_t e, bool first) {  // O_i (+)= P_i V
+        const uint32_t va = smem_u32(ring + (e % kSlots) * L::kTileBytes);
+#pragma unroll
+        for (int kk = 0; kk < kTile / 16; ++kk)
+          umma_bf16_ta(tmem + kColO + i * 128, tmem + kColS + i * 128 + kk * 8,
+                       sdesc_sw128_mn(va + kk * 16 * 128, kTile * 128), id_o, !first || kk > 0);
+        umma_commit(&o_full[i]);
+      };
+      for (int64_t r = 0; ok && item_of_round(r) < sc.n_items; ++r) {
+        const Item x = item_at(a, sc, item_of_round(r));
+        const int n = x.n();
+        if (n == 0) continue;
+        ok = wait_slot(g);
+        for (int i = 0; ok && i < 2; ++i) {
+          if (x.tiles[i] == 0) continue;
+          if (!mbar_wait(&q_full[i], nq[i] & 1, err, abort)) {
+            ok = false;
+            break;
+          }
+          ++nq[i];
+          tc_fence_after();
+          scores(i, g);
+          if (x.tiles[i] == 1) umma_commit(&q_empty[i]);
+        }
+        if (!ok) break;
+        umma_commit(&kv_empty[g % kSlots]);
+        for (int j = 0; ok && j < n; ++j) {
+          const uint32_t ev = g + 2 * j + 1, ek = ev + 1;
+          if (x.mixed(j)) {
+            const int s = ev % kSlots;
+            ok = mbar_wait(&v_clean[s], (clean >> s) & 1, err, abort);
+            clean ^= 1u << s;
+          } else {
+            ok = wait_slot(ev);
+          }
+          if (ok && j + 1 < n) ok = wait_slot(ek);
+          for (int i = 0; ok && i < 2; ++i) {
+            if (j < x.tiles[i]) {
+              if (!mbar_wait(&p_full[i], np[i] & 1, err, abort)) {
+                ok = false;
+                break;
+              }
+              ++np[i];
+              tc_fence_after();
+              outputs(i, ev, j == 0);
+            }
+            if (i == 1) umma_commit(&kv_empty[ev % kSlots]);
+            if (j + 1 < x.tiles[i]) {
+              scores(i, ek);
+              if (j + 2 == x.tiles[i]) umma_commit(&q_empty[i]);
+            }
+            if (i == 1 && j + 1 < n) umma_commit(&kv_empty[ek % kSlots]);
+          }
+        }
+        g += 2 * n;
+      }
+      // every product issued has completed before the TMEM is released
+      for (int i = 0; i < 2; ++i) {
+        if (np[i] > 0) mbar_drain(&o_full[i], (np[i] - 1) & 1);
+        if (*abort && nq[i] > 0) mbar_drain(&s_full[i], np[i] & 1);
+      }
+    }
+  } else if (warp >= 10) {
+    // ------------------------------------------- V tiles that are seen in part
+    const int t = threadIdx.x - 320;
+    uint32_t g = 0, full = 0;
+    int item = 0;
+    bool ok = true;
+    if (blockIdx.x == 0)  // every sequence's offsets, whatever the schedule reaches
+      for (int b = t; b < a.n_seqs; b += 64) {
+        int q0, lq, k0, lk;
+        seq_rows(a, b, &q0, &lq, &k0, &lk);
+      }
+    for (int64_t r = 0; ok && item_of_round(r) < sc.n_items; ++r) {
+      const Item x = item_at(a, sc, item_of_round(r));
+      const int n = x.n();
+      for (int j = 0; ok && j < n; ++j) {
+        if (!x.mixed(j)) continue;
+        const uint32_t e = g + 2 * j + 1;
+        const int s = e % kSlots;
+        ok = __all_sync(0xffffffffu, mbar_wait(&mx_full[s], (full >> s) & 1, err, abort));
+        if (!ok) break;
+        full ^= 1u << s;
+        const int lo = max(0, x.see(0) - j * kTile), hi = min(kTile, x.lk - j * kTile);
+        uint32_t bad = 0;
+        // 16-byte unit u of the tile: row (u / 8) % 128; the swizzle stays within a row
+        for (int u = t; u < L::kTileBytes / 16; u += 64) {
+          const int row = (u >> 3) & (kTile - 1);
+          uint4* p = reinterpret_cast<uint4*>(ring + s * L::kTileBytes) + u;
+          if (row >= hi) {
+            *p = make_uint4(0, 0, 0, 0);
+          } else if (row >= lo) {
+            const uint4 w = *p;
+            // the carry out of an exponent of ones: infinity or NaN
+            bad |= ((w.x & 0x7f807f80u) + 0x00800080u) | ((w.y & 0x7f807f80u) + 0x00800080u) |
+                   ((w.z & 0x7f807f80u) + 0x00800080u) | ((w.w & 0x7f807f80u) + 0x00800080u);
+          }
+        }
+        if (bad & 0x80008000u) reinterpret_cast<volatile int*>(sick)[item % L::kSick] = item + 1;
+        fence_proxy_async_smem();
+        mbar_arrive(&v_clean[s]);
+      }
+      g += 2 * n;
+      item += n > 0;
+    }
+  } else {
+    // ------------------------------------------------------------ softmax
+    const int i = warp >> 2;                         // query tile
+    const int row = (warp & 3) * 32 + lane;          // row of the tile = TMEM lane
+    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t ts = tmem + kColS + i * 128 + lane_off, to = tmem + kColO + i * 128 + lane_off;
+    const int tok = i * sc.tpt + row / a.G, gh = row % a.G;
+    const bool used = row < sc.tpt * a.G;
+    uint32_t np = 0;
+    int item = 0;
+    bool ok = true;
+    for (int64_t r = 0; ok && item_of_round(r) < sc.n_items; ++r) {
+      const Item x = item_at(a, sc, item_of_round(r));
+      const int n = x.tiles[i];
+      const int see = x.see(tok);
+      float m = -INFINITY, l = 0.f;
+      for (int j = 0; j < n; ++j, ++np) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&s_full[i], np & 1, err, abort));
+        if (!ok) break;
+        tc_fence_after();
+        const int limit = see - j * kTile;
+        const bool part = (j + 1) * kTile > x.see(i * sc.tpt);  // warp-uniform
+        float mx = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < 4; c += 2) {
+          float v[2][32];
+          tmem_ld32(ts + c * 32, v[0]);
+          tmem_ld32(ts + c * 32 + 32, v[1]);
+          tmem_ld_wait();
+          if (part) {
+#pragma unroll
+            for (int u = 0; u < 64; ++u) mx = c * 32 + u < limit ? fmaxf(mx, v[u >> 5][u & 31]) : mx;
+          } else {
+            float m1 = -INFINITY;
+#pragma unroll
+            for (int u = 0; u < 32; ++u) {
+              mx = fmaxf(mx, v[0][u]);
+              m1 = fmaxf(m1, v[1][u]);
+            }
+            mx = fmaxf(mx, m1);
+          }
+        }
+        const float want = mx == -INFINITY ? -INFINITY : mx * a.c2;
+        const bool move = j == 0 || want > m + kGrow;
+        if (j == 0) {
+          m = want;
+        } else if (__any_sync(0xffffffffu, move)) {
+          const float mz = move ? want : m;
+          const float f = move ? ex2(m - mz) : 1.f;  // m = -inf: nothing seen so far, O and l are 0
+          ok = __all_sync(0xffffffffu, mbar_wait(&o_full[i], (np - 1) & 1, err, abort));
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int c = 0; c < D / 16; ++c) {
+            float v[16];
+            uint32_t w[16];
+            tmem_ld16(to + c * 16, v);
+            tmem_ld_wait();
+#pragma unroll
+            for (int u = 0; u < 16; ++u) w[u] = __float_as_uint(v[u] * f);
+            tmem_st16(to + c * 16, w);
+          }
+          l *= f;
+          m = mz;
+        }
+        const float mu = m == -INFINITY ? 0.f : m;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          float v[32];
+          uint32_t w[16];
+          tmem_ld32(ts + c * 32, v);
+          tmem_ld_wait();
+#pragma unroll
+          for (int u = 0; u < 32; ++u) {
+            v[u] = ex2(fmaf(v[u], a.c2, -mu));
+            if (part) v[u] = c * 32 + u < limit ? v[u] : 0.f;
+          }
+          float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+          for (int u = 0; u < 32; u += 2) {
+            s0 += v[u];
+            s1 += v[u + 1];
+            w[u / 2] = pack2(v[u], v[u + 1]);
+          }
+          l += s0 + s1;
+          tmem_st16(ts + c * 16, w);  // over scores that are read already
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(&p_full[i]);
+      }
+      if (!ok) break;
+      if (n > 0) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&o_full[i], (np - 1) & 1, err, abort));
+        if (!ok) break;
+        tc_fence_after();
+      }
+      const bool mine = used && tok < x.n_tok;
+      const bool again = reinterpret_cast<volatile int*>(sick)[item % L::kSick] == item + 1;
+      if (n > 0 && __any_sync(0xffffffffu, again)) {
+        // each warp its own rows: the other tile's keys may be looked at meanwhile
+        for (int rr = (warp & 3) * 32; rr < min(sc.tpt * a.G, (warp & 3) * 32 + 32); ++rr) {
+          const int tt = i * sc.tpt + rr / a.G;
+          if (tt < x.n_tok) attend_row<D>(a, x.qtok + tt, x.head * a.G + rr % a.G, x.k0, x.see(tt));
+        }
+      } else {
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        uint16_t* out = a.out + (static_cast<int64_t>(x.qtok + tok) * a.Hq + x.head * a.G + gh) * D;
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          float v[32];
+          if (n > 0) {
+            tmem_ld32(to + c * 32, v);
+            tmem_ld_wait();
+          }
+          if (mine) {
+            // a row that sees nothing is zero even where its tile computed something
+#pragma unroll
+            for (int u = 0; u < 32; u += 8) {
+              uint4 w = make_uint4(0, 0, 0, 0);
+              if (l != 0.f)
+                w = make_uint4(pack2(v[u] * inv, v[u + 1] * inv), pack2(v[u + 2] * inv, v[u + 3] * inv),
+                               pack2(v[u + 4] * inv, v[u + 5] * inv), pack2(v[u + 6] * inv, v[u + 7] * inv));
+              *reinterpret_cast<uint4*>(out + c * 32 + u) = w;
+            }
+          }
+        }
+        if (mine && a.lse)
+          a.lse[static_cast<int64_t>(x.qtok + tok) * a.Hq + x.head * a.G + gh] =
+              l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+      }
+      item += x.n() > 0;
+      tc_fence_before();  // O is read before the next item's first product writes it
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Tensor map of [tokens, heads, D] bf16 with a box of 64 elements x
+// box_heads x box_tokens, 128-byte swizzle; out-of-range rows read 0.
+bool map_rows(CUtensorMap* m, const void* p, int64_t tokens, int heads, int D, int64_t tok_stride, int64_t head_stride,
+              int box_heads, int box_tokens) {
+  static PFN_cuTensorMapEncodeTiled_v12000 enc = nullptr;
+  if (!enc) {
+    void* fn = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &fn, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess || !fn)
+      return false;
+    enc = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+  }
+  // a dimension of one element never moves by its stride
+  if (heads == 1) head_stride = D;
+  if (tokens == 1) tok_stride = static_cast<int64_t>(heads) * D;
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(tokens)};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(head_stride) * 2, static_cast<cuuint64_t>(tok_stride) * 2};
+  cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_heads), static_cast<cuuint32_t>(box_tokens)};
+  cuuint32_t es[3] = {1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(p), dims, strides, box, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D>
+cudaError_t launch_prompt(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const PromptArgs& a,
+                          const Schedule& sc, cudaStream_t st) {
+  int dev = 0, sms = 148;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  const cudaError_t e =
+      cudaFuncSetAttribute(k_prompt_tc<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::kBytes);
+  if (e != cudaSuccess) return e;
+  count_launch();
+  k_prompt_tc<D><<<static_cast<int>(sc.n_items < sms ? sc.n_items : sms), kThreads, Smem<D>::kBytes, st>>>(mq, mk, mv,
+                                                                                                         a, sc);
+  return cudaGetLastError();
 }
 
 }  // namespace
@@ -135,7 +666,7 @@ extern "C" int ai_attend_prompt(const void* q_dev, const int64_t* q_strides, con
   if (n_heads <= 0 || n_kv_heads <= 0 || n_heads % n_kv_heads != 0)
     return fail(AI_ERR_ARG, "query heads must be a multiple of the key heads");
   if (n_heads / n_kv_heads > 128) return fail(AI_ERR_ARG, "more than 128 query heads per key head");
-  if (!(scale == scale) || scale - scale != 0.f) return fail(AI_ERR_ARG, "scale must be finite");
+  if (!(scale >= 0.f) || scale - scale != 0.f) return fail(AI_ERR_ARG, "scale must be finite and not negative");
   if ((reinterpret_cast<uintptr_t>(q_dev) | reinterpret_cast<uintptr_t>(k_dev) | reinterpret_cast<uintptr_t>(v_dev) |
        reinterpret_cast<uintptr_t>(out_dev)) % 16 != 0)
     return fail(AI_ERR_ARG, "q, k, v and out must be 16-byte aligned");
@@ -170,12 +701,24 @@ extern "C" int ai_attend_prompt(const void* q_dev, const int64_t* q_strides, con
   a.out = static_cast<uint16_t*>(out_dev);
   a.lse = lse_dev;
   a.status = status_dev;
-  if (n_seqs > 65535) return fail(AI_ERR_ARG, "more than 65535 sequences");
-  const dim3 grid(static_cast<unsigned>(total_q < 4096 ? total_q : 4096), n_seqs);
+  Schedule sc;
+  sc.tpt = kTile / a.G;
+  sc.qb = 2 * sc.tpt;
+  const int64_t slots = static_cast<int64_t>(total_q) / sc.qb + n_seqs;
+  if (slots > 0x7fffffff) return fail(AI_ERR_ARG, "too many query blocks");
+  sc.n_slots = static_cast<int>(slots);
+  sc.n_items = slots * n_kv_heads;
+  CUtensorMap mq, mk, mv;
+  // without keys nothing is loaded, but a map needs a row
+  const bool none = total_k == 0;
+  if (!map_rows(&mq, q_dev, total_q, n_heads, head_dim, a.q_tok, a.q_head, a.G, sc.tpt) ||
+      !map_rows(&mk, none ? q_dev : k_dev, none ? 1 : total_k, n_kv_heads, head_dim, a.k_tok, none ? head_dim : a.k_head,
+                1, kTile) ||
+      !map_rows(&mv, none ? q_dev : v_dev, none ? 1 : total_k, n_kv_heads, head_dim, a.v_tok, none ? head_dim : a.v_head,
+                1, kTile))
+    return fail(AI_ERR_CUDA, "tensor map encoding failed");
   cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
-  count_launch();
-  if (head_dim == 64) k_prompt_rows<64><<<grid, 256, 0, st>>>(a);
-  else k_prompt_rows<128><<<grid, 256, 0, st>>>(a);
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e =
+      head_dim == 64 ? launch_prompt<64>(mq, mk, mv, a, sc, st) : launch_prompt<128>(mq, mk, mv, a, sc, st);
   return e == cudaSuccess ? AI_OK : fail(AI_ERR_CUDA, cudaGetErrorString(e));
 }

@@ -788,7 +788,7 @@ int run_rows(const ai_cache* c, int32_t layer, const void* q, int32_t R, int32_t
   if (R < 0 || Hq <= 0 || Hq % c->n_kv_heads != 0) return fail(AI_ERR_ARG, "query heads must be a multiple of the key heads");
   if (R > 0 && !seqs && c->n_seqs != R && !(ids && c->n_seqs == 1))
     return fail(AI_ERR_ARG, "without seqs the table needs one row per query row");
-  if (!(scale == scale) || scale - scale != 0.f) return fail(AI_ERR_ARG, "scale must be finite");
+  if (!(scale >= 0.f) || scale - scale != 0.f) return fail(AI_ERR_ARG, "scale must be finite and not negative");
   if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(out) | reinterpret_cast<uintptr_t>(ws)) % 16 != 0)
     return fail(AI_ERR_ARG, "q, out and the workspace must be 16-byte aligned");
   if (ws_bytes < workspace_for(Hq, c->n_kv_heads, c->head_dim)) return fail(AI_ERR_ARG, "workspace too small");

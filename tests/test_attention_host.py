@@ -52,6 +52,7 @@ def test_bad_caches_are_refused(change, match):
     (dict(layer=2), "layer"), (dict(layer=-1), "layer"), (dict(q=None), "null"), (dict(out=None), "null"),
     (dict(ws=None), "null"), (dict(ws_bytes=100), "workspace"), (dict(heads=3), "multiple"), (dict(heads=0), "multiple"),
     (dict(rows=2), "seqs"), (dict(scale=float("nan")), "finite"), (dict(scale=float("inf")), "finite"),
+    (dict(scale=-0.5), "negative"),
     (dict(q=P + 2), "aligned"), (dict(out=P + 8), "aligned"), (dict(rows=-1, seqs=P), "multiple"),
     (dict(rows=1 << 30, seqs=P), "too many"),
 ])
@@ -77,7 +78,7 @@ def test_selected_needs_ids_and_head_dims_that_the_kernels_have():
 @pytest.mark.parametrize("args,match", [
     (dict(q=None), "null"), (dict(k=None), "null"), (dict(v=None), "null"), (dict(out=None), "null"),
     (dict(cu_q=None), "null"), (dict(n_seqs=-1), "negative"), (dict(total_q=-1), "negative"), (dict(D=96), "head_dim"),
-    (dict(Hq=5), "multiple"), (dict(Hq=258), "128 query heads"), (dict(scale=float("inf")), "finite"),
+    (dict(Hq=5), "multiple"), (dict(Hq=258), "128 query heads"), (dict(scale=float("inf")), "finite"), (dict(scale=-0.5), "negative"),
     (dict(q=P + 8), "aligned"), (dict(qs=(257, 128)), "strides"), (dict(ks=(256, 4)), "strides"),
     (dict(vs=(-256, 128)), "strides"), (dict(ks=(0, 128)), "strides"), (dict(qs=(1024, 0)), "strides"),
 ])
