@@ -9,18 +9,29 @@
 // (base-2 exponents: scale * log2 e is one factor).  The G = Hq / Hkv query
 // heads that share a key head are the rows of one matrix product, so every
 // key and value is read once per group.  What bounds it is reading the keys
-// and values; the products are mma.sync m16n8k16 (at G <= 64 rows a 128-row
-// tcgen05 tile would be half empty or worse, and its operands would have to
-// be converted and rearranged by extra warps: the fp8 codes are widened in
-// registers here).
+// and values; the products are mma.sync m16n8k16 (G <= 64 rows would leave a
+// 128-row tcgen05 tile half empty or worse, and fp8 codes are widened in
+// registers, between shared memory and the product).
 //
-// Work: tiles of 64 keys.  The CTAs (two per SM) divide all tiles of the
+// Work: tiles of 64 keys.  The CTAs (one per SM) divide all tiles of the
 // batch evenly, whatever the lengths; a row whose tiles lie in several CTAs
 // is joined by a second kernel from per-CTA partial results, always in tile
 // order (no atomics: results do not depend on timing).  With several rows
 // per CTA (prefill) whole rows are dealt out in turn, heads outermost, so
 // that rows running at the same time read the same head's keys (L2), and
 // only the last part wave is divided.
+//
+// In a CTA four warps copy, each sixteen keys of a tile: one lane per key looks
+// up where it lies (ids two tiles ahead, the page one), then the warp copies
+// the rows (cp.async, zeros for what is masked) into a ring of stages.  Eight
+// warps compute: two groups of four take the row's tiles in turn, each warp its
+// share of the tile's keys (or of the heads), with its own maximum, sum and
+// output; they meet once per row.  Every warp follows the division of work by
+// itself, a row at a time: what is done per tile by one warp bounds the tile
+// rate (its instructions wait for one another, about 5 cycles each), so it is
+// kept to about a hundred instructions.  (One warp that looked up all keys and
+// told the others took 1500 cycles a tile; gathering rows by TMA, four an
+// operation from one warp, 6500.)
 #include <cmath>
 
 #include "../../include/ai_index.h"
@@ -31,7 +42,9 @@ namespace aiidx {
 namespace {
 
 constexpr int kTile = 64;
-constexpr int kThreads = 128;
+constexpr int kWarps = 8;                       // that compute
+constexpr int kCopiers = 4;                     // that look up and copy sixteen keys of a tile each
+constexpr int kThreads = (kWarps + kCopiers) * 32;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -49,6 +62,8 @@ struct RowsArgs {
   int R, n_ids, Hq, Hkv, G;
   int n_mb, mb_rows;        // row blocks per key head, query heads per block
   int n_seqs, width, n_pages, page_size;
+  uint64_t page_mul;        // token / page_size = token * page_mul >> page_shift
+  int page_shift;
   float c2;                 // scale * log2 e
   uint16_t* out;            // [R, Hq, D] bf16
   float* lse;               // [R, Hq] or nullptr
@@ -58,12 +73,20 @@ struct RowsArgs {
 };
 
 // ------------------------------------------------------------- warp products
-__device__ __forceinline__ void mma_bf16(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-      "{%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+template <bool F16>
+__device__ __forceinline__ void mma(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  if constexpr (F16)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ void ldsm4(uint32_t* r, uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -79,18 +102,21 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&b);
 }
-// Two e4m3 codes (low byte first) to two bf16 values, exactly.
-__device__ __forceinline__ uint32_t e4m3x2_to_bf16x2(uint16_t codes) {
-  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(codes, __NV_E4M3);
-  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-  return pack_bf16(f.x, f.y);
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+// Two e4m3 codes (low byte first) to two f16 values, exactly.
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t codes) {
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(codes), __NV_E4M3);
+  return static_cast<uint32_t>(h.x) | (static_cast<uint32_t>(h.y) << 16);
 }
 __device__ __forceinline__ float exp2_approx(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// 16 bytes to shared memory, zeros where !real.
+// 16 or 4 bytes to shared memory, zeros where !real.
 __device__ __forceinline__ void cp16z(uint32_t dst, const void* src, bool real) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(real ? 16 : 0) : "memory");
 }
@@ -99,51 +125,44 @@ __device__ __forceinline__ void cp4z(uint32_t dst, const void* src, bool real) {
 }
 
 // ------------------------------------------------------------ shared memory
-// What the consumer of a tile has to know about it.
-struct TileMeta {
-  int row, head;   // row of q; key head * n_mb + row block
-  int first, last; // of this CTA's share of the row
-  int slot;        // -1: the row lies whole in this CTA; 0 / 1: partial result slot
-  int any;         // some key of the tile is real
-};
-
 template <int D, bool FP8, int MT>
 struct Layout {
   static constexpr int kRow = FP8 ? D : 2 * D;          // bytes of a key row
-  static constexpr int kChunks = kRow / 16;
+  static constexpr int kLine = kRow < 128 ? kRow : 128; // bytes of it that lie together
   static constexpr int kKV = kTile * kRow;              // bytes of a K or V tile
   static constexpr int kQRow = 2 * D + 16;              // padded: rows fall on different banks
   static constexpr int kQ = 16 * MT * kQRow;
   static constexpr int kScales = FP8 ? 2 * kTile * 4 : 0;
-  static constexpr int kStage = 2 * kKV + kQ + kScales;
-  static constexpr int kWK = 4 / MT;                    // warps along the keys
-  static constexpr int kMerge = (kWK - 1) * 16 * MT * (D + 2) * 4;
-  static constexpr int kStages = FP8 ? (MT == 1 ? 4 : 3) : 2;
-  static constexpr int kRing = kStages + 1;
-  static constexpr int kBytes =
-      kStages * kStage + kMerge + kRing * (kTile * 4 + static_cast<int>(sizeof(TileMeta)));
-  // 16-byte chunk c of tile row r is stored at chunk c ^ swz(r), so that the
-  // eight rows of an ldmatrix, and (fp8) the two rows of a quarter warp's
-  // 16-byte loads, fall on different banks
-  __device__ static int swz(int r) {
-    if constexpr (!FP8) return r & 7;
-    if constexpr (kChunks == 8) return ((r & 1) << 2) | ((r >> 1) & 3);
-    return (r >> 1) & 3;
+  static constexpr int kWK = 4 / MT;                    // warps of a group along the keys
+  static constexpr int kParts = 2 * kWK;                // states that meet per head row
+  static constexpr int kMerge = (kParts - 1) * 16 * MT * (D + 2) * 4;
+  static constexpr int kStages = 131072 / (2 * kKV);    // 128 KB of keys and values
+  static constexpr int kBars = 2 * kStages + 6;
+  static constexpr int kBytes = 1024 + kStages * (2 * kKV + kScales + 8) + 2 * kQ + kMerge + kBars * 8 + 16;
+  static_assert(kBytes <= 227 * 1024 - 256, "shared memory");
+  // 16-byte chunk c of tile row r: the eight rows of an ldmatrix fall on
+  // different banks
+  __device__ static uint32_t at(int r, int c) {
+    if constexpr (kLine == 128) return (c >> 3) * (kTile * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+    return r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
+  }
+  // Tile row of column i of an 8-key product: for fp8 rows of 128 bytes such
+  // that the rows of a quarter warp's 16-byte loads fall on different banks
+  __device__ static constexpr int key(int i) {
+    if constexpr (FP8 && kLine == 128) return ((i & 1) << 2) | (i >> 1);
+    return i;
   }
 };
 
-// ----------------------------------------------------------- division of work
-// Item: one row and one (key head, row block).  Tiles of an item are
-// consecutive; CTA c takes the whole items it, it + grid, .. < n_whole and
-// then the tiles [b0, b1) of the items from n_whole on.
-struct Walk {
-  int it;             // whole items: the current one
-  int n_whole, grid;
-  int64_t b, b1;      // divided tiles: current, end
-  int row, head, tile, n_tiles;  // current position
-  bool divided;
-};
+__device__ int g_no_status;  // where flags go when the caller gives no status word
 
+// ----------------------------------------------------------- division of work
+// Division of a token (< 2^31) by the page size: with s = ceil(log2 d),
+// m = ceil(2^(31 + s) / d) < 2^32 the quotient is exactly n m >> (31 + s)
+// (Granlund and Montgomery, 1994).
+__device__ __forceinline__ int page_of(const RowsArgs& a, int tok) {
+  return static_cast<int>(static_cast<uint64_t>(static_cast<uint32_t>(tok)) * a.page_mul >> a.page_shift);
+}
 __device__ __forceinline__ int seq_of(const RowsArgs& a, int row) {
   return a.seqs ? a.seqs[row] : row * a.seq_mul;
 }
@@ -158,6 +177,63 @@ __device__ __forceinline__ int len_of(const RowsArgs& a, int row) {
 __device__ __forceinline__ int tiles_of(const RowsArgs& a, int row) {
   return ((a.ids ? a.n_ids : len_of(a, row)) + kTile - 1) / kTile;
 }
+
+// A share of one item: tiles [t0, t1) of a row and a (key head, row block).
+struct Share {
+  int row, head, t0, t1;
+  int slot;     // -1: the whole item; 0 / 1: partial result slot
+  bool ends;    // the item's last tile is in it
+};
+
+// The shares of a CTA in order: whole items dealt out in turn (item it, it +
+// grid, .. < n_whole; heads outermost), then the tiles [b, b1) of the divided
+// items, which follow one another.  Every warp runs its own.
+struct Walk {
+  int it, n_whole, grid;
+  int64_t b, b1;
+  bool by_head;        // heads outermost (selected), else rows (cached)
+  int row, head;       // of the next divided item
+  int tile, n_tiles;   // its next tile, and its tiles
+  int nt_ids, n_heads;
+
+  __device__ bool next(const RowsArgs& a, Share* s) {
+    if (it < n_whole) {
+      s->head = it / a.R;
+      s->row = it - s->head * a.R;
+      s->t0 = 0;
+      s->t1 = nt_ids;
+      s->slot = -1;
+      s->ends = true;
+      it += grid;
+      return true;
+    }
+    if (b >= b1) return false;
+    const int64_t left = b1 - b;
+    s->row = row;
+    s->head = head;
+    s->t0 = tile;
+    s->ends = left >= n_tiles - tile;
+    s->t1 = s->ends ? n_tiles : tile + static_cast<int>(left);
+    // begun in an earlier CTA: its first slot; goes on in a later one: its second
+    s->slot = tile > 0 ? 0 : (s->ends ? -1 : 1);
+    b += s->t1 - tile;
+    tile = 0;
+    if (by_head) {
+      if (++row == a.R) {
+        row = 0;
+        ++head;
+      }
+    } else if (++head == n_heads) {
+      head = 0;
+      if (b < b1) {
+        do ++row;
+        while (row < a.R && tiles_of(a, row) == 0);
+        n_tiles = row < a.R ? tiles_of(a, row) : 1;
+      }
+    }
+    return true;
+  }
+};
 
 // Block-wide sum and exclusive prefix of one int64 per thread.
 __device__ int64_t block_scan(int64_t x, int64_t* total, int64_t* warp_sums) {
@@ -180,47 +256,73 @@ __device__ int64_t block_scan(int64_t x, int64_t* total, int64_t* warp_sums) {
 }
 
 template <int D, bool FP8, int MT>
-__global__ void __launch_bounds__(kThreads, 2) k_attend_rows(const RowsArgs a) {
+__global__ void __launch_bounds__(kThreads, 1)
+    k_attend_rows(const RowsArgs a) {
   using L = Layout<D, FP8, MT>;
   constexpr int S = L::kStages;
   constexpr int WK = L::kWK;
   constexpr int NK = kTile / WK;   // keys of a tile per warp
-  extern __shared__ __align__(128) uint8_t smem[];
-  uint8_t* merge = smem + S * L::kStage;
-  int32_t* ring_row = reinterpret_cast<int32_t*>(merge + L::kMerge);
-  TileMeta* ring_meta = reinterpret_cast<TileMeta*>(ring_row + L::kRing * kTile);
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* stages = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sq = stages + S * 2 * L::kKV;                        // [2] queries
+  float* merge = reinterpret_cast<float*>(sq + 2 * L::kQ);
+  float* scales = merge + L::kMerge / 4;                        // [S][2][64]
+  uint64_t* reals = reinterpret_cast<uint64_t*>(scales + S * L::kScales / 4);  // [S] bit i: key i of the tile is there
+  uint64_t* full = reals + S;                                   // [S] tile landed
+  uint64_t* empty = full + S;                                   // [S] tile read
+  uint64_t* q_full = empty + S;                                 // [2] queries landed
+  uint64_t* q_empty = q_full + 2;                               // [2] queries read
+  uint64_t* joined = q_empty + 2;                               // [2] states written / read
+  int* abort = reinterpret_cast<int*>(joined + 2);
   __shared__ int64_t sh_scan[kThreads / 32];
   __shared__ int64_t sh_b0;
-  __shared__ int sh_row;
+  __shared__ int sh_row, sh_n_none;
+  __shared__ int sh_none[kThreads];
+  int* err = a.status ? a.status : &g_no_status;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int g = lane >> 2, t = lane & 3;
-  const int wm = warp % MT, wk = warp / MT;
   const int n_heads = a.Hkv * a.n_mb;
   const int grid = gridDim.x, cta = blockIdx.x;
+
+  if (tid == 0) {
+    for (int i = 0; i < S; ++i) {
+      mbar_init(&full[i], kCopiers * 33);   // each lane's copies, each warp's bits
+      mbar_init(&empty[i], kWarps);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&q_full[i], kCopiers * 32);
+      mbar_init(&q_empty[i], kWarps);
+    }
+    mbar_init(&joined[0], kWarps - MT);
+    mbar_init(&joined[1], MT);
+    *abort = 0;
+    sh_n_none = 0;
+    fence_mbar_init();
+  }
 
   // ---------------------------------------------------- this CTA's share
   Walk w;
   w.grid = grid;
   w.it = cta;
   w.n_whole = 0;
-  int start_tile = 0;     // first divided tile within its row's tiles of all heads
+  w.by_head = a.ids != nullptr;
+  w.nt_ids = (a.n_ids + kTile - 1) / kTile;
+  w.n_heads = n_heads;
   int64_t total;
   if (a.ids) {
     const int64_t items = static_cast<int64_t>(a.R) * n_heads;
-    const int nt = (a.n_ids + kTile - 1) / kTile;
     w.n_whole = static_cast<int>(items / grid) * grid;
-    total = (items - w.n_whole) * nt;
+    total = (items - w.n_whole) * w.nt_ids;
     w.b = total * cta / grid;
     w.b1 = total * (cta + 1) / grid;
   } else {
-    // two passes over the lengths: the number of tiles, and the row where
-    // this CTA's share begins
-    total = 0;
-    for (int r0 = 0; r0 < a.R; r0 += kThreads) {
+    // the number of tiles, then the row where this CTA's share begins (a
+    // second pass over the lengths where there are more rows than threads)
+    int64_t mine = tid < a.R ? tiles_of(a, tid) : 0, before;
+    before = block_scan(mine, &total, sh_scan);
+    for (int r0 = kThreads; r0 < a.R; r0 += kThreads) {
       int64_t sum;
-      const int r = r0 + tid;
-      block_scan(r < a.R ? tiles_of(a, r) : 0, &sum, sh_scan);
+      block_scan(r0 + tid < a.R ? tiles_of(a, r0 + tid) : 0, &sum, sh_scan);
       total += sum;
     }
     total *= n_heads;
@@ -228,397 +330,427 @@ __global__ void __launch_bounds__(kThreads, 2) k_attend_rows(const RowsArgs a) {
     w.b1 = total * (cta + 1) / grid;
     int64_t seen = 0;
     for (int r0 = 0; r0 < a.R; r0 += kThreads) {
-      int64_t sum;
+      int64_t sum = 0;
       const int r = r0 + tid;
-      const int64_t n = r < a.R ? static_cast<int64_t>(tiles_of(a, r)) * n_heads : 0;
-      const int64_t p = seen + block_scan(n, &sum, sh_scan);
+      if (r0 > 0) {
+        mine = r < a.R ? tiles_of(a, r) : 0;
+        before = block_scan(mine, &sum, sh_scan);
+      } else if (a.R > kThreads) {
+        block_scan(mine, &sum, sh_scan);
+      }
+      const int64_t n = mine * n_heads, p = seen + before * n_heads;
       if (n > 0 && p <= w.b && w.b < p + n) {
         sh_row = r;
         sh_b0 = p;
       }
-      seen += sum;
+      seen += sum * n_heads;
       // rows that see nothing: zeros, and the log of an empty sum
-      for (int rr = r0; rr < r0 + kThreads && rr < a.R; ++rr) {
-        if (rr % grid != cta || tiles_of(a, rr) > 0) continue;
-        for (int i = tid; i < a.Hq * D / 2; i += kThreads)
-          reinterpret_cast<uint32_t*>(a.out)[static_cast<int64_t>(rr) * a.Hq * D / 2 + i] = 0;
+      if (r < a.R && mine == 0 && r % grid == cta) {
+        sh_none[atomicAdd(&sh_n_none, 1)] = r;
+        const int s = seq_of(a, r);
+        if (s < 0 || s >= a.n_seqs) atomicOr(err, AI_DEVFLAG_RANGE);
+      }
+      __syncthreads();
+      for (int i = 0; i < sh_n_none; ++i) {
+        const int64_t at = static_cast<int64_t>(sh_none[i]) * a.Hq;
+        for (int j = tid; j < a.Hq * D / 8; j += kThreads)
+          reinterpret_cast<uint4*>(a.out + at * D)[j] = make_uint4(0, 0, 0, 0);
         if (a.lse)
-          for (int i = tid; i < a.Hq; i += kThreads) a.lse[static_cast<int64_t>(rr) * a.Hq + i] = -INFINITY;
-        if (a.status && tid == 0) {
-          const int s = seq_of(a, rr);
-          if (s < 0 || s >= a.n_seqs) atomicOr(a.status, AI_DEVFLAG_RANGE);
-        }
+          for (int j = tid; j < a.Hq; j += kThreads) a.lse[at + j] = -INFINITY;
       }
+      __syncthreads();
+      if (tid == 0) sh_n_none = 0;
     }
-    __syncthreads();
-    if (w.b < w.b1) {
-      w.row = sh_row;
-      start_tile = static_cast<int>(w.b - sh_b0);
-    }
-  }
-  // position the walk on its first tile
-  w.divided = w.it >= w.n_whole;
-  auto locate_item = [&](int64_t item) {   // selected: heads outermost
-    w.head = static_cast<int>(item / a.R);
-    w.row = static_cast<int>(item % a.R);
-  };
-  auto enter_divided = [&]() {
-    w.divided = true;
-    if (a.ids) {
-      w.n_tiles = (a.n_ids + kTile - 1) / kTile;
-      locate_item(w.n_whole + w.b / w.n_tiles);
-      w.tile = static_cast<int>(w.b % w.n_tiles);
-    } else if (w.b < w.b1) {
-      w.n_tiles = tiles_of(a, w.row);
-      w.head = start_tile / w.n_tiles;
-      w.tile = start_tile % w.n_tiles;
-    }
-  };
-  if (w.divided) {
-    enter_divided();
-  } else {
-    locate_item(w.it);
-    w.n_tiles = (a.n_ids + kTile - 1) / kTile;
-    w.tile = 0;
-  }
-  const int64_t n_mine =
-      (w.n_whole > 0 ? static_cast<int64_t>(w.n_whole / grid) * ((a.n_ids + kTile - 1) / kTile) : 0) + (w.b1 - w.b);
-  const int64_t b_begin = w.b;
-
-  // what the joining kernel reads: the item that began before this CTA, or
-  // -1 (0), whether it ends here (1), and the item that begins here and goes
-  // on in the next CTA that has a share, or -1 (2)
-  if (tid == 0) {
-    a.meta[cta * 4 + 0] = -1;
-    a.meta[cta * 4 + 1] = 1;
-    a.meta[cta * 4 + 2] = -1;
-    a.meta[cta * 4 + 3] = -1;
-  }
-  // the slot of the current item's share, -1 where the item lies whole here
-  auto slot_of = [&]() {
-    if (!w.divided) return -1;
-    const int64_t i0 = w.b - w.tile, i1 = i0 + w.n_tiles;
-    if (i0 < b_begin) return i1 > w.b1 ? 2 : 0;   // 2: began before and goes on
-    return i1 > w.b1 ? 1 : -1;
-  };
-  auto advance = [&]() {
-    ++w.tile;
-    if (w.divided) ++w.b;
-    if (w.tile < w.n_tiles) return;
-    w.tile = 0;
-    if (!w.divided) {
-      w.it += grid;
-      if (w.it >= w.n_whole) enter_divided();
-      else locate_item(w.it);
-    } else if (a.ids) {
-      if (++w.row == a.R) {
-        w.row = 0;
-        ++w.head;
-      }
-    } else if (++w.head == n_heads) {
-      w.head = 0;
-      if (w.b < w.b1) {
-        do ++w.row;
-        while (w.row < a.R && tiles_of(a, w.row) == 0);
-        w.n_tiles = w.row < a.R ? tiles_of(a, w.row) : 1;
-      }
-    }
-  };
-
-  // ------------------------------------------------- plan, two steps ahead
-  // Threads 0..63 follow the walk; thread i looks up key i of a tile.
-  int plan_tok = -1;               // token of the tile planned next
-  TileMeta plan_meta{};
-  int plan_seq = 0;
-  auto plan_token = [&](int64_t n) {  // step 1: the token
-    plan_tok = -1;
-    if (n >= n_mine) return;
-    const int s = seq_of(a, w.row);
-    const int len = len_of(a, w.row);
-    const int at = w.tile * kTile + tid;
-    int tok = -1;
-    if (a.ids) {
-      if (at < a.n_ids) {
-        tok = a.ids[static_cast<int64_t>(w.row) * a.n_ids + at];
-        if (tok >= len) {
-          if (a.status) atomicOr(a.status, AI_DEVFLAG_RANGE);
-          tok = -1;
-        }
-      }
-    } else if (at < len) {
-      tok = at;
-    }
-    plan_tok = tok < 0 ? -1 : tok;
-    plan_seq = s;
-    plan_meta.row = w.row;
-    plan_meta.head = w.head;
-    int slot = slot_of();
-    plan_meta.first = w.tile == 0 || (w.divided && w.b == b_begin);
-    plan_meta.last = w.tile == w.n_tiles - 1 || (w.divided && w.b == w.b1 - 1);
-    if (tid == 0 && plan_meta.first && slot >= 0) {
-      const int item = w.row * n_heads + w.head;
-      if (slot == 1) a.meta[cta * 4 + 2] = item;
-      else {
-        a.meta[cta * 4 + 0] = item;
-        a.meta[cta * 4 + 1] = slot == 0;
-      }
-    }
-    plan_meta.slot = slot == 2 ? 0 : slot;
-    advance();
-  };
-  int plan_row = -1;
-  auto plan_lookup = [&]() {          // step 2: its page
-    plan_row = -1;
-    if (plan_tok >= 0) {
-      const int page = a.tables[static_cast<int64_t>(plan_seq) * a.width + plan_tok / a.page_size];
-      if (page >= 0 && page < a.n_pages) plan_row = page * a.page_size + plan_tok % a.page_size;
-      else if (a.status) atomicOr(a.status, AI_DEVFLAG_RANGE);
-    }
-  };
-  auto plan_store = [&](int64_t n, int row, TileMeta m) {
-    const int e = static_cast<int>(n % L::kRing);
-    ring_row[e * kTile + tid] = row;
-    if (tid == 0) {
-      m.any = 0;
-      ring_meta[e] = m;
-    }
-  };
-
-  auto issue = [&](int64_t n) {
-    if (n < n_mine) {
-      const int e = static_cast<int>(n % L::kRing);
-      const TileMeta m = ring_meta[e];
-      const uint32_t st = smem_u32(smem + (n % S) * L::kStage);
-      const int h = m.head / a.n_mb;
-      const int64_t row_bytes = static_cast<int64_t>(a.Hkv) * L::kRow;
-      const int c = tid % L::kChunks;
-      for (int r = tid / L::kChunks; r < kTile; r += kThreads / L::kChunks) {
-        const int row = ring_row[e * kTile + r];
-        const int64_t off = row < 0 ? 0 : row * row_bytes + h * L::kRow + c * 16;
-        const uint32_t dst = st + r * L::kRow + ((c ^ L::swz(r)) << 4);
-        cp16z(dst, a.k + off, row >= 0);
-        cp16z(dst + L::kKV, a.v + off, row >= 0);
-      }
-      if constexpr (FP8) {
-        const int r = tid & 63;
-        const int row = ring_row[e * kTile + r];
-        const float* src = tid < 64 ? a.ks : a.vs;
-        const int64_t off = row < 0 ? 0 : static_cast<int64_t>(row) * a.Hkv + h;
-        cp4z(st + 2 * L::kKV + L::kQ + tid * 4, src + off, row >= 0);
-      }
-      if (m.first) {
-        const int h0 = h * a.G + (m.head % a.n_mb) * a.mb_rows;
-        const int n_rows = min(a.mb_rows, (h + 1) * a.G - h0);
-        for (int i = tid; i < 16 * MT * (D / 8); i += kThreads) {
-          const int r = i / (D / 8), cc = i % (D / 8);
-          const bool real = r < n_rows;
-          const uint16_t* src = a.q + (static_cast<int64_t>(m.row) * a.Hq + h0 + (real ? r : 0)) * D + cc * 8;
-          cp16z(st + 2 * L::kKV + r * L::kQRow + cc * 16, src, real);
-        }
-      }
-    }
-    cp_async_commit();
-  };
-
-  // -------------------------------------------------------------- prologue
-  if (warp < 2) {
-    for (int n = 0; n < S; ++n) {
-      plan_token(n);
-      plan_lookup();
-      plan_store(n, plan_row, plan_meta);
-    }
-    plan_token(S);
   }
   __syncthreads();
-  for (int n = 0; n < S - 1; ++n) issue(n);
-
-  uint32_t qf[D / 16][4];
-  float o[D / 8][4];
-  float m_run[2], l_run[2];
-
-  // ------------------------------------------------------------- main loop
-  for (int64_t n = 0; n < n_mine; ++n) {
-    cp_async_wait<S - 2>();
-    __syncthreads();
-    issue(n + S - 1);
-    TileMeta next_meta;
-    if (warp < 2) {
-      plan_lookup();                 // tile n + S
-      next_meta = plan_meta;
+  if (w.b < w.b1) {
+    if (a.ids) {
+      const int64_t item = w.n_whole + w.b / w.nt_ids;
+      w.head = static_cast<int>(item / a.R);
+      w.row = static_cast<int>(item % a.R);
+      w.tile = static_cast<int>(w.b % w.nt_ids);
+      w.n_tiles = w.nt_ids;
+    } else {
+      const int start = static_cast<int>(w.b - sh_b0);   // within the row's tiles of all heads
+      w.row = sh_row;
+      w.n_tiles = tiles_of(a, w.row);
+      w.head = start / w.n_tiles;
+      w.tile = start % w.n_tiles;
     }
-    const int next_row = plan_row;
-    if (warp < 2) plan_token(n + S + 1);
+  }
+  Share x;
 
-    const int e = static_cast<int>(n % L::kRing);
-    const TileMeta m = ring_meta[e];
-    const uint8_t* stage = smem + (n % S) * L::kStage;
-    const uint32_t sk = smem_u32(stage);
-    const uint32_t sv = sk + L::kKV;
-    if (m.first) {
-      const uint8_t* sq = stage + 2 * L::kKV + wm * 16 * L::kQRow;
-#pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) {
-        if constexpr (!FP8) {
-          ldsm4(qf[kk], smem_u32(sq) + (lane & 15) * L::kQRow + kk * 32 + (lane >> 4) * 16);
+  if (warp >= kWarps) {
+    // ============================================================== copies
+    const int cw = warp - kWarps;
+    constexpr int kChunks = L::kRow / 16;            // 16-byte chunks of a key row
+    constexpr int kStep = 32 / kChunks;              // rows that the warp copies at a time
+    const int chunk = lane % kChunks, r_lane = lane / kChunks;
+    const int64_t row_bytes = static_cast<int64_t>(a.Hkv) * L::kRow;
+    // what the joining kernel reads: the item that began before this CTA, or
+    // -1 (0), whether it ends here (1), and the item that begins here and goes
+    // on in the next CTA that has a share, or -1 (2)
+    if (cw == 0 && lane == 0) *reinterpret_cast<int4*>(a.meta + cta * 4) = make_int4(-1, 1, -1, -1);
+    __syncwarp();
+    uint32_t n = 0, n_shares = 0;
+    bool ok = true;
+    while (ok && w.next(a, &x)) {
+      const int seq = seq_of(a, x.row), len = len_of(a, x.row);
+      const int kv_head = a.n_mb == 1 ? x.head : x.head / a.n_mb;
+      if (cw == 0 && lane == 0 && x.slot >= 0) {
+        const int item = x.row * n_heads + x.head;
+        if (x.slot == 1) {
+          a.meta[cta * 4 + 2] = item;
         } else {
-          // the product's sum over d in the order of the codes' 16-byte loads
-          const int d = (kk / 4) * 64 + t * 16 + (kk % 4) * 4;
-          const uint2 x = *reinterpret_cast<const uint2*>(sq + g * L::kQRow + d * 2);
-          const uint2 y = *reinterpret_cast<const uint2*>(sq + (g + 8) * L::kQRow + d * 2);
-          qf[kk][0] = x.x;
-          qf[kk][1] = y.x;
-          qf[kk][2] = x.y;
-          qf[kk][3] = y.y;
+          a.meta[cta * 4 + 0] = item;
+          a.meta[cta * 4 + 1] = x.ends;
         }
       }
+      // the queries
+      const uint32_t qs = n_shares & 1;
+      if (n_shares >= 2 && !__all_sync(0xffffffffu, mbar_wait(&q_empty[qs], (n_shares / 2 - 1) & 1, err, abort))) break;
+      {
+        const int h0 = kv_head * a.G + (x.head - kv_head * a.n_mb) * a.mb_rows;
+        const int n_rows = min(a.mb_rows, (kv_head + 1) * a.G - h0);
+        const uint32_t dst = smem_u32(sq + qs * L::kQ);
+        const uint16_t* src = a.q + (static_cast<int64_t>(x.row) * a.Hq + h0) * D;
+        for (int i = cw * 32 + lane; i < 16 * MT * (D / 8); i += kCopiers * 32) {
+          const int r = i / (D / 8), c = i % (D / 8);
+          cp16z(dst + r * L::kQRow + c * 16, src + (r < n_rows ? r * D : 0) + c * 8, r < n_rows);
+        }
+        cp_async_mbar_arrive_noinc(&q_full[qs]);
+      }
+      ++n_shares;
+      // lane l (and l + 16) looks up key l of this warp's sixteen of a tile:
+      // its token, then its page, then its row in the pool (-1: none)
+      const int32_t* table = a.tables + static_cast<int64_t>(seq) * a.width;
+      const int32_t* ids = a.ids ? a.ids + static_cast<int64_t>(x.row) * a.n_ids : nullptr;
+      const int key = cw * 16 + (lane & 15);
+      auto token = [&](int t) {
+        const int at = t * kTile + key;
+        if (!ids) return t < x.t1 && at < len ? at : -1;
+        return t < x.t1 && at < a.n_ids ? ids[at] : -1;
+      };
+      auto page = [&](int* tok) {
+        if (*tok >= len) {
+          atomicOr(err, AI_DEVFLAG_RANGE);
+          *tok = -1;
+        }
+        return *tok >= 0 ? table[page_of(a, *tok)] : -1;
+      };
+      int tok = token(x.t0), tok1 = token(x.t0 + 1);
+      int pg = page(&tok);
+      const uint8_t* kb = a.k + kv_head * L::kRow + chunk * 16;
+      const uint8_t* vb = a.v + kv_head * L::kRow + chunk * 16;
+      for (int t = x.t0; t < x.t1; ++t, ++n) {
+        const int tok2 = token(t + 2);
+        const int pg1 = page(&tok1);
+        int row = -1;
+        if (tok >= 0) {
+          if (pg >= 0 && pg < a.n_pages) row = pg * a.page_size + (tok - page_of(a, tok) * a.page_size);
+          else atomicOr(err, AI_DEVFLAG_RANGE);
+        }
+        tok = tok1;
+        tok1 = tok2;
+        pg = pg1;
+        const uint32_t st = n % S;
+        if (n >= S && !__all_sync(0xffffffffu, mbar_wait(&empty[st], (n / S - 1) & 1, err, abort))) {
+          ok = false;
+          break;
+        }
+        const uint32_t real = __ballot_sync(0xffffffffu, row >= 0) & 0xffffu;
+        if (lane == 0) reinterpret_cast<uint16_t*>(reals + st)[cw] = static_cast<uint16_t>(real);
+        // (a computing warp that takes keys of several copying warps needs the
+        // zeros of those that have none)
+        if (real || NK > 16) {
+          const uint32_t dst = smem_u32(stages + st * 2 * L::kKV);
 #pragma unroll
-      for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-      m_run[0] = m_run[1] = -INFINITY;
-      l_run[0] = l_run[1] = 0.f;
+          for (int i = 0; i < 16; i += kStep) {
+            const int r = i + r_lane;
+            const int src = __shfl_sync(0xffffffffu, row, r);
+            const int64_t off = src < 0 ? 0 : src * row_bytes;
+            const uint32_t to = dst + L::at(cw * 16 + r, chunk);
+            cp16z(to, kb + off, src >= 0);
+            cp16z(to + L::kKV, vb + off, src >= 0);
+          }
+          if constexpr (FP8) {
+            const int64_t off = row < 0 ? 0 : static_cast<int64_t>(row) * a.Hkv + kv_head;
+            cp4z(smem_u32(scales + st * 2 * kTile + (lane >> 4) * kTile + key), (lane < 16 ? a.ks : a.vs) + off,
+                 row >= 0);
+          }
+        }
+        cp_async_mbar_arrive_noinc(&full[st]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&full[st]);
+      }
     }
-    const int32_t* rows = ring_row + e * kTile + wk * NK;
-    bool any = false;
-#pragma unroll
-    for (int i = 0; i < NK; i += 32) any |= (i + lane < NK) && rows[i + lane] >= 0;
-    if (__any_sync(0xffffffffu, any)) {
-      float s[NK / 8][4];
-#pragma unroll
-      for (int j = 0; j < NK / 8; ++j) s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
-      if constexpr (!FP8) {
+    cp_async_wait_all();
+  } else {
+    // ============================================================= compute
+    const int g = lane >> 2, t = lane & 3;
+    const int group = warp >> 2, wm = warp % MT, wk = (warp & 3) / MT;
+    const int part = group * WK + wk;              // which of the states of its head rows
+    uint32_t qf[D / 16][4];
+    float o[D / 8][4];
+    float m_run[2], l_run[2];
+    float c2[2] = {a.c2, a.c2};                    // by row: scale * log2 e (fp8: and the queries' power of two)
+    float e_run = -INFINITY;                       // fp8: log2 of the largest value scale so far
+    bool begun = false;
+    // The maximum moves only when it grows by more than 2^kGrow: the weights
+    // stay in range and most tiles leave o as it is.  fp8: weights are
+    // 2^kLift e^(s - m) * (value scale / largest value scale so far), in f16:
+    // 11 bits down to 2^-25 of the largest, and at most 2^15.
+    constexpr float kGrow = FP8 ? 4.f : 8.f, kLift = 11.f;
+
+    uint32_t n = 0, n_shares = 0;
+    bool ok = true;
+    while (ok && w.next(a, &x)) {
+      const uint32_t qs = n_shares & 1;
+      if (!__all_sync(0xffffffffu, mbar_wait(&q_full[qs], (n_shares / 2) & 1, err, abort))) break;
+      {
+        const uint8_t* q = sq + qs * L::kQ + wm * 16 * L::kQRow;
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
-#pragma unroll
-          for (int j = 0; j < NK / 16; ++j) {
-            uint32_t b[4];
-            const int r = wk * NK + j * 16 + (lane & 7) + ((lane >> 4) << 3);
-            const int c = kk * 2 + ((lane >> 3) & 1);
-            ldsm4(b, sk + r * L::kRow + ((c ^ L::swz(r)) << 4));
-            mma_bf16(s[2 * j], qf[kk], b[0], b[1]);
-            mma_bf16(s[2 * j + 1], qf[kk], b[2], b[3]);
+          if constexpr (!FP8) {
+            ldsm4(qf[kk], smem_u32(q) + (lane & 15) * L::kQRow + kk * 32 + (lane >> 4) * 16);
+          } else {
+            // the product's sum over d in the order of the codes' 16-byte loads
+            const int d = (kk / 4) * 64 + t * 16 + (kk % 4) * 4;
+            const uint2 x = *reinterpret_cast<const uint2*>(q + g * L::kQRow + d * 2);
+            const uint2 y = *reinterpret_cast<const uint2*>(q + (g + 8) * L::kQRow + d * 2);
+            qf[kk][0] = x.x;
+            qf[kk][1] = y.x;
+            qf[kk][2] = x.y;
+            qf[kk][3] = y.y;
           }
         }
-      } else {
+        if constexpr (FP8) {
+          // the codes are widened to f16, so the queries are f16 too: scaled by
+          // a power of two that brings the row's largest to 2^14 .. 2^15 (exact;
+          // what falls below f16's range is below 2^-39 of the largest)
+          uint32_t mx[2] = {0, 0};
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t x = qf[kk][i] & 0x7fff7fffu;
+              mx[i & 1] = max(mx[i & 1], max(x & 0xffffu, x >> 16));
+            }
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            mx[i] = max(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 1));
+            mx[i] = max(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 2));
+            const int e = static_cast<int>(mx[i] >> 7);           // biased exponent
+            const int up = e == 0 || e == 255 ? 0 : max(-100, min(100, 127 + 14 - e));
+            const float f = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
+            c2[i] = a.c2 * __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk)
+#pragma unroll
+              for (int j = i; j < 4; j += 2)
+                qf[kk][j] = pack_f16(__uint_as_float(qf[kk][j] << 16) * f, __uint_as_float(qf[kk][j] & 0xffff0000u) * f);
+          }
+          e_run = -INFINITY;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&q_empty[qs]);
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+        m_run[0] = m_run[1] = -INFINITY;
+        l_run[0] = l_run[1] = 0.f;
+        begun = false;
+      }
+      for (int tile = x.t0; tile < x.t1; ++tile, ++n) {
+      const uint32_t st = n % S;
+      if (!__all_sync(0xffffffffu, mbar_wait(&full[st], (n / S) & 1, err, abort))) {
+        ok = false;
+        break;
+      }
+      const uint8_t* stage = stages + st * 2 * L::kKV;
+      const uint32_t sk = smem_u32(stage), sv = sk + L::kKV;
+      // the warp's keys of the tile, one bit each
+      const uint64_t real = reals[st] >> (wk * NK);
+      constexpr uint64_t kAll = NK == 64 ? ~0ull : (1ull << (NK % 64)) - 1;
+      if ((n & 1) == group && (real & kAll)) {
+        float s[NK / 8][4];
+#pragma unroll
+        for (int j = 0; j < NK / 8; ++j) s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
+        if constexpr (!FP8) {
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+#pragma unroll
+            for (int j = 0; j < NK / 16; ++j) {
+              uint32_t b[4];
+              ldsm4(b, sk + L::at(wk * NK + j * 16 + (lane & 7) + ((lane >> 4) << 3), kk * 2 + ((lane >> 3) & 1)));
+              mma<false>(s[2 * j], qf[kk], b[0], b[1]);
+              mma<false>(s[2 * j + 1], qf[kk], b[2], b[3]);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < NK / 8; ++j) {
+#pragma unroll
+            for (int c4 = 0; c4 < D / 64; ++c4) {
+              const uint4 x =
+                  *reinterpret_cast<const uint4*>(stage + L::at(wk * NK + j * 8 + L::key(g), c4 * 4 + t));
+              const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                mma<true>(s[j], qf[c4 * 4 + i], e4m3x2_to_f16x2(u[i] & 0xffff), e4m3x2_to_f16x2(u[i] >> 16));
+            }
+          }
+        }
+        // scale, mask and the running maximum
+        const float* ksc = scales + st * 2 * kTile + wk * NK;
+        float mx[2] = {-INFINITY, -INFINITY};
+        float lv[FP8 ? NK / 4 : 1], e_max = e_run;
 #pragma unroll
         for (int j = 0; j < NK / 8; ++j) {
-          const int r = wk * NK + j * 8 + g;
+          if constexpr (FP8) {
+            const int k0 = j * 8 + L::key(2 * t), k1 = j * 8 + L::key(2 * t + 1);
+            const float f0 = ksc[k0], f1 = ksc[k1];
+            s[j][0] *= c2[0] * f0;
+            s[j][1] *= c2[0] * f1;
+            s[j][2] *= c2[1] * f0;
+            s[j][3] *= c2[1] * f1;
+            lv[2 * j] = __log2f(ksc[kTile + k0]);
+            lv[2 * j + 1] = __log2f(ksc[kTile + k1]);
+            e_max = fmaxf(e_max, fmaxf(lv[2 * j], lv[2 * j + 1]));
+          } else {
 #pragma unroll
-          for (int c4 = 0; c4 < D / 64; ++c4) {
-            const uint4 x = *reinterpret_cast<const uint4*>(stage + r * L::kRow + (((c4 * 4 + t) ^ L::swz(r)) << 4));
-            const uint32_t u[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              mma_bf16(s[j], qf[c4 * 4 + i], e4m3x2_to_bf16x2(static_cast<uint16_t>(u[i] & 0xffff)),
-                       e4m3x2_to_bf16x2(static_cast<uint16_t>(u[i] >> 16)));
+            for (int i = 0; i < 4; ++i) s[j][i] *= a.c2;
           }
         }
-      }
-      // scale, mask and the running maximum
-      const float* ksc = reinterpret_cast<const float*>(stage + 2 * L::kKV + L::kQ) + wk * NK;
-      float mx[2] = {m_run[0], m_run[1]};
+        if ((real & kAll) != kAll) {
 #pragma unroll
-      for (int j = 0; j < NK / 8; ++j) {
-        const int2 rr = *reinterpret_cast<const int2*>(rows + j * 8 + 2 * t);
-        float f0 = a.c2, f1 = a.c2;
-        if constexpr (FP8) {
-          f0 *= ksc[j * 8 + 2 * t];
-          f1 *= ksc[j * 8 + 2 * t + 1];
-        }
-        s[j][0] = rr.x >= 0 ? s[j][0] * f0 : -INFINITY;
-        s[j][1] = rr.y >= 0 ? s[j][1] * f1 : -INFINITY;
-        s[j][2] = rr.x >= 0 ? s[j][2] * f0 : -INFINITY;
-        s[j][3] = rr.y >= 0 ? s[j][3] * f1 : -INFINITY;
-        mx[0] = fmaxf(mx[0], fmaxf(s[j][0], s[j][1]));
-        mx[1] = fmaxf(mx[1], fmaxf(s[j][2], s[j][3]));
-      }
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 1));
-        mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 2));
-      }
-      // a row without a finite score so far: exponents against 0 (all e^-inf = 0)
-      const float mu[2] = {mx[0] == -INFINITY ? 0.f : mx[0], mx[1] == -INFINITY ? 0.f : mx[1]};
-      const float al[2] = {exp2_approx(m_run[0] - mu[0]), exp2_approx(m_run[1] - mu[1])};
-      const bool moved = mx[0] != m_run[0] || mx[1] != m_run[1];
-      m_run[0] = mx[0];
-      m_run[1] = mx[1];
-      if (__any_sync(0xffffffffu, moved)) {
-        l_run[0] *= al[0];
-        l_run[1] *= al[1];
-#pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
-          o[i][0] *= al[0];
-          o[i][1] *= al[0];
-          o[i][2] *= al[1];
-          o[i][3] *= al[1];
-        }
-      }
-      // the weights, rounded once to bf16 for the product with v; their sum
-      // is taken before that rounding
-      uint32_t p[NK / 16][4];
-#pragma unroll
-      for (int j = 0; j < NK / 8; ++j) {
-        const float e0 = exp2_approx(s[j][0] - mu[0]), e1 = exp2_approx(s[j][1] - mu[0]);
-        const float e2 = exp2_approx(s[j][2] - mu[1]), e3 = exp2_approx(s[j][3] - mu[1]);
-        l_run[0] += e0 + e1;
-        l_run[1] += e2 + e3;
-        float f0 = 1.f, f1 = 1.f;
-        if constexpr (FP8) {
-          f0 = ksc[kTile + j * 8 + 2 * t];
-          f1 = ksc[kTile + j * 8 + 2 * t + 1];
-        }
-        p[j / 2][(j & 1) * 2 + 0] = pack_bf16(e0 * f0, e1 * f1);
-        p[j / 2][(j & 1) * 2 + 1] = pack_bf16(e2 * f0, e3 * f1);
-      }
-      if constexpr (!FP8) {
-#pragma unroll
-        for (int j = 0; j < NK / 16; ++j) {
-#pragma unroll
-          for (int dd = 0; dd < D / 16; ++dd) {
-            uint32_t b[4];
-            const int r = wk * NK + j * 16 + (lane & 15);
-            const int c = dd * 2 + (lane >> 4);
-            ldsm4t(b, sv + r * L::kRow + ((c ^ L::swz(r)) << 4));
-            mma_bf16(o[2 * dd], p[j], b[0], b[1]);
-            mma_bf16(o[2 * dd + 1], p[j], b[2], b[3]);
+          for (int j = 0; j < NK / 8; ++j) {
+            const uint32_t bits = static_cast<uint32_t>(real >> (j * 8));
+            const bool r0 = (bits >> L::key(2 * t)) & 1, r1 = (bits >> L::key(2 * t + 1)) & 1;
+            s[j][0] = r0 ? s[j][0] : -INFINITY;
+            s[j][1] = r1 ? s[j][1] : -INFINITY;
+            s[j][2] = r0 ? s[j][2] : -INFINITY;
+            s[j][3] = r1 ? s[j][3] : -INFINITY;
           }
         }
-      } else {
-        // 16-bit transposed loads bring two neighbouring codes of two keys;
-        // accumulator 2 i holds the even, 2 i + 1 the odd d of 16-code chunk i
 #pragma unroll
-        for (int j = 0; j < NK / 16; ++j) {
+        for (int j = 0; j < NK / 8; ++j) {
+          mx[0] = fmaxf(mx[0], fmaxf(s[j][0], s[j][1]));
+          mx[1] = fmaxf(mx[1], fmaxf(s[j][2], s[j][3]));
+        }
 #pragma unroll
-          for (int cc = 0; cc < D / 32; ++cc) {
-            uint32_t b[4];
-            const int r = wk * NK + j * 16 + (lane & 15);
-            const int c = cc * 2 + (lane >> 4);
-            ldsm4t(b, sv + r * L::kRow + ((c ^ L::swz(r)) << 4));
+        for (int i = 0; i < 2; ++i) {
+          mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 1));
+          mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 2));
+        }
+        if constexpr (FP8) {
+          e_max = fmaxf(e_max, __shfl_xor_sync(0xffffffffu, e_max, 1));
+          e_max = fmaxf(e_max, __shfl_xor_sync(0xffffffffu, e_max, 2));
+        }
+        const bool move0 = !begun ? mx[0] > -INFINITY : mx[0] > m_run[0] + kGrow || (m_run[0] == -INFINITY && mx[0] > -INFINITY);
+        const bool move1 = !begun ? mx[1] > -INFINITY : mx[1] > m_run[1] + kGrow || (m_run[1] == -INFINITY && mx[1] > -INFINITY);
+        if (__any_sync(0xffffffffu, move0 || move1) || (FP8 && e_max > e_run)) {
+          const float m0 = move0 ? mx[0] : m_run[0], m1 = move1 ? mx[1] : m_run[1];
+          const float f0 = move0 ? exp2_approx(m_run[0] - m0) : 1.f, f1 = move1 ? exp2_approx(m_run[1] - m1) : 1.f;
+          m_run[0] = m0;
+          m_run[1] = m1;
+          if (begun) {
+            l_run[0] *= f0;
+            l_run[1] *= f1;
+            const float fe = FP8 && e_max > e_run ? exp2_approx(e_run - e_max) : 1.f;
+            const float g0 = f0 * fe, g1 = f1 * fe;
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const uint32_t lo = b[2 * i], hi = b[2 * i + 1];
-              mma_bf16(o[(cc * 2 + i) * 2], p[j],
-                       e4m3x2_to_bf16x2(static_cast<uint16_t>(__byte_perm(lo, 0, 0x4420))),
-                       e4m3x2_to_bf16x2(static_cast<uint16_t>(__byte_perm(hi, 0, 0x4420))));
-              mma_bf16(o[(cc * 2 + i) * 2 + 1], p[j],
-                       e4m3x2_to_bf16x2(static_cast<uint16_t>(__byte_perm(lo, 0, 0x4431))),
-                       e4m3x2_to_bf16x2(static_cast<uint16_t>(__byte_perm(hi, 0, 0x4431))));
+            for (int i = 0; i < D / 8; ++i) {
+              o[i][0] *= g0;
+              o[i][1] *= g0;
+              o[i][2] *= g1;
+              o[i][3] *= g1;
+            }
+          }
+          e_run = e_max;
+        }
+        begun = true;
+        // a row without a finite score so far: exponents against 0 (all e^-inf = 0)
+        const float mu[2] = {m_run[0] == -INFINITY ? 0.f : m_run[0], m_run[1] == -INFINITY ? 0.f : m_run[1]};
+        // the weights, rounded once (bf16; fp8: f16) for the product with v;
+        // their sum is taken before that rounding
+        uint32_t p[NK / 16][4];
+        const float lift = kLift - (e_run == -INFINITY ? 0.f : e_run);
+#pragma unroll
+        for (int j = 0; j < NK / 8; ++j) {
+          const float x0 = s[j][0] - mu[0], x1 = s[j][1] - mu[0], x2 = s[j][2] - mu[1], x3 = s[j][3] - mu[1];
+          const float e0 = exp2_approx(x0), e1 = exp2_approx(x1), e2 = exp2_approx(x2), e3 = exp2_approx(x3);
+          l_run[0] += e0 + e1;
+          l_run[1] += e2 + e3;
+          if constexpr (FP8) {
+            const float v0 = lv[2 * j] + lift, v1 = lv[2 * j + 1] + lift;
+            p[j / 2][(j & 1) * 2 + 0] = pack_f16(exp2_approx(x0 + v0), exp2_approx(x1 + v1));
+            p[j / 2][(j & 1) * 2 + 1] = pack_f16(exp2_approx(x2 + v0), exp2_approx(x3 + v1));
+          } else {
+            p[j / 2][(j & 1) * 2 + 0] = pack_bf16(e0, e1);
+            p[j / 2][(j & 1) * 2 + 1] = pack_bf16(e2, e3);
+          }
+        }
+        // lane i gives the address of row i of an 8 x 8 block, in the keys' order
+        const int vr = wk * NK + (lane & 8) + L::key(lane & 7);
+        if constexpr (!FP8) {
+#pragma unroll
+          for (int j = 0; j < NK / 16; ++j) {
+#pragma unroll
+            for (int dd = 0; dd < D / 16; ++dd) {
+              uint32_t b[4];
+              ldsm4t(b, sv + L::at(vr + j * 16, dd * 2 + (lane >> 4)));
+              mma<false>(o[2 * dd], p[j], b[0], b[1]);
+              mma<false>(o[2 * dd + 1], p[j], b[2], b[3]);
+            }
+          }
+        } else {
+          // 16-bit transposed loads bring two neighbouring codes of two keys;
+          // accumulator 2 i holds the even, 2 i + 1 the odd d of 16-code chunk i
+#pragma unroll
+          for (int j = 0; j < NK / 16; ++j) {
+#pragma unroll
+            for (int cc = 0; cc < D / 32; ++cc) {
+              uint32_t b[4];
+              ldsm4t(b, sv + L::at(vr + j * 16, cc * 2 + (lane >> 4)));
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const uint32_t lo = b[2 * i], hi = b[2 * i + 1];
+                mma<true>(o[(cc * 2 + i) * 2], p[j], e4m3x2_to_f16x2(__byte_perm(lo, 0, 0x4420)),
+                          e4m3x2_to_f16x2(__byte_perm(hi, 0, 0x4420)));
+                mma<true>(o[(cc * 2 + i) * 2 + 1], p[j], e4m3x2_to_f16x2(__byte_perm(lo, 0, 0x4431)),
+                          e4m3x2_to_f16x2(__byte_perm(hi, 0, 0x4431)));
+              }
             }
           }
         }
       }
-    }
-    if (warp < 2) plan_store(n + S, next_row, next_meta);
-
-    if (m.last) {
-      // the row sums over the four lanes of a row, then over the key warps
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        l_run[i] += __shfl_xor_sync(0xffffffffu, l_run[i], 1);
-        l_run[i] += __shfl_xor_sync(0xffffffffu, l_run[i], 2);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[st]);
       }
-      float* mine = reinterpret_cast<float*>(merge) + static_cast<int64_t>((wk - 1) * MT + wm) * 16 * (D + 2);
-      if constexpr (WK > 1) {
-        if (wk > 0) {
+      if (!ok) break;
+      {
+        // the row sums over the four lanes of a row, then over the states
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          l_run[i] += __shfl_xor_sync(0xffffffffu, l_run[i], 1);
+          l_run[i] += __shfl_xor_sync(0xffffffffu, l_run[i], 2);
+        }
+        if constexpr (FP8) {
+          const float f = e_run == -INFINITY ? 0.f : exp2_approx(e_run - kLift);
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i) {
+            o[i][0] *= f;
+            o[i][1] *= f;
+            o[i][2] *= f;
+            o[i][3] *= f;
+          }
+        }
+        float* mine = merge + ((part - 1) * MT + wm) * 16 * (D + 2);
+        if (part > 0) {
+          // the states of the row before have been read
+          if (n_shares > 0 &&
+              !__all_sync(0xffffffffu, mbar_wait(&joined[1], (n_shares - 1) & 1, err, abort)))
+            break;
 #pragma unroll
           for (int i = 0; i < D / 8; ++i) {
             *reinterpret_cast<float2*>(mine + g * (D + 2) + i * 8 + 2 * t) = make_float2(o[i][0], o[i][1]);
@@ -629,10 +761,13 @@ __global__ void __launch_bounds__(kThreads, 2) k_attend_rows(const RowsArgs a) {
             *reinterpret_cast<float2*>(mine + (g + 8) * (D + 2) + D) = make_float2(m_run[1], l_run[1]);
           }
         }
-        __syncthreads();
-        if (wk == 0) {
-          for (int ww = 1; ww < WK; ++ww) {
-            const float* src = reinterpret_cast<const float*>(merge) + static_cast<int64_t>((ww - 1) * MT + wm) * 16 * (D + 2);
+        __syncwarp();
+        if (part > 0) {
+          if (lane == 0) mbar_arrive(&joined[0]);
+        } else {
+          if (!__all_sync(0xffffffffu, mbar_wait(&joined[0], n_shares & 1, err, abort))) break;
+          for (int ww = 1; ww < L::kParts; ++ww) {
+            const float* src = merge + ((ww - 1) * MT + wm) * 16 * (D + 2);
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
               const float* sr = src + (g + half * 8) * (D + 2);
@@ -650,54 +785,53 @@ __global__ void __launch_bounds__(kThreads, 2) k_attend_rows(const RowsArgs a) {
               }
             }
           }
-        }
-      }
-      if (wk == 0) {
-        const int h = m.head / a.n_mb;
-        const int h0 = h * a.G + (m.head % a.n_mb) * a.mb_rows;
-        const int n_rows = min(a.mb_rows, (h + 1) * a.G - h0);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&joined[1]);
+          const int kv_head = a.n_mb == 1 ? x.head : x.head / a.n_mb;
+          const int h0 = kv_head * a.G + (x.head - kv_head * a.n_mb) * a.mb_rows;
+          const int n_rows = min(a.mb_rows, (kv_head + 1) * a.G - h0);
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const int r = wm * 16 + g + half * 8;
-          if (r >= n_rows) continue;
-          // where accumulator pair i of this lane belongs (fp8: even and odd d)
-          if (m.slot < 0) {
-            const float inv = l_run[half] == 0.f ? 0.f : 1.f / l_run[half];
-            uint16_t* dst = a.out + (static_cast<int64_t>(m.row) * a.Hq + h0 + r) * D;
-            if constexpr (!FP8) {
-#pragma unroll
-              for (int i = 0; i < D / 8; ++i)
-                *reinterpret_cast<uint32_t*>(dst + i * 8 + 2 * t) =
-                    pack_bf16(o[i][2 * half] * inv, o[i][2 * half + 1] * inv);
-            } else {
-#pragma unroll
-              for (int i = 0; i < D / 16; ++i) {
-                const uint2 x = make_uint2(pack_bf16(o[2 * i][2 * half] * inv, o[2 * i + 1][2 * half] * inv),
-                                           pack_bf16(o[2 * i][2 * half + 1] * inv, o[2 * i + 1][2 * half + 1] * inv));
-                *reinterpret_cast<uint2*>(dst + i * 16 + 4 * t) = x;
-              }
-            }
-            if (a.lse && t == 0)
-              a.lse[static_cast<int64_t>(m.row) * a.Hq + h0 + r] =
-                  l_run[half] == 0.f ? -INFINITY : (m_run[half] + log2f(l_run[half])) * kLn2;
-          } else {
-            float* dst = a.part + (static_cast<int64_t>(cta * 2 + m.slot) * 16 * MT + r) * (D + 2);
-#pragma unroll
-            for (int i = 0; i < D / 8; ++i) {
+          for (int half = 0; half < 2; ++half) {
+            const int r = wm * 16 + g + half * 8;
+            if (r >= n_rows) continue;
+            if (x.slot < 0) {
+              const float inv = l_run[half] == 0.f ? 0.f : 1.f / l_run[half];
+              uint16_t* dst = a.out + (static_cast<int64_t>(x.row) * a.Hq + h0 + r) * D;
               if constexpr (!FP8) {
-                *reinterpret_cast<float2*>(dst + i * 8 + 2 * t) = make_float2(o[i][2 * half], o[i][2 * half + 1]);
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i)
+                  *reinterpret_cast<uint32_t*>(dst + i * 8 + 2 * t) =
+                      pack_bf16(o[i][2 * half] * inv, o[i][2 * half + 1] * inv);
               } else {
-                dst[(i / 2) * 16 + 4 * t + (i & 1)] = o[i][2 * half];
-                dst[(i / 2) * 16 + 4 * t + 2 + (i & 1)] = o[i][2 * half + 1];
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i) {
+                  const uint2 x = make_uint2(pack_bf16(o[2 * i][2 * half] * inv, o[2 * i + 1][2 * half] * inv),
+                                             pack_bf16(o[2 * i][2 * half + 1] * inv, o[2 * i + 1][2 * half + 1] * inv));
+                  *reinterpret_cast<uint2*>(dst + i * 16 + 4 * t) = x;
+                }
               }
+              if (a.lse && t == 0)
+                a.lse[static_cast<int64_t>(x.row) * a.Hq + h0 + r] =
+                    l_run[half] == 0.f ? -INFINITY : (m_run[half] + log2f(l_run[half])) * kLn2;
+            } else {
+              float* dst = a.part + (static_cast<int64_t>(cta * 2 + x.slot) * 16 * MT + r) * (D + 2);
+#pragma unroll
+              for (int i = 0; i < D / 8; ++i) {
+                if constexpr (!FP8) {
+                  *reinterpret_cast<float2*>(dst + i * 8 + 2 * t) = make_float2(o[i][2 * half], o[i][2 * half + 1]);
+                } else {
+                  dst[(i / 2) * 16 + 4 * t + (i & 1)] = o[i][2 * half];
+                  dst[(i / 2) * 16 + 4 * t + 2 + (i & 1)] = o[i][2 * half + 1];
+                }
+              }
+              if (t == 0) *reinterpret_cast<float2*>(dst + D) = make_float2(m_run[half], l_run[half]);
             }
-            if (t == 0) *reinterpret_cast<float2*>(dst + D) = make_float2(m_run[half], l_run[half]);
           }
         }
       }
+      ++n_shares;
     }
   }
-  cp_async_wait_all();
 }
 
 // Joins the parts of a row that begins in CTA blockIdx.x and goes on in the
@@ -735,7 +869,6 @@ __global__ void __launch_bounds__(D) k_join_rows(const RowsArgs a, int n_ctas, i
 template <int D, bool FP8, int MT>
 cudaError_t launch_mt(const RowsArgs& a, int grid, cudaStream_t st) {
   using L = Layout<D, FP8, MT>;
-  static_assert(2 * (L::kBytes + 2048) <= 227 * 1024, "two CTAs per SM");
   cudaError_t e = cudaFuncSetAttribute(k_attend_rows<D, FP8, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes);
   if (e != cudaSuccess) return e;
   count_launch();
@@ -767,7 +900,7 @@ int num_sms() {
 }
 
 // The largest grid (partial results are sized for it).
-int max_grid() { return 2 * num_sms(); }
+int max_grid() { return num_sms(); }
 
 int64_t workspace_for(int Hq, int Hkv, int D) {
   const int G = Hq / Hkv;
@@ -823,6 +956,10 @@ int run_rows(const ai_cache* c, int32_t layer, const void* q, int32_t R, int32_t
   a.width = c->max_pages;
   a.n_pages = c->n_pages;
   a.page_size = c->page_size;
+  int s = 0;
+  while ((int64_t(1) << s) < c->page_size) ++s;
+  a.page_shift = 31 + s;
+  a.page_mul = ((uint64_t(1) << a.page_shift) + c->page_size - 1) / c->page_size;
   a.c2 = scale * kLog2e;
   a.out = static_cast<uint16_t*>(out);
   a.lse = lse;
