@@ -13,7 +13,7 @@
 // 128-row tcgen05 tile half empty or worse, and fp8 codes are widened in
 // registers, between shared memory and the product).
 //
-// Work: tiles of 64 keys.  The CTAs (one per SM) divide all tiles of the
+// Work: tiles of 64 or 128 keys (32 KB of keys and values, at most 128 keys).  The CTAs (one per SM) divide all tiles of the
 // batch evenly, whatever the lengths; a row whose tiles lie in several CTAs
 // is joined by a second kernel from per-CTA partial results, always in tile
 // order (no atomics: results do not depend on timing).  With several rows
@@ -21,17 +21,17 @@
 // that rows running at the same time read the same head's keys (L2), and
 // only the last part wave is divided.
 //
-// In a CTA four warps copy, each sixteen keys of a tile: one lane per key looks
-// up where it lies (ids two tiles ahead, the page one), then the warp copies
-// the rows (cp.async, zeros for what is masked) into a ring of stages.  Eight
-// warps compute: two groups of four take the row's tiles in turn, each warp its
-// share of the tile's keys (or of the heads), with its own maximum, sum and
-// output; they meet once per row.  Every warp follows the division of work by
-// itself, a row at a time: what is done per tile by one warp bounds the tile
-// rate (its instructions wait for one another, about 5 cycles each), so it is
-// kept to about a hundred instructions.  (One warp that looked up all keys and
-// told the others took 1500 cycles a tile; gathering rows by TMA, four an
-// operation from one warp, 6500.)
+// In a CTA four warps copy, each a quarter of a tile's keys: one lane per key
+// looks up where it lies (ids two batches of 32 keys ahead, the page one), then
+// the warp copies the rows (cp.async, zeros for what is masked) into a ring of
+// stages.  Eight warps compute: two groups of four take the row's tiles in
+// turn, each warp its share of the tile's keys (or of the heads), with its own
+// maximum, sum and output; they meet once per row.  Every warp follows the
+// division of work by itself, a row at a time: what one warp does per tile
+// bounds the tile rate (its instructions wait for one another, about 5 cycles
+// each, and a look-up for memory).  (One warp that looked up all keys and told
+// the others took 1500 cycles a tile; gathering rows by TMA, four an operation
+// from one warp, 6500.)
 #include <cmath>
 
 #include "../../include/ai_index.h"
@@ -41,9 +41,8 @@
 namespace aiidx {
 namespace {
 
-constexpr int kTile = 64;
 constexpr int kWarps = 8;                       // that compute
-constexpr int kCopiers = 4;                     // that look up and copy sixteen keys of a tile each
+constexpr int kCopiers = 4;                     // that look up and copy a quarter of a tile's keys each
 constexpr int kThreads = (kWarps + kCopiers) * 32;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -59,15 +58,16 @@ struct RowsArgs {
   const int32_t* seqs;      // [R] or nullptr
   int seq_mul;              // sequence of row r without seqs: r * seq_mul
   const int32_t* ids;       // [R, n_ids] or nullptr (cached)
-  int R, n_ids, Hq, Hkv, G;
+  int R, n_ids, nt_ids, Hq, Hkv, G;
   int n_mb, mb_rows;        // row blocks per key head, query heads per block
   int n_seqs, width, n_pages, page_size;
+  int tile;                 // keys of a tile
   uint64_t page_mul;        // token / page_size = token * page_mul >> page_shift
   int page_shift;
   float c2;                 // scale * log2 e
   uint16_t* out;            // [R, Hq, D] bf16
   float* lse;               // [R, Hq] or nullptr
-  float* part;              // partial results: [2 * grid][16 MT][D + 2]
+  float* part;              // partial results: [2 * grid][16 MT][D + 4]
   int32_t* meta;            // [grid][4]
   int32_t* status;          // or nullptr
 };
@@ -129,23 +129,29 @@ template <int D, bool FP8, int MT>
 struct Layout {
   static constexpr int kRow = FP8 ? D : 2 * D;          // bytes of a key row
   static constexpr int kLine = kRow < 128 ? kRow : 128; // bytes of it that lie together
+  static constexpr int kTile = kRow >= 256 ? 64 : 128;  // keys of a tile
   static constexpr int kKV = kTile * kRow;              // bytes of a K or V tile
-  static constexpr int kQRow = 2 * D + 16;              // padded: rows fall on different banks
+  static constexpr int kQRow = 2 * D;
   static constexpr int kQ = 16 * MT * kQRow;
   static constexpr int kScales = FP8 ? 2 * kTile * 4 : 0;
   static constexpr int kWK = 4 / MT;                    // warps of a group along the keys
   static constexpr int kParts = 2 * kWK;                // states that meet per head row
-  static constexpr int kMerge = (kParts - 1) * 16 * MT * (D + 2) * 4;
-  static constexpr int kStages = 131072 / (2 * kKV);    // 128 KB of keys and values
+  static constexpr int kState = D + 4;                  // floats: output, maximum, sum
+  static constexpr int kMerge = kParts * 16 * MT * kState * 4;
+  // 128 KB of keys and values, or what the rest leaves
+  static constexpr int kRoom = (227 * 1024 - 768 - 2 * kQ - kMerge) / (2 * kKV + kScales + 32);
+  static constexpr int kStages = kRoom < 131072 / (2 * kKV) ? kRoom : 131072 / (2 * kKV);
   static constexpr int kBars = 2 * kStages + 6;
-  static constexpr int kBytes = 1024 + kStages * (2 * kKV + kScales + 8) + 2 * kQ + kMerge + kBars * 8 + 16;
-  static_assert(kBytes <= 227 * 1024 - 256, "shared memory");
+  static constexpr int kBytes = kStages * (2 * kKV + kScales + 16) + 2 * kQ + kMerge + kBars * 8 + 16;
+  static_assert(kBytes <= 227 * 1024 - 512, "shared memory");
   // 16-byte chunk c of tile row r: the eight rows of an ldmatrix fall on
   // different banks
   __device__ static uint32_t at(int r, int c) {
     if constexpr (kLine == 128) return (c >> 3) * (kTile * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
     return r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
   }
+  // 16-byte chunk c of query row r
+  __device__ static uint32_t q_at(int r, int c) { return r * kQRow + ((c ^ (r & 7)) << 4); }
   // Tile row of column i of an 8-key product: for fp8 rows of 128 bytes such
   // that the rows of a quarter warp's 16-byte loads fall on different banks
   __device__ static constexpr int key(int i) {
@@ -175,7 +181,7 @@ __device__ __forceinline__ int len_of(const RowsArgs& a, int row) {
   return n < 0 ? 0 : (n > most ? static_cast<int>(most) : n);
 }
 __device__ __forceinline__ int tiles_of(const RowsArgs& a, int row) {
-  return ((a.ids ? a.n_ids : len_of(a, row)) + kTile - 1) / kTile;
+  return (len_of(a, row) + a.tile - 1) / a.tile;
 }
 
 // A share of one item: tiles [t0, t1) of a row and a (key head, row block).
@@ -261,14 +267,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   using L = Layout<D, FP8, MT>;
   constexpr int S = L::kStages;
   constexpr int WK = L::kWK;
-  constexpr int NK = kTile / WK;   // keys of a tile per warp
-  extern __shared__ __align__(1024) uint8_t smem_raw[];
-  uint8_t* stages = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  constexpr int kTile = L::kTile;
+  constexpr int NK = kTile / WK;               // keys of a tile per computing warp
+  constexpr int NB = NK < 32 ? NK : 32;        // of which at a time
+  extern __shared__ __align__(128) uint8_t stages[];
   uint8_t* sq = stages + S * 2 * L::kKV;                        // [2] queries
   float* merge = reinterpret_cast<float*>(sq + 2 * L::kQ);
   float* scales = merge + L::kMerge / 4;                        // [S][2][64]
-  uint64_t* reals = reinterpret_cast<uint64_t*>(scales + S * L::kScales / 4);  // [S] bit i: key i of the tile is there
-  uint64_t* full = reals + S;                                   // [S] tile landed
+  uint32_t* reals = reinterpret_cast<uint32_t*>(scales + S * L::kScales / 4);  // [S][4] bit i of w: key 32 w + i is there
+  uint64_t* full = reinterpret_cast<uint64_t*>(reals + S * 4);                                  // [S] tile landed
   uint64_t* empty = full + S;                                   // [S] tile read
   uint64_t* q_full = empty + S;                                 // [2] queries landed
   uint64_t* q_empty = q_full + 2;                               // [2] queries read
@@ -277,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ int64_t sh_scan[kThreads / 32];
   __shared__ int64_t sh_b0;
   __shared__ int sh_row, sh_n_none;
-  __shared__ int sh_none[kThreads];
+  int* sh_none = reinterpret_cast<int*>(merge);   // before the first row is joined
   int* err = a.status ? a.status : &g_no_status;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -293,8 +300,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&q_full[i], kCopiers * 32);
       mbar_init(&q_empty[i], kWarps);
     }
-    mbar_init(&joined[0], kWarps - MT);
-    mbar_init(&joined[1], MT);
+    mbar_init(&joined[0], kWarps);
+    mbar_init(&joined[1], kWarps);
     *abort = 0;
     sh_n_none = 0;
     fence_mbar_init();
@@ -306,7 +313,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   w.it = cta;
   w.n_whole = 0;
   w.by_head = a.ids != nullptr;
-  w.nt_ids = (a.n_ids + kTile - 1) / kTile;
+  w.nt_ids = a.nt_ids;
   w.n_heads = n_heads;
   int64_t total;
   if (a.ids) {
@@ -392,97 +399,138 @@ __global__ void __launch_bounds__(kThreads, 1)
     // on in the next CTA that has a share, or -1 (2)
     if (cw == 0 && lane == 0) *reinterpret_cast<int4*>(a.meta + cta * 4) = make_int4(-1, 1, -1, -1);
     __syncwarp();
+    // A batch: 32 keys of this warp, that is one or two tiles of a share.
+    constexpr int KW = kTile / kCopiers, BT = 32 / KW;
+    const int sub = lane / KW, key = cw * KW + lane % KW;
+    struct Batch {
+      Share x;
+      int t;          // first tile; x.t1 where there is none
+      int seq, len;
+      int tok;        // this lane's token, -1: none
+    };
+    bool more = w.next(a, &x);
+    int seq = 0, len = 0, t_next = 0;
+    auto enter = [&]() {
+      seq = seq_of(a, x.row);
+      len = len_of(a, x.row);
+      t_next = x.t0;
+    };
+    if (more) enter();
+    // step 1: the tokens of the next batch
+    auto plan = [&](Batch& p) {
+      p.tok = -1;
+      p.len = 0;
+      p.t = p.x.t1 = 0;
+      if (!more) return;
+      p.x = x;
+      p.t = t_next;
+      p.seq = seq;
+      p.len = len;
+      const int t = t_next + sub, at = t * kTile + key;
+      if (t < x.t1) {
+        if (!a.ids) p.tok = at < len ? at : -1;
+        else if (at < a.n_ids) p.tok = a.ids[static_cast<int64_t>(x.row) * a.n_ids + at];
+      }
+      t_next += BT;
+      if (t_next >= x.t1) {
+        const int row = x.row;
+        more = w.next(a, &x);
+        t_next = x.t0;
+        if (more && x.row != row) enter();
+      }
+    };
+    // step 2: their pages
+    auto page = [&](Batch& p) {
+      if (p.tok >= p.len) {
+        if (p.tok >= 0) atomicOr(err, AI_DEVFLAG_RANGE);
+        p.tok = -1;
+      }
+      return p.tok >= 0 ? a.tables[static_cast<int64_t>(p.seq) * a.width + page_of(a, p.tok)] : -1;
+    };
+    Batch now, ahead;
+    plan(now);
+    int pg = page(now);
+    plan(ahead);
     uint32_t n = 0, n_shares = 0;
     bool ok = true;
-    while (ok && w.next(a, &x)) {
-      const int seq = seq_of(a, x.row), len = len_of(a, x.row);
-      const int kv_head = a.n_mb == 1 ? x.head : x.head / a.n_mb;
-      if (cw == 0 && lane == 0 && x.slot >= 0) {
-        const int item = x.row * n_heads + x.head;
-        if (x.slot == 1) {
-          a.meta[cta * 4 + 2] = item;
-        } else {
-          a.meta[cta * 4 + 0] = item;
-          a.meta[cta * 4 + 1] = x.ends;
-        }
+    int kv_head = 0;
+    while (ok && now.t < now.x.t1) {
+      const int next_pg = page(ahead);
+      Batch later;
+      plan(later);
+      // step 3: their rows in the pool (-1: none), and the copies
+      int row = -1;
+      if (now.tok >= 0) {
+        if (pg >= 0 && pg < a.n_pages) row = pg * a.page_size + (now.tok - page_of(a, now.tok) * a.page_size);
+        else atomicOr(err, AI_DEVFLAG_RANGE);
       }
-      // the queries
-      const uint32_t qs = n_shares & 1;
-      if (n_shares >= 2 && !__all_sync(0xffffffffu, mbar_wait(&q_empty[qs], (n_shares / 2 - 1) & 1, err, abort))) break;
-      {
-        const int h0 = kv_head * a.G + (x.head - kv_head * a.n_mb) * a.mb_rows;
+      const uint32_t real = __ballot_sync(0xffffffffu, row >= 0);
+      if (now.t == now.x.t0) {
+        kv_head = a.n_mb == 1 ? now.x.head : now.x.head / a.n_mb;
+        if (cw == 0 && lane == 0 && now.x.slot >= 0) {
+          const int item = now.x.row * n_heads + now.x.head;
+          if (now.x.slot == 1) {
+            a.meta[cta * 4 + 2] = item;
+          } else {
+            a.meta[cta * 4 + 0] = item;
+            a.meta[cta * 4 + 1] = now.x.ends;
+          }
+        }
+        const uint32_t qs = n_shares & 1;
+        if (n_shares >= 2 && !__all_sync(0xffffffffu, mbar_wait(&q_empty[qs], (n_shares / 2 - 1) & 1, err, abort))) break;
+        const int h0 = kv_head * a.G + (now.x.head - kv_head * a.n_mb) * a.mb_rows;
         const int n_rows = min(a.mb_rows, (kv_head + 1) * a.G - h0);
         const uint32_t dst = smem_u32(sq + qs * L::kQ);
-        const uint16_t* src = a.q + (static_cast<int64_t>(x.row) * a.Hq + h0) * D;
+        const uint16_t* src = a.q + (static_cast<int64_t>(now.x.row) * a.Hq + h0) * D;
         for (int i = cw * 32 + lane; i < 16 * MT * (D / 8); i += kCopiers * 32) {
           const int r = i / (D / 8), c = i % (D / 8);
-          cp16z(dst + r * L::kQRow + c * 16, src + (r < n_rows ? r * D : 0) + c * 8, r < n_rows);
+          cp16z(dst + L::q_at(r, c), src + (r < n_rows ? r * D : 0) + c * 8, r < n_rows);
         }
         cp_async_mbar_arrive_noinc(&q_full[qs]);
+        ++n_shares;
       }
-      ++n_shares;
-      // lane l (and l + 16) looks up key l of this warp's sixteen of a tile:
-      // its token, then its page, then its row in the pool (-1: none)
-      const int32_t* table = a.tables + static_cast<int64_t>(seq) * a.width;
-      const int32_t* ids = a.ids ? a.ids + static_cast<int64_t>(x.row) * a.n_ids : nullptr;
-      const int key = cw * 16 + (lane & 15);
-      auto token = [&](int t) {
-        const int at = t * kTile + key;
-        if (!ids) return t < x.t1 && at < len ? at : -1;
-        return t < x.t1 && at < a.n_ids ? ids[at] : -1;
-      };
-      auto page = [&](int* tok) {
-        if (*tok >= len) {
-          atomicOr(err, AI_DEVFLAG_RANGE);
-          *tok = -1;
-        }
-        return *tok >= 0 ? table[page_of(a, *tok)] : -1;
-      };
-      int tok = token(x.t0), tok1 = token(x.t0 + 1);
-      int pg = page(&tok);
       const uint8_t* kb = a.k + kv_head * L::kRow + chunk * 16;
       const uint8_t* vb = a.v + kv_head * L::kRow + chunk * 16;
-      for (int t = x.t0; t < x.t1; ++t, ++n) {
-        const int tok2 = token(t + 2);
-        const int pg1 = page(&tok1);
-        int row = -1;
-        if (tok >= 0) {
-          if (pg >= 0 && pg < a.n_pages) row = pg * a.page_size + (tok - page_of(a, tok) * a.page_size);
-          else atomicOr(err, AI_DEVFLAG_RANGE);
-        }
-        tok = tok1;
-        tok1 = tok2;
-        pg = pg1;
+#pragma unroll
+      for (int j = 0; j < BT; ++j) {
+        if (now.t + j >= now.x.t1) break;
         const uint32_t st = n % S;
         if (n >= S && !__all_sync(0xffffffffu, mbar_wait(&empty[st], (n / S - 1) & 1, err, abort))) {
           ok = false;
           break;
         }
-        const uint32_t real = __ballot_sync(0xffffffffu, row >= 0) & 0xffffu;
-        if (lane == 0) reinterpret_cast<uint16_t*>(reals + st)[cw] = static_cast<uint16_t>(real);
-        // (a computing warp that takes keys of several copying warps needs the
+        if (lane == 0) {
+          if constexpr (KW == 32) reals[st * 4 + cw] = real;
+          else reinterpret_cast<uint16_t*>(reals + st * 4)[cw] = static_cast<uint16_t>(real >> (j * 16));
+        }
+        // (a computing warp's keys may be several copying warps', and needs the
         // zeros of those that have none)
-        if (real || NK > 16) {
+        if (NB > KW || (real >> (j * KW)) & (KW == 32 ? 0xffffffffu : 0xffffu)) {
           const uint32_t dst = smem_u32(stages + st * 2 * L::kKV);
 #pragma unroll
-          for (int i = 0; i < 16; i += kStep) {
+          for (int i = 0; i < KW; i += kStep) {
             const int r = i + r_lane;
-            const int src = __shfl_sync(0xffffffffu, row, r);
+            const int src = __shfl_sync(0xffffffffu, row, j * KW + r);
             const int64_t off = src < 0 ? 0 : src * row_bytes;
-            const uint32_t to = dst + L::at(cw * 16 + r, chunk);
+            const uint32_t to = dst + L::at(cw * KW + r, chunk);
             cp16z(to, kb + off, src >= 0);
             cp16z(to + L::kKV, vb + off, src >= 0);
           }
           if constexpr (FP8) {
             const int64_t off = row < 0 ? 0 : static_cast<int64_t>(row) * a.Hkv + kv_head;
-            cp4z(smem_u32(scales + st * 2 * kTile + (lane >> 4) * kTile + key), (lane < 16 ? a.ks : a.vs) + off,
-                 row >= 0);
+            const uint32_t to = smem_u32(scales + st * 2 * kTile + key);
+            cp4z(to, a.ks + off, row >= 0);
+            cp4z(to + kTile * 4, a.vs + off, row >= 0);
           }
         }
         cp_async_mbar_arrive_noinc(&full[st]);
         __syncwarp();
         if (lane == 0) mbar_arrive(&full[st]);
+        ++n;
       }
+      now = ahead;
+      ahead = later;
+      pg = next_pg;
     }
     cp_async_wait_all();
   } else {
@@ -508,16 +556,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t qs = n_shares & 1;
       if (!__all_sync(0xffffffffu, mbar_wait(&q_full[qs], (n_shares / 2) & 1, err, abort))) break;
       {
-        const uint8_t* q = sq + qs * L::kQ + wm * 16 * L::kQRow;
+        const uint8_t* q = sq + qs * L::kQ;
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           if constexpr (!FP8) {
-            ldsm4(qf[kk], smem_u32(q) + (lane & 15) * L::kQRow + kk * 32 + (lane >> 4) * 16);
+            ldsm4(qf[kk], smem_u32(q) + L::q_at(wm * 16 + (lane & 15), kk * 2 + (lane >> 4)));
           } else {
             // the product's sum over d in the order of the codes' 16-byte loads
             const int d = (kk / 4) * 64 + t * 16 + (kk % 4) * 4;
-            const uint2 x = *reinterpret_cast<const uint2*>(q + g * L::kQRow + d * 2);
-            const uint2 y = *reinterpret_cast<const uint2*>(q + (g + 8) * L::kQRow + d * 2);
+            const uint2 x = *reinterpret_cast<const uint2*>(q + L::q_at(wm * 16 + g, d / 8) + (d % 8) * 2);
+            const uint2 y = *reinterpret_cast<const uint2*>(q + L::q_at(wm * 16 + g + 8, d / 8) + (d % 8) * 2);
             qf[kk][0] = x.x;
             qf[kk][1] = y.x;
             qf[kk][2] = x.y;
@@ -568,31 +616,34 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const uint8_t* stage = stages + st * 2 * L::kKV;
       const uint32_t sk = smem_u32(stage), sv = sk + L::kKV;
-      // the warp's keys of the tile, one bit each
-      const uint64_t real = reals[st] >> (wk * NK);
-      constexpr uint64_t kAll = NK == 64 ? ~0ull : (1ull << (NK % 64)) - 1;
-      if ((n & 1) == group && (real & kAll)) {
-        float s[NK / 8][4];
+      if ((n & 1) == group) {
 #pragma unroll
-        for (int j = 0; j < NK / 8; ++j) s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
+      for (int blk = 0; blk < NK / NB; ++blk) {
+        const int k0 = wk * NK + blk * NB;      // first key of the block
+        constexpr uint32_t kAll = NB == 32 ? 0xffffffffu : (1u << (NB % 32)) - 1;
+        const uint32_t real = (reals[st * 4 + k0 / 32] >> (k0 % 32)) & kAll;  // its keys, one bit each
+        if (real == 0) continue;
+        float s[NB / 8][4];
+#pragma unroll
+        for (int j = 0; j < NB / 8; ++j) s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
         if constexpr (!FP8) {
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
 #pragma unroll
-            for (int j = 0; j < NK / 16; ++j) {
+            for (int j = 0; j < NB / 16; ++j) {
               uint32_t b[4];
-              ldsm4(b, sk + L::at(wk * NK + j * 16 + (lane & 7) + ((lane >> 4) << 3), kk * 2 + ((lane >> 3) & 1)));
+              ldsm4(b, sk + L::at(k0 + j * 16 + (lane & 7) + ((lane >> 4) << 3), kk * 2 + ((lane >> 3) & 1)));
               mma<false>(s[2 * j], qf[kk], b[0], b[1]);
               mma<false>(s[2 * j + 1], qf[kk], b[2], b[3]);
             }
           }
         } else {
 #pragma unroll
-          for (int j = 0; j < NK / 8; ++j) {
+          for (int c4 = 0; c4 < D / 64; ++c4) {
 #pragma unroll
-            for (int c4 = 0; c4 < D / 64; ++c4) {
+            for (int j = 0; j < NB / 8; ++j) {
               const uint4 x =
-                  *reinterpret_cast<const uint4*>(stage + L::at(wk * NK + j * 8 + L::key(g), c4 * 4 + t));
+                  *reinterpret_cast<const uint4*>(stage + L::at(k0 + j * 8 + L::key(g), c4 * 4 + t));
               const uint32_t u[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
               for (int i = 0; i < 4; ++i)
@@ -601,30 +652,30 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         // scale, mask and the running maximum
-        const float* ksc = scales + st * 2 * kTile + wk * NK;
+        const float* ksc = scales + st * 2 * kTile + k0;
         float mx[2] = {-INFINITY, -INFINITY};
-        float lv[FP8 ? NK / 4 : 1], e_max = e_run;
+        float lv[FP8 ? NB / 4 : 1], e_max = e_run;
 #pragma unroll
-        for (int j = 0; j < NK / 8; ++j) {
+        for (int j = 0; j < NB / 8; ++j) {
           if constexpr (FP8) {
-            const int k0 = j * 8 + L::key(2 * t), k1 = j * 8 + L::key(2 * t + 1);
-            const float f0 = ksc[k0], f1 = ksc[k1];
+            const int i0 = j * 8 + L::key(2 * t), i1 = j * 8 + L::key(2 * t + 1);
+            const float f0 = ksc[i0], f1 = ksc[i1];
             s[j][0] *= c2[0] * f0;
             s[j][1] *= c2[0] * f1;
             s[j][2] *= c2[1] * f0;
             s[j][3] *= c2[1] * f1;
-            lv[2 * j] = __log2f(ksc[kTile + k0]);
-            lv[2 * j + 1] = __log2f(ksc[kTile + k1]);
+            lv[2 * j] = __log2f(ksc[kTile + i0]);
+            lv[2 * j + 1] = __log2f(ksc[kTile + i1]);
             e_max = fmaxf(e_max, fmaxf(lv[2 * j], lv[2 * j + 1]));
           } else {
 #pragma unroll
             for (int i = 0; i < 4; ++i) s[j][i] *= a.c2;
           }
         }
-        if ((real & kAll) != kAll) {
+        if (real != kAll) {
 #pragma unroll
-          for (int j = 0; j < NK / 8; ++j) {
-            const uint32_t bits = static_cast<uint32_t>(real >> (j * 8));
+          for (int j = 0; j < NB / 8; ++j) {
+            const uint32_t bits = real >> (j * 8);
             const bool r0 = (bits >> L::key(2 * t)) & 1, r1 = (bits >> L::key(2 * t + 1)) & 1;
             s[j][0] = r0 ? s[j][0] : -INFINITY;
             s[j][1] = r1 ? s[j][1] : -INFINITY;
@@ -633,7 +684,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
 #pragma unroll
-        for (int j = 0; j < NK / 8; ++j) {
+        for (int j = 0; j < NB / 8; ++j) {
           mx[0] = fmaxf(mx[0], fmaxf(s[j][0], s[j][1]));
           mx[1] = fmaxf(mx[1], fmaxf(s[j][2], s[j][3]));
         }
@@ -673,10 +724,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float mu[2] = {m_run[0] == -INFINITY ? 0.f : m_run[0], m_run[1] == -INFINITY ? 0.f : m_run[1]};
         // the weights, rounded once (bf16; fp8: f16) for the product with v;
         // their sum is taken before that rounding
-        uint32_t p[NK / 16][4];
+        uint32_t p[NB / 16][4];
         const float lift = kLift - (e_run == -INFINITY ? 0.f : e_run);
 #pragma unroll
-        for (int j = 0; j < NK / 8; ++j) {
+        for (int j = 0; j < NB / 8; ++j) {
           const float x0 = s[j][0] - mu[0], x1 = s[j][1] - mu[0], x2 = s[j][2] - mu[1], x3 = s[j][3] - mu[1];
           const float e0 = exp2_approx(x0), e1 = exp2_approx(x1), e2 = exp2_approx(x2), e3 = exp2_approx(x3);
           l_run[0] += e0 + e1;
@@ -691,10 +742,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         // lane i gives the address of row i of an 8 x 8 block, in the keys' order
-        const int vr = wk * NK + (lane & 8) + L::key(lane & 7);
+        const int vr = k0 + (lane & 8) + L::key(lane & 7);
         if constexpr (!FP8) {
 #pragma unroll
-          for (int j = 0; j < NK / 16; ++j) {
+          for (int j = 0; j < NB / 16; ++j) {
 #pragma unroll
             for (int dd = 0; dd < D / 16; ++dd) {
               uint32_t b[4];
@@ -707,7 +758,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // 16-bit transposed loads bring two neighbouring codes of two keys;
           // accumulator 2 i holds the even, 2 i + 1 the odd d of 16-code chunk i
 #pragma unroll
-          for (int j = 0; j < NK / 16; ++j) {
+          for (int j = 0; j < NB / 16; ++j) {
 #pragma unroll
             for (int cc = 0; cc < D / 32; ++cc) {
               uint32_t b[4];
@@ -723,6 +774,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
+      }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[st]);
@@ -745,89 +797,74 @@ __global__ void __launch_bounds__(kThreads, 1)
             o[i][3] *= f;
           }
         }
-        float* mine = merge + ((part - 1) * MT + wm) * 16 * (D + 2);
-        if (part > 0) {
-          // the states of the row before have been read
-          if (n_shares > 0 &&
-              !__all_sync(0xffffffffu, mbar_wait(&joined[1], (n_shares - 1) & 1, err, abort)))
-            break;
+        // the states of the row before have been read
+        if (n_shares > 0 && !__all_sync(0xffffffffu, mbar_wait(&joined[1], (n_shares - 1) & 1, err, abort))) break;
+        float* mine = merge + (part * MT + wm) * 16 * L::kState;
 #pragma unroll
-          for (int i = 0; i < D / 8; ++i) {
-            *reinterpret_cast<float2*>(mine + g * (D + 2) + i * 8 + 2 * t) = make_float2(o[i][0], o[i][1]);
-            *reinterpret_cast<float2*>(mine + (g + 8) * (D + 2) + i * 8 + 2 * t) = make_float2(o[i][2], o[i][3]);
+        for (int half = 0; half < 2; ++half) {
+          float* to = mine + (g + half * 8) * L::kState;
+          if constexpr (!FP8) {
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i)
+              *reinterpret_cast<float2*>(to + i * 8 + 2 * t) = make_float2(o[i][2 * half], o[i][2 * half + 1]);
+          } else {
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i)
+              *reinterpret_cast<float4*>(to + i * 16 + 4 * t) =
+                  make_float4(o[2 * i][2 * half], o[2 * i + 1][2 * half], o[2 * i][2 * half + 1], o[2 * i + 1][2 * half + 1]);
           }
-          if (t == 0) {
-            *reinterpret_cast<float2*>(mine + g * (D + 2) + D) = make_float2(m_run[0], l_run[0]);
-            *reinterpret_cast<float2*>(mine + (g + 8) * (D + 2) + D) = make_float2(m_run[1], l_run[1]);
-          }
+          if (t == 0) *reinterpret_cast<float2*>(to + D) = make_float2(m_run[half], l_run[half]);
         }
         __syncwarp();
-        if (part > 0) {
-          if (lane == 0) mbar_arrive(&joined[0]);
-        } else {
-          if (!__all_sync(0xffffffffu, mbar_wait(&joined[0], n_shares & 1, err, abort))) break;
-          for (int ww = 1; ww < L::kParts; ++ww) {
-            const float* src = merge + ((ww - 1) * MT + wm) * 16 * (D + 2);
+        if (lane == 0) mbar_arrive(&joined[0]);
+        if (!__all_sync(0xffffffffu, mbar_wait(&joined[0], n_shares & 1, err, abort))) break;
+        // each thread joins a piece of one head row
+        constexpr int kPer = 16 * MT * D / (kWarps * 32);   // its columns: 8 to 32 (D = 64: 4 to 16)
+        const int r = tid * kPer / D, c0 = tid * kPer % D;
+        const float* from = merge + ((r >> 4) * 16 + (r & 15)) * L::kState;
+        constexpr int kNext = MT * 16 * L::kState;          // the next part's state of the row
+        float wgt[L::kParts], m = -INFINITY, l = 0.f;
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              const float* sr = src + (g + half * 8) * (D + 2);
-              const float2 ml = *reinterpret_cast<const float2*>(sr + D);
-              const float mn = fmaxf(m_run[half], ml.x);
-              const float mz = mn == -INFINITY ? 0.f : mn;
-              const float f0 = exp2_approx(m_run[half] - mz), f1 = exp2_approx(ml.x - mz);
-              m_run[half] = mn;
-              l_run[half] = l_run[half] * f0 + ml.y * f1;
+        for (int i = 0; i < L::kParts; ++i) m = fmaxf(m, from[i * kNext + D]);
+        const float mz = m == -INFINITY ? 0.f : m;
 #pragma unroll
-              for (int i = 0; i < D / 8; ++i) {
-                const float2 x = *reinterpret_cast<const float2*>(sr + i * 8 + 2 * t);
-                o[i][2 * half] = o[i][2 * half] * f0 + x.x * f1;
-                o[i][2 * half + 1] = o[i][2 * half + 1] * f0 + x.y * f1;
-              }
-            }
+        for (int i = 0; i < L::kParts; ++i) {
+          wgt[i] = exp2_approx(from[i * kNext + D] - mz);
+          l += from[i * kNext + D + 1] * wgt[i];
+        }
+        const int kv_head = a.n_mb == 1 ? x.head : x.head / a.n_mb;
+        const int h0 = kv_head * a.G + (x.head - kv_head * a.n_mb) * a.mb_rows;
+        const bool used = r < min(a.mb_rows, (kv_head + 1) * a.G - h0);
+        const float inv = x.slot >= 0 ? 1.f : (l == 0.f ? 0.f : 1.f / l);
+#pragma unroll
+        for (int c = 0; c < kPer; c += 4) {
+          float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int i = 0; i < L::kParts; ++i) {
+            const float4 z = *reinterpret_cast<const float4*>(from + i * kNext + c0 + c);
+            y.x = fmaf(z.x, wgt[i], y.x);
+            y.y = fmaf(z.y, wgt[i], y.y);
+            y.z = fmaf(z.z, wgt[i], y.z);
+            y.w = fmaf(z.w, wgt[i], y.w);
           }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&joined[1]);
-          const int kv_head = a.n_mb == 1 ? x.head : x.head / a.n_mb;
-          const int h0 = kv_head * a.G + (x.head - kv_head * a.n_mb) * a.mb_rows;
-          const int n_rows = min(a.mb_rows, (kv_head + 1) * a.G - h0);
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            const int r = wm * 16 + g + half * 8;
-            if (r >= n_rows) continue;
-            if (x.slot < 0) {
-              const float inv = l_run[half] == 0.f ? 0.f : 1.f / l_run[half];
-              uint16_t* dst = a.out + (static_cast<int64_t>(x.row) * a.Hq + h0 + r) * D;
-              if constexpr (!FP8) {
-#pragma unroll
-                for (int i = 0; i < D / 8; ++i)
-                  *reinterpret_cast<uint32_t*>(dst + i * 8 + 2 * t) =
-                      pack_bf16(o[i][2 * half] * inv, o[i][2 * half + 1] * inv);
-              } else {
-#pragma unroll
-                for (int i = 0; i < D / 16; ++i) {
-                  const uint2 x = make_uint2(pack_bf16(o[2 * i][2 * half] * inv, o[2 * i + 1][2 * half] * inv),
-                                             pack_bf16(o[2 * i][2 * half + 1] * inv, o[2 * i + 1][2 * half + 1] * inv));
-                  *reinterpret_cast<uint2*>(dst + i * 16 + 4 * t) = x;
-                }
-              }
-              if (a.lse && t == 0)
-                a.lse[static_cast<int64_t>(x.row) * a.Hq + h0 + r] =
-                    l_run[half] == 0.f ? -INFINITY : (m_run[half] + log2f(l_run[half])) * kLn2;
-            } else {
-              float* dst = a.part + (static_cast<int64_t>(cta * 2 + x.slot) * 16 * MT + r) * (D + 2);
-#pragma unroll
-              for (int i = 0; i < D / 8; ++i) {
-                if constexpr (!FP8) {
-                  *reinterpret_cast<float2*>(dst + i * 8 + 2 * t) = make_float2(o[i][2 * half], o[i][2 * half + 1]);
-                } else {
-                  dst[(i / 2) * 16 + 4 * t + (i & 1)] = o[i][2 * half];
-                  dst[(i / 2) * 16 + 4 * t + 2 + (i & 1)] = o[i][2 * half + 1];
-                }
-              }
-              if (t == 0) *reinterpret_cast<float2*>(dst + D) = make_float2(m_run[half], l_run[half]);
-            }
+          if (used) {
+            if (x.slot < 0)
+              *reinterpret_cast<uint2*>(a.out + (static_cast<int64_t>(x.row) * a.Hq + h0 + r) * D + c0 + c) =
+                  make_uint2(pack_bf16(y.x * inv, y.y * inv), pack_bf16(y.z * inv, y.w * inv));
+            else
+              *reinterpret_cast<float4*>(a.part + (static_cast<int64_t>(cta * 2 + x.slot) * 16 * MT + r) * L::kState +
+                                         c0 + c) = y;
           }
         }
+        if (used && c0 == 0) {
+          if (x.slot >= 0)
+            *reinterpret_cast<float2*>(a.part + (static_cast<int64_t>(cta * 2 + x.slot) * 16 * MT + r) * L::kState + D) =
+                make_float2(m, l);
+          else if (a.lse)
+            a.lse[static_cast<int64_t>(x.row) * a.Hq + h0 + r] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&joined[1]);
       }
       ++n_shares;
     }
@@ -846,12 +883,12 @@ __global__ void __launch_bounds__(D) k_join_rows(const RowsArgs a, int n_ctas, i
   const int h = head / a.n_mb;
   const int h0 = h * a.G + (head % a.n_mb) * a.mb_rows;
   if (r >= min(a.mb_rows, (h + 1) * a.G - h0)) return;
-  const float* p = a.part + (static_cast<int64_t>(c * 2 + 1) * rows_per_slot + r) * (D + 2);
+  const float* p = a.part + (static_cast<int64_t>(c * 2 + 1) * rows_per_slot + r) * (D + 4);
   float m = p[D], l = p[D + 1], o = p[d];
   for (int n = c + 1; n < n_ctas; ++n) {
     if (a.meta[n * 4] < 0) continue;  // a CTA without a share
     const bool ends = a.meta[n * 4 + 1] != 0;
-    const float* q = a.part + (static_cast<int64_t>(n * 2) * rows_per_slot + r) * (D + 2);
+    const float* q = a.part + (static_cast<int64_t>(n * 2) * rows_per_slot + r) * (D + 4);
     const float mn = fmaxf(m, q[D]);
     const float mz = mn == -INFINITY ? 0.f : mn;
     const float f0 = exp2_approx(m - mz), f1 = exp2_approx(q[D] - mz);
@@ -908,7 +945,7 @@ int64_t workspace_for(int Hq, int Hkv, int D) {
   const int rows = ((G + mb - 1) / mb + 15) / 16 * 16;
   const int padded = rows <= 16 ? 16 : (rows <= 32 ? 32 : 64);
   const int64_t g = max_grid();
-  return g * 16 + g * 2 * padded * (D + 2) * 4;
+  return g * 16 + g * 2 * padded * (D + 4) * 4;
 }
 
 int run_rows(const ai_cache* c, int32_t layer, const void* q, int32_t R, int32_t Hq, const int32_t* ids, int32_t n_ids,
@@ -960,12 +997,14 @@ int run_rows(const ai_cache* c, int32_t layer, const void* q, int32_t R, int32_t
   while ((int64_t(1) << s) < c->page_size) ++s;
   a.page_shift = 31 + s;
   a.page_mul = ((uint64_t(1) << a.page_shift) + c->page_size - 1) / c->page_size;
+  a.tile = c->head_dim * es >= 256 ? 64 : 128;  // Layout::kTile
+  a.nt_ids = (n_ids + a.tile - 1) / a.tile;
   a.c2 = scale * kLog2e;
   a.out = static_cast<uint16_t*>(out);
   a.lse = lse;
   a.status = c->status;
   const int64_t most = ids ? n_ids : static_cast<int64_t>(c->max_pages) * c->page_size;
-  const int64_t tiles = static_cast<int64_t>(R) * a.Hkv * n_mb * ((most + kTile - 1) / kTile);
+  const int64_t tiles = static_cast<int64_t>(R) * a.Hkv * n_mb * ((most + a.tile - 1) / a.tile);
   const int grid = static_cast<int>(tiles < 1 ? 1 : (tiles < max_grid() ? tiles : max_grid()));
   a.meta = static_cast<int32_t*>(ws);
   a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + static_cast<int64_t>(max_grid()) * 16);
