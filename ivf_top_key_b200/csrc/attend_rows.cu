@@ -34,9 +34,7 @@
 // from one warp, 6500.)
 #include <cmath>
 
-#include "../../include/ai_index.h"
-#include "common.cuh"
-#include "kernels.h"
+#include "attend_rows.cuh"
 
 namespace aiidx {
 namespace {
@@ -44,86 +42,6 @@ namespace {
 constexpr int kWarps = 8;                       // that compute
 constexpr int kCopiers = 4;                     // that look up and copy a quarter of a tile's keys each
 constexpr int kThreads = (kWarps + kCopiers) * 32;
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
-
-struct RowsArgs {
-  const uint16_t* q;        // [R, Hq, D] bf16
-  const uint8_t* k;         // pages of one layer, bytes
-  const uint8_t* v;
-  const float* ks;          // [n_pages * page_size, Hkv] or nullptr
-  const float* vs;
-  const int32_t* tables;    // [n_seqs, width]
-  const int32_t* lens;      // [n_seqs]
-  const int32_t* seqs;      // [R] or nullptr
-  int seq_mul;              // sequence of row r without seqs: r * seq_mul
-  const int32_t* ids;       // [R, n_ids] or nullptr (cached)
-  int R, n_ids, nt_ids, Hq, Hkv, G;
-  int n_mb, mb_rows;        // row blocks per key head, query heads per block
-  int n_seqs, width, n_pages, page_size;
-  int tile;                 // keys of a tile
-  uint64_t page_mul;        // token / page_size = token * page_mul >> page_shift
-  int page_shift;
-  float c2;                 // scale * log2 e
-  uint16_t* out;            // [R, Hq, D] bf16
-  float* lse;               // [R, Hq] or nullptr
-  float* part;              // partial results: [2 * grid][16 MT][D + 4]
-  int32_t* meta;            // [grid][4]
-  int32_t* status;          // or nullptr
-};
-
-// ------------------------------------------------------------- warp products
-template <bool F16>
-__device__ __forceinline__ void mma(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
-  if constexpr (F16)
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-        "{%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-  else
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-        "{%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ void ldsm4(uint32_t* r, uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr));
-}
-__device__ __forceinline__ void ldsm4t(uint32_t* r, uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr));
-}
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&b);
-}
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-  const __half2 h = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-// Two e4m3 codes (low byte first) to two f16 values, exactly.
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t codes) {
-  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(codes), __NV_E4M3);
-  return static_cast<uint32_t>(h.x) | (static_cast<uint32_t>(h.y) << 16);
-}
-__device__ __forceinline__ float exp2_approx(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-// 16 or 4 bytes to shared memory, zeros where !real.
-__device__ __forceinline__ void cp16z(uint32_t dst, const void* src, bool real) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(real ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void cp4z(uint32_t dst, const void* src, bool real) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(real ? 4 : 0) : "memory");
-}
-
 // ------------------------------------------------------------ shared memory
 template <int D, bool FP8, int MT>
 struct Layout {
@@ -160,107 +78,6 @@ struct Layout {
   }
 };
 
-__device__ int g_no_status;  // where flags go when the caller gives no status word
-
-// ----------------------------------------------------------- division of work
-// Division of a token (< 2^31) by the page size: with s = ceil(log2 d),
-// m = ceil(2^(31 + s) / d) < 2^32 the quotient is exactly n m >> (31 + s)
-// (Granlund and Montgomery, 1994).
-__device__ __forceinline__ int page_of(const RowsArgs& a, int tok) {
-  return static_cast<int>(static_cast<uint64_t>(static_cast<uint32_t>(tok)) * a.page_mul >> a.page_shift);
-}
-__device__ __forceinline__ int seq_of(const RowsArgs& a, int row) {
-  return a.seqs ? a.seqs[row] : row * a.seq_mul;
-}
-__device__ __forceinline__ int len_of(const RowsArgs& a, int row) {
-  const int s = seq_of(a, row);
-  if (s < 0 || s >= a.n_seqs) return 0;
-  const int64_t most = static_cast<int64_t>(a.width) * a.page_size;
-  const int n = a.lens[s];
-  if ((n < 0 || n > most) && a.status) atomicOr(a.status, AI_DEVFLAG_RANGE);
-  return n < 0 ? 0 : (n > most ? static_cast<int>(most) : n);
-}
-__device__ __forceinline__ int tiles_of(const RowsArgs& a, int row) {
-  return (len_of(a, row) + a.tile - 1) / a.tile;
-}
-
-// A share of one item: tiles [t0, t1) of a row and a (key head, row block).
-struct Share {
-  int row, head, t0, t1;
-  int slot;     // -1: the whole item; 0 / 1: partial result slot
-  bool ends;    // the item's last tile is in it
-};
-
-// The shares of a CTA in order: whole items dealt out in turn (item it, it +
-// grid, .. < n_whole; heads outermost), then the tiles [b, b1) of the divided
-// items, which follow one another.  Every warp runs its own.
-struct Walk {
-  int it, n_whole, grid;
-  int64_t b, b1;
-  bool by_head;        // heads outermost (selected), else rows (cached)
-  int row, head;       // of the next divided item
-  int tile, n_tiles;   // its next tile, and its tiles
-  int nt_ids, n_heads;
-
-  __device__ bool next(const RowsArgs& a, Share* s) {
-    if (it < n_whole) {
-      s->head = it / a.R;
-      s->row = it - s->head * a.R;
-      s->t0 = 0;
-      s->t1 = nt_ids;
-      s->slot = -1;
-      s->ends = true;
-      it += grid;
-      return true;
-    }
-    if (b >= b1) return false;
-    const int64_t left = b1 - b;
-    s->row = row;
-    s->head = head;
-    s->t0 = tile;
-    s->ends = left >= n_tiles - tile;
-    s->t1 = s->ends ? n_tiles : tile + static_cast<int>(left);
-    // begun in an earlier CTA: its first slot; goes on in a later one: its second
-    s->slot = tile > 0 ? 0 : (s->ends ? -1 : 1);
-    b += s->t1 - tile;
-    tile = 0;
-    if (by_head) {
-      if (++row == a.R) {
-        row = 0;
-        ++head;
-      }
-    } else if (++head == n_heads) {
-      head = 0;
-      if (b < b1) {
-        do ++row;
-        while (row < a.R && tiles_of(a, row) == 0);
-        n_tiles = row < a.R ? tiles_of(a, row) : 1;
-      }
-    }
-    return true;
-  }
-};
-
-// Block-wide sum and exclusive prefix of one int64 per thread.
-__device__ int64_t block_scan(int64_t x, int64_t* total, int64_t* warp_sums) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int64_t inc = x;
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t y = __shfl_up_sync(0xffffffffu, inc, o);
-    if (lane >= o) inc += y;
-  }
-  __syncthreads();
-  if (lane == 31) warp_sums[warp] = inc;
-  __syncthreads();
-  int64_t before = 0, sum = 0;
-  for (int w = 0; w < kThreads / 32; ++w) {
-    if (w < warp) before += warp_sums[w];
-    sum += warp_sums[w];
-  }
-  *total = sum;
-  return before + inc - x;
-}
-
 template <int D, bool FP8, int MT>
 __global__ void __launch_bounds__(kThreads, 1)
     k_attend_rows(const RowsArgs a) {
@@ -281,15 +98,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* q_empty = q_full + 2;                               // [2] queries read
   uint64_t* joined = q_empty + 2;                               // [2] states written / read
   int* abort = reinterpret_cast<int*>(joined + 2);
-  __shared__ int64_t sh_scan[kThreads / 32];
-  __shared__ int64_t sh_b0;
-  __shared__ int sh_row, sh_n_none;
-  int* sh_none = reinterpret_cast<int*>(merge);   // before the first row is joined
   int* err = a.status ? a.status : &g_no_status;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int n_heads = a.Hkv * a.n_mb;
-  const int grid = gridDim.x, cta = blockIdx.x;
+  const int cta = blockIdx.x;
 
   if (tid == 0) {
     for (int i = 0; i < S; ++i) {
@@ -303,88 +116,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&joined[0], kWarps);
     mbar_init(&joined[1], kWarps);
     *abort = 0;
-    sh_n_none = 0;
     fence_mbar_init();
   }
 
-  // ---------------------------------------------------- this CTA's share
   Walk w;
-  w.grid = grid;
-  w.it = cta;
-  w.n_whole = 0;
-  w.by_head = a.ids != nullptr;
-  w.nt_ids = a.nt_ids;
-  w.n_heads = n_heads;
-  int64_t total;
-  if (a.ids) {
-    const int64_t items = static_cast<int64_t>(a.R) * n_heads;
-    w.n_whole = static_cast<int>(items / grid) * grid;
-    total = (items - w.n_whole) * w.nt_ids;
-    w.b = total * cta / grid;
-    w.b1 = total * (cta + 1) / grid;
-  } else {
-    // the number of tiles, then the row where this CTA's share begins (a
-    // second pass over the lengths where there are more rows than threads)
-    int64_t mine = tid < a.R ? tiles_of(a, tid) : 0, before;
-    before = block_scan(mine, &total, sh_scan);
-    for (int r0 = kThreads; r0 < a.R; r0 += kThreads) {
-      int64_t sum;
-      block_scan(r0 + tid < a.R ? tiles_of(a, r0 + tid) : 0, &sum, sh_scan);
-      total += sum;
-    }
-    total *= n_heads;
-    w.b = total * cta / grid;
-    w.b1 = total * (cta + 1) / grid;
-    int64_t seen = 0;
-    for (int r0 = 0; r0 < a.R; r0 += kThreads) {
-      int64_t sum = 0;
-      const int r = r0 + tid;
-      if (r0 > 0) {
-        mine = r < a.R ? tiles_of(a, r) : 0;
-        before = block_scan(mine, &sum, sh_scan);
-      } else if (a.R > kThreads) {
-        block_scan(mine, &sum, sh_scan);
-      }
-      const int64_t n = mine * n_heads, p = seen + before * n_heads;
-      if (n > 0 && p <= w.b && w.b < p + n) {
-        sh_row = r;
-        sh_b0 = p;
-      }
-      seen += sum * n_heads;
-      // rows that see nothing: zeros, and the log of an empty sum
-      if (r < a.R && mine == 0 && r % grid == cta) {
-        sh_none[atomicAdd(&sh_n_none, 1)] = r;
-        const int s = seq_of(a, r);
-        if (s < 0 || s >= a.n_seqs) atomicOr(err, AI_DEVFLAG_RANGE);
-      }
-      __syncthreads();
-      for (int i = 0; i < sh_n_none; ++i) {
-        const int64_t at = static_cast<int64_t>(sh_none[i]) * a.Hq;
-        for (int j = tid; j < a.Hq * D / 8; j += kThreads)
-          reinterpret_cast<uint4*>(a.out + at * D)[j] = make_uint4(0, 0, 0, 0);
-        if (a.lse)
-          for (int j = tid; j < a.Hq; j += kThreads) a.lse[at + j] = -INFINITY;
-      }
-      __syncthreads();
-      if (tid == 0) sh_n_none = 0;
-    }
-  }
-  __syncthreads();
-  if (w.b < w.b1) {
-    if (a.ids) {
-      const int64_t item = w.n_whole + w.b / w.nt_ids;
-      w.head = static_cast<int>(item / a.R);
-      w.row = static_cast<int>(item % a.R);
-      w.tile = static_cast<int>(w.b % w.nt_ids);
-      w.n_tiles = w.nt_ids;
-    } else {
-      const int start = static_cast<int>(w.b - sh_b0);   // within the row's tiles of all heads
-      w.row = sh_row;
-      w.n_tiles = tiles_of(a, w.row);
-      w.head = start / w.n_tiles;
-      w.tile = start % w.n_tiles;
-    }
-  }
+  begin_walk<kThreads, D>(a, reinterpret_cast<int*>(merge) /* before the first row is joined */, err, &w);
   Share x;
 
   if (warp >= kWarps) {
@@ -871,10 +607,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
+// Head rows of a partial result, padded to the kernels' tiles.
+int rows_per_slot(int mb_rows) { return mb_rows <= kFewHeads ? 8 : (mb_rows <= 16 ? 16 : (mb_rows <= 32 ? 32 : 64)); }
+
 // Joins the parts of a row that begins in CTA blockIdx.x and goes on in the
 // following ones; blockIdx.y is the row within the block of query heads.
 template <int D>
-__global__ void __launch_bounds__(D) k_join_rows(const RowsArgs a, int n_ctas, int rows_per_slot) {
+__global__ void __launch_bounds__(D) k_join_rows(const RowsArgs a, int n_ctas, int slot_rows) {
   const int c = blockIdx.x, r = blockIdx.y, d = threadIdx.x;
   const int item = a.meta[c * 4 + 2];
   if (item < 0) return;
@@ -883,12 +622,12 @@ __global__ void __launch_bounds__(D) k_join_rows(const RowsArgs a, int n_ctas, i
   const int h = head / a.n_mb;
   const int h0 = h * a.G + (head % a.n_mb) * a.mb_rows;
   if (r >= min(a.mb_rows, (h + 1) * a.G - h0)) return;
-  const float* p = a.part + (static_cast<int64_t>(c * 2 + 1) * rows_per_slot + r) * (D + 4);
+  const float* p = a.part + (static_cast<int64_t>(c * 2 + 1) * slot_rows + r) * (D + 4);
   float m = p[D], l = p[D + 1], o = p[d];
   for (int n = c + 1; n < n_ctas; ++n) {
     if (a.meta[n * 4] < 0) continue;  // a CTA without a share
     const bool ends = a.meta[n * 4 + 1] != 0;
-    const float* q = a.part + (static_cast<int64_t>(n * 2) * rows_per_slot + r) * (D + 4);
+    const float* q = a.part + (static_cast<int64_t>(n * 2) * slot_rows + r) * (D + 4);
     const float mn = fmaxf(m, q[D]);
     const float mz = mn == -INFINITY ? 0.f : mn;
     const float f0 = exp2_approx(m - mz), f1 = exp2_approx(q[D] - mz);
@@ -910,18 +649,20 @@ cudaError_t launch_mt(const RowsArgs& a, int grid, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   count_launch();
   k_attend_rows<D, FP8, MT><<<grid, kThreads, L::kBytes, st>>>(a);
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  count_launch();
-  k_join_rows<D><<<dim3(grid, a.mb_rows), D, 0, st>>>(a, grid, 16 * MT);
   return cudaGetLastError();
 }
 
 template <int D, bool FP8>
 cudaError_t launch_d(const RowsArgs& a, int grid, cudaStream_t st) {
-  if (a.mb_rows <= 16) return launch_mt<D, FP8, 1>(a, grid, st);
-  if (a.mb_rows <= 32) return launch_mt<D, FP8, 2>(a, grid, st);
-  return launch_mt<D, FP8, 4>(a, grid, st);
+  cudaError_t e;
+  if (a.mb_rows <= kFewHeads) e = launch_rows_few(a, D, FP8, grid, st);
+  else if (a.mb_rows <= 16) e = launch_mt<D, FP8, 1>(a, grid, st);
+  else if (a.mb_rows <= 32) e = launch_mt<D, FP8, 2>(a, grid, st);
+  else e = launch_mt<D, FP8, 4>(a, grid, st);
+  if (e != cudaSuccess) return e;
+  count_launch();
+  k_join_rows<D><<<dim3(grid, a.mb_rows), D, 0, st>>>(a, grid, rows_per_slot(a.mb_rows));
+  return cudaGetLastError();
 }
 
 int fail(int code, const char* msg) {
@@ -942,10 +683,8 @@ int max_grid() { return num_sms(); }
 int64_t workspace_for(int Hq, int Hkv, int D) {
   const int G = Hq / Hkv;
   const int mb = (G + 63) / 64;
-  const int rows = ((G + mb - 1) / mb + 15) / 16 * 16;
-  const int padded = rows <= 16 ? 16 : (rows <= 32 ? 32 : 64);
   const int64_t g = max_grid();
-  return g * 16 + g * 2 * padded * (D + 4) * 4;
+  return g * 16 + g * 2 * rows_per_slot((G + mb - 1) / mb) * (D + 4) * 4;
 }
 
 int run_rows(const ai_cache* c, int32_t layer, const void* q, int32_t R, int32_t Hq, const int32_t* ids, int32_t n_ids,
@@ -997,7 +736,7 @@ int run_rows(const ai_cache* c, int32_t layer, const void* q, int32_t R, int32_t
   while ((int64_t(1) << s) < c->page_size) ++s;
   a.page_shift = 31 + s;
   a.page_mul = ((uint64_t(1) << a.page_shift) + c->page_size - 1) / c->page_size;
-  a.tile = c->head_dim * es >= 256 ? 64 : 128;  // Layout::kTile
+  a.tile = a.mb_rows <= kFewHeads ? rows_few_tile() : (c->head_dim * es >= 256 ? 64 : 128);  // Layout::kTile
   a.nt_ids = (n_ids + a.tile - 1) / a.tile;
   a.c2 = scale * kLog2e;
   a.out = static_cast<uint16_t*>(out);
