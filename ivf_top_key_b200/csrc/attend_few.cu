@@ -30,13 +30,13 @@ struct Few {
   static constexpr int kLine = kRow < 128 ? kRow : 128; // bytes of it that lie together
   static constexpr int kKV = kTile * kRow;
   // sixteen warps at most: 128 registers each
-  static constexpr int kComp = kRow > 128 ? 8 : 10;
-  static constexpr int kCopiers = kRow > 128 ? 4 : 5;
-  static constexpr int kJoiners = kRow > 128 ? 2 : 1;
+  static constexpr int kComp = kRow > 64 ? 8 : 10;
+  static constexpr int kCopiers = kRow > 64 ? 4 : 5;
+  static constexpr int kJoiners = kRow > 64 ? 2 : 1;
   static constexpr int kThreads = (kComp + kCopiers + kJoiners) * 32;
   // a multiple of both, so that a stage is always the same two warps': each
   // waits for every phase of its barriers in turn
-  static constexpr int kStages = kRow > 128 ? 8 : (kRow > 64 ? 10 : 20);
+  static constexpr int kStages = kRow > 128 ? 8 : (kRow > 64 ? 16 : 20);
   static_assert(kStages % kComp == 0 && kStages % kCopiers == 0, "stages");
   static constexpr int kScales = FP8 ? 2 * kTile * 4 : 0;
   static constexpr int kState = D + 4;                  // floats: output, maximum, sum
@@ -388,8 +388,9 @@ __global__ void __launch_bounds__(Few<D, FP8>::kThreads, 1) k_attend_few(const R
                 for (int j = 0; j < 2; ++j) {
                   const uint32_t lo = reinterpret_cast<const uint32_t*>(&u[j][0])[i];
                   const uint32_t hi = reinterpret_cast<const uint32_t*>(&u[j][1])[i];
-                  const uint32_t k4[4] = {e4m3x2_to_f16x2(lo & 0xffff), e4m3x2_to_f16x2(hi & 0xffff),
-                                          e4m3x2_to_f16x2(lo >> 16), e4m3x2_to_f16x2(hi >> 16)};
+                  uint32_t k4[4];
+                  e4m3x4_to_f16x4(lo, &k4[0], &k4[2]);
+                  e4m3x4_to_f16x4(hi, &k4[1], &k4[3]);
                   mma<true>(s[j], k4, qf[c4 * 4 + i][0], qf[c4 * 4 + i][1]);
                 }
             }
@@ -503,10 +504,9 @@ __global__ void __launch_bounds__(Few<D, FP8>::kThreads, 1) k_attend_few(const R
                 ldsm4t(b, sv + L::at(j * 16 + vr, cc * 2 + (lane >> 4)));
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                  const uint32_t lo = b[2 * i], hi = b[2 * i + 1];
-                  const uint32_t v4[4] = {
-                      e4m3x2_to_f16x2(__byte_perm(lo, 0, 0x4420)), e4m3x2_to_f16x2(__byte_perm(lo, 0, 0x4431)),
-                      e4m3x2_to_f16x2(__byte_perm(hi, 0, 0x4420)), e4m3x2_to_f16x2(__byte_perm(hi, 0, 0x4431))};
+                  uint32_t v4[4];
+                  e4m3x4_to_f16x4(__byte_perm(b[2 * i], 0, 0x3120), &v4[0], &v4[1]);
+                  e4m3x4_to_f16x4(__byte_perm(b[2 * i + 1], 0, 0x3120), &v4[2], &v4[3]);
                   mma<true>(o[cc * 2 + i], v4, p[j][0], p[j][1]);
                 }
               }

@@ -382,8 +382,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                   *reinterpret_cast<const uint4*>(stage + L::at(k0 + j * 8 + L::key(g), c4 * 4 + t));
               const uint32_t u[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
-                mma<true>(s[j], qf[c4 * 4 + i], e4m3x2_to_f16x2(u[i] & 0xffff), e4m3x2_to_f16x2(u[i] >> 16));
+              for (int i = 0; i < 4; ++i) {
+                uint32_t b0, b1;
+                e4m3x4_to_f16x4(u[i], &b0, &b1);
+                mma<true>(s[j], qf[c4 * 4 + i], b0, b1);
+              }
             }
           }
         }
@@ -501,11 +504,11 @@ __global__ void __launch_bounds__(kThreads, 1)
               ldsm4t(b, sv + L::at(vr + j * 16, cc * 2 + (lane >> 4)));
 #pragma unroll
               for (int i = 0; i < 2; ++i) {
-                const uint32_t lo = b[2 * i], hi = b[2 * i + 1];
-                mma<true>(o[(cc * 2 + i) * 2], p[j], e4m3x2_to_f16x2(__byte_perm(lo, 0, 0x4420)),
-                          e4m3x2_to_f16x2(__byte_perm(hi, 0, 0x4420)));
-                mma<true>(o[(cc * 2 + i) * 2 + 1], p[j], e4m3x2_to_f16x2(__byte_perm(lo, 0, 0x4431)),
-                          e4m3x2_to_f16x2(__byte_perm(hi, 0, 0x4431)));
+                uint32_t even[2], odd[2];   // by key half
+                e4m3x4_to_f16x4(__byte_perm(b[2 * i], 0, 0x3120), &even[0], &odd[0]);
+                e4m3x4_to_f16x4(__byte_perm(b[2 * i + 1], 0, 0x3120), &even[1], &odd[1]);
+                mma<true>(o[(cc * 2 + i) * 2], p[j], even[0], even[1]);
+                mma<true>(o[(cc * 2 + i) * 2 + 1], p[j], odd[0], odd[1]);
               }
             }
           }

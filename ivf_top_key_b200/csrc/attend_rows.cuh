@@ -72,10 +72,11 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
-// Two e4m3 codes (low byte first) to two f16 values, exactly.
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t codes) {
-  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(codes), __NV_E4M3);
-  return static_cast<uint32_t>(h.x) | (static_cast<uint32_t>(h.y) << 16);
+// Four e4m3 codes (low byte first) to two pairs of f16 values, exactly.
+__device__ __forceinline__ void e4m3x4_to_f16x4(uint32_t codes, uint32_t* lo, uint32_t* hi) {
+  asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.rn.f16x2.e4m3x2 %0, a;\n cvt.rn.f16x2.e4m3x2 %1, b;\n}"
+      : "=r"(*lo), "=r"(*hi)
+      : "r"(codes));
 }
 __device__ __forceinline__ float exp2_approx(float x) {
   float y;
