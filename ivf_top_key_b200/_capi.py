@@ -314,13 +314,15 @@ def ai_refine_kernel_choice(h, C: int) -> int:
     return v.value
 
 
+_Pair = ctypes.c_int64 * 2
+
+
 # ---- attention over the keys; tensors are passed as addresses (ints or
 # None) because the callers below check them and strides go separately
 
 def ai_attend_prompt(q, q_strides, k, k_strides, v, v_strides, cu_q, cu_k, n_seqs: int, total_q: int, total_k: int,
                      n_heads: int, n_kv_heads: int, head_dim: int, scale: float, out, lse, status, stream: int):
-    pair = ctypes.c_int64 * 2
-    _check(_lib.ai_attend_prompt(q, pair(*q_strides), k, pair(*k_strides), v, pair(*v_strides), cu_q, cu_k, n_seqs,
+    _check(_lib.ai_attend_prompt(q, _Pair(*q_strides), k, _Pair(*k_strides), v, _Pair(*v_strides), cu_q, cu_k, n_seqs,
                                  total_q, total_k, n_heads, n_kv_heads, head_dim, scale, out, lse, status, stream))
 
 

@@ -15,12 +15,14 @@ tensors' device; by default the current one of that device.
 from __future__ import annotations
 
 import contextlib
+import functools
 
 import torch
 
 from . import _capi as C
 
 _INT, _BF16, _F32 = torch.int32, torch.bfloat16, torch.float32
+_CODES = (torch.uint8, torch.float8_e4m3fn)
 
 
 def _need(ok: bool, what: str):
@@ -29,12 +31,11 @@ def _need(ok: bool, what: str):
 
 
 def _dense(t: torch.Tensor, dtype, device, what: str, shape=None):
-    _need(t.dtype == dtype, f"{what} must be {dtype}")
-    _need(t.device == device, f"{what} must be on {device}")
-    _need(t.is_contiguous(), f"{what} must be contiguous")
-    if shape is not None:
-        _need(t.shape == shape, f"{what} must have shape {tuple(shape)}")
-    return t.data_ptr()
+    """The address of a tensor that has to be dense, of this type and shape, and on this device."""
+    if t.dtype is dtype and t.device == device and t.is_contiguous() and (shape is None or t.shape == shape):
+        return t.data_ptr()
+    raise ValueError(f"{what} must be a contiguous {dtype} tensor on {device}"
+                     + ("" if shape is None else f" of shape {tuple(shape)}"))
 
 
 @contextlib.contextmanager
@@ -43,15 +44,21 @@ def _entered(device: torch.device, stream):
         yield
 
 
+_HERE = contextlib.nullcontext()
+
+
 def _on(device: torch.device, stream):
     """Context in which the call's memory belongs to its stream, and that stream's handle."""
     if stream is None:
-        s = torch.cuda.current_stream(device)
-        if device.index == torch.cuda.current_device():
-            return contextlib.nullcontext(), s.cuda_stream
-        return torch.cuda.device(device), s.cuda_stream
-    _need(stream.device == device, f"the stream must be on {device}")
+        s = torch._C._cuda_getCurrentRawStream(device.index)
+        return (_HERE if device.index == torch._C._cuda_getDevice() else torch.cuda.device(device)), s
+    _need(stream.device == device, "the stream must be on the tensors' device")
     return _entered(device, stream), stream.cuda_stream
+
+
+@functools.lru_cache(maxsize=None)
+def _attend_workspace(device: int, n_heads: int, n_kv_heads: int, head_dim: int) -> int:
+    return C.ai_attend_workspace(n_heads, n_kv_heads, head_dim)
 
 
 def _gpu(t: torch.Tensor, what: str) -> torch.device:
@@ -59,33 +66,28 @@ def _gpu(t: torch.Tensor, what: str) -> torch.device:
     return t.device
 
 
-def _view(k, v, tables, lens, refs=None, k_scale=None, v_scale=None, status=None, pages: bool = True):
-    """The ai_cache of these tensors and the number of its layers' leading dimensions."""
+def _view(k, v, tables, lens, refs=None, k_scale=None, v_scale=None, status=None):
+    """The ai_cache of these tensors, and their device."""
     dev = _gpu(tables, "tables")
-    c = C.AiCache()
     _need(tables.dim() == 2, "tables must be [n_seqs, max_pages]")
-    c.tables = _dense(tables, _INT, dev, "tables")
-    c.n_seqs, c.max_pages = tables.shape
-    c.lens = _dense(lens, _INT, dev, "lens", tables.shape[:1])
-    if pages:
-        _need(k.dim() in (4, 5), "k must be [n_layers, n_pages, page_size, n_kv_heads, head_dim] or one layer of it")
-        _need(k.dtype in (_BF16, torch.uint8, torch.float8_e4m3fn), "the cache holds bfloat16, or e4m3 codes")
-        fp8 = k.dtype != _BF16
-        c.k = _dense(k, k.dtype, dev, "k")
-        c.v = _dense(v, k.dtype, dev, "v", k.shape)
-        c.n_layers = k.shape[0] if k.dim() == 5 else 1
-        c.n_pages, c.page_size, c.n_kv_heads, c.head_dim = k.shape[-4:]
-        c.dtype = C.AI_FP8E4M3 if fp8 else C.AI_BF16
-        _need(fp8 == (k_scale is not None) and fp8 == (v_scale is not None),
-              "k_scale and v_scale go with e4m3 codes, and only with them")
-        if fp8:
-            c.k_scale = _dense(k_scale, _F32, dev, "k_scale", k.shape[:-1])
-            c.v_scale = _dense(v_scale, _F32, dev, "v_scale", k.shape[:-1])
-        if refs is not None:
-            c.refs = _dense(refs, _INT, dev, "refs", (c.n_pages,))
-    if status is not None:
-        c.status = _dense(status, _INT, dev, "status", (1,))
-    return c, dev
+    shape = k.shape
+    _need(len(shape) in (4, 5), "k must be [n_layers, n_pages, page_size, n_kv_heads, head_dim] or one layer of it")
+    kind = k.dtype
+    fp8 = kind is not _BF16
+    _need(not fp8 or kind in _CODES, "the cache holds bfloat16, or e4m3 codes")
+    _need(fp8 == (k_scale is not None) and fp8 == (v_scale is not None),
+          "k_scale and v_scale go with e4m3 codes, and only with them")
+    n_seqs, width = tables.shape
+    n_pages, page, heads, D = shape[-4:]
+    return C.AiCache(
+        _dense(k, kind, dev, "k"), _dense(v, kind, dev, "v", shape),
+        _dense(k_scale, _F32, dev, "k_scale", shape[:-1]) if fp8 else None,
+        _dense(v_scale, _F32, dev, "v_scale", shape[:-1]) if fp8 else None,
+        _dense(tables, _INT, dev, "tables"), _dense(lens, _INT, dev, "lens", (n_seqs,)),
+        None if refs is None else _dense(refs, _INT, dev, "refs", (n_pages,)),
+        None if status is None else _dense(status, _INT, dev, "status", (1,)),
+        C.AI_FP8E4M3 if fp8 else C.AI_BF16, shape[0] if len(shape) == 5 else 1, n_pages, page, heads, D, n_seqs,
+        width), dev
 
 
 def _list(t, dev, what: str, n=None):
@@ -104,11 +106,9 @@ def attend_prompt(q, k, v, cu_q, cu_k=None, *, scale=None, out=None, out_lse=Non
     Returns out [total_q, Hq, D]; out_lse: None or float32 [total_q, Hq]."""
     dev = _gpu(q, "q")
     cu_k = cu_q if cu_k is None else cu_k
-    for t, what in ((q, "q"), (k, "k"), (v, "v")):
-        _need(t.dim() == 3, f"{what} must be [tokens, heads, head_dim]")
-        _need(t.dtype == _BF16, f"{what} must be torch.bfloat16")
-        _need(t.device == dev, f"{what} must be on {dev}")
-        _need(t.stride(2) == 1 or t.shape[2] == 1, f"the last dimension of {what} must be dense")
+    for t in (q, k, v):
+        if t.dim() != 3 or t.dtype is not _BF16 or t.device != dev or (t.stride(2) != 1 and t.shape[2] != 1):
+            raise ValueError(f"q, k and v must be torch.bfloat16 [tokens, heads, head_dim] on {dev}, the last dimension dense")
     _need(v.shape == k.shape and k.shape[2] == q.shape[2], "k and v must be [total_k, n_kv_heads, head_dim of q]")
     _need(cu_q.dim() == 1 and cu_q.shape[0] >= 1, "cu_q must be [n_seqs + 1]")
     pq, pk = _dense(cu_q, _INT, dev, "cu_q"), _dense(cu_k, _INT, dev, "cu_k", cu_q.shape)
@@ -141,7 +141,7 @@ def _rows(q, ids, cache, dev, seqs, layer, scale, out, out_lse, stream):
             out = torch.empty((T, Hq, D), dtype=_BF16, device=dev)
         po = _dense(out, _BF16, dev, "out", (T, Hq, D))
         pl = None if out_lse is None else _dense(out_lse, _F32, dev, "out_lse", (T, Hq))
-        n = C.ai_attend_workspace(Hq, cache.n_kv_heads, D)
+        n = _attend_workspace(dev.index, Hq, cache.n_kv_heads, D)
         ws = torch.empty(n, dtype=torch.uint8, device=dev)
         if ids is None:
             C.ai_attend_cached(cache, layer, pq, T, Hq, ps, scale, po, pl, ws.data_ptr(), n, st)
@@ -216,9 +216,12 @@ def cache_fork(k, v, tables, lens, refs, src, dst, *, k_scale=None, v_scale=None
 
 def cache_free(tables, lens, refs, seqs, *, page_size: int, status=None, stream=None):
     """Release sequences (ai_cache_free)."""
-    c, dev = _view(None, None, tables, lens, status=status, pages=False)
-    _need(refs.dim() == 1, "refs must be [n_pages]")
-    c.refs, c.n_pages, c.page_size = _dense(refs, _INT, dev, "refs"), refs.shape[0], page_size
+    dev = _gpu(tables, "tables")
+    _need(tables.dim() == 2 and refs.dim() == 1, "tables must be [n_seqs, max_pages], refs [n_pages]")
+    c = C.AiCache(None, None, None, None, _dense(tables, _INT, dev, "tables"),
+                  _dense(lens, _INT, dev, "lens", tables.shape[:1]), _dense(refs, _INT, dev, "refs"),
+                  None if status is None else _dense(status, _INT, dev, "status", (1,)),
+                  0, 0, refs.shape[0], page_size, 0, 0, *tables.shape)
     ps = _list(seqs, dev, "seqs")
     ctx, st = _on(dev, stream)
     with ctx:

@@ -97,6 +97,8 @@ __global__ void __launch_bounds__(Few<D, FP8>::kThreads, 1) k_attend_few(const R
   }
   Walk w;
   begin_walk<L::kThreads, D>(a, reinterpret_cast<int*>(states) /* before the first state */, err, &w);
+  // the joining kernel may be set up now; it waits for this one to end
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   Share x;
 
   if (warp >= kComp + kCopiers) {
@@ -556,7 +558,8 @@ __global__ void __launch_bounds__(Few<D, FP8>::kThreads, 1) k_attend_few(const R
 template <int D, bool FP8>
 cudaError_t launch_few(const RowsArgs& a, int grid, cudaStream_t st) {
   using L = Few<D, FP8>;
-  const cudaError_t e = cudaFuncSetAttribute(k_attend_few<D, FP8>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes);
+  static ReadyOnce ready;
+  const cudaError_t e = ready.shared_memory(k_attend_few<D, FP8>, L::kBytes);
   if (e != cudaSuccess) return e;
   count_launch();
   k_attend_few<D, FP8><<<grid, L::kThreads, L::kBytes, st>>>(a);

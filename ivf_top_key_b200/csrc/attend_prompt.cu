@@ -637,11 +637,9 @@ bool map_rows(CUtensorMap* m, const void* p, int64_t tokens, int heads, int D, i
 template <int D>
 cudaError_t launch_prompt(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const PromptArgs& a,
                           const Schedule& sc, cudaStream_t st) {
-  int dev = 0, sms = 148;
-  cudaGetDevice(&dev);
-  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  const cudaError_t e =
-      cudaFuncSetAttribute(k_prompt_tc<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::kBytes);
+  const int sms = device_sms();
+  static ReadyOnce ready;
+  const cudaError_t e = ready.shared_memory(k_prompt_tc<D>, Smem<D>::kBytes);
   if (e != cudaSuccess) return e;
   count_launch();
   k_prompt_tc<D><<<static_cast<int>(sc.n_items < sms ? sc.n_items : sms), kThreads, Smem<D>::kBytes, st>>>(mq, mk, mv,

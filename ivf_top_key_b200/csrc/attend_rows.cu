@@ -121,6 +121,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   Walk w;
   begin_walk<kThreads, D>(a, reinterpret_cast<int*>(merge) /* before the first row is joined */, err, &w);
+  // the joining kernel may be set up now; it waits for this one to end
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   Share x;
 
   if (warp >= kWarps) {
@@ -614,10 +616,18 @@ __global__ void __launch_bounds__(kThreads, 1)
 int rows_per_slot(int mb_rows) { return mb_rows <= kFewHeads ? 8 : (mb_rows <= 16 ? 16 : (mb_rows <= 32 ? 32 : 64)); }
 
 // Joins the parts of a row that begins in CTA blockIdx.x and goes on in the
-// following ones; blockIdx.y is the row within the block of query heads.
+// following ones; blockIdx.y is the row within the block of query heads.  A
+// thread takes a part's maximum and sum, then a column: what is read in turn
+// is read by many at once (one part after another took 0.4 us each).
+// Launched to start while the partial kernel ends (programmatic dependence):
+// it waits for it before it reads.
+constexpr int kJoin = 128;
 template <int D>
-__global__ void __launch_bounds__(D) k_join_rows(const RowsArgs a, int n_ctas, int slot_rows) {
-  const int c = blockIdx.x, r = blockIdx.y, d = threadIdx.x;
+__global__ void __launch_bounds__(kJoin) k_join_rows(const RowsArgs a, int n_ctas, int slot_rows) {
+  __shared__ float sh_w[kJoin], sh_red[kJoin / 32], sh_o[kJoin];
+  __shared__ int sh_end;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int c = blockIdx.x, r = blockIdx.y, tid = threadIdx.x;
   const int item = a.meta[c * 4 + 2];
   if (item < 0) return;
   const int n_heads = a.Hkv * a.n_mb;
@@ -625,19 +635,65 @@ __global__ void __launch_bounds__(D) k_join_rows(const RowsArgs a, int n_ctas, i
   const int h = head / a.n_mb;
   const int h0 = h * a.G + (head % a.n_mb) * a.mb_rows;
   if (r >= min(a.mb_rows, (h + 1) * a.G - h0)) return;
-  const float* p = a.part + (static_cast<int64_t>(c * 2 + 1) * slot_rows + r) * (D + 4);
-  float m = p[D], l = p[D + 1], o = p[d];
-  for (int n = c + 1; n < n_ctas; ++n) {
-    if (a.meta[n * 4] < 0) continue;  // a CTA without a share
-    const bool ends = a.meta[n * 4 + 1] != 0;
-    const float* q = a.part + (static_cast<int64_t>(n * 2) * slot_rows + r) * (D + 4);
-    const float mn = fmaxf(m, q[D]);
+  auto part = [&](int n) {   // of CTA n; the row's first part is its CTA's second slot
+    return a.part + (static_cast<int64_t>(n * 2 + (n == c)) * slot_rows + r) * (D + 4);
+  };
+  constexpr int kCols = kJoin / D;     // threads per column: parts n0 + tid / D, + kCols, ..
+  const int d = tid % D, sub = tid / D;
+  float m = -INFINITY, l = 0.f, o = 0.f;
+  for (int n0 = c, end = n_ctas; n0 < end; n0 += kJoin) {
+    // up to kJoin parts: CTAs n0 .. ; the row ends in the first that says so
+    const int n = n0 + tid;
+    float pm = -INFINITY, pl = 0.f;
+    if (tid == 0) sh_end = n_ctas;
+    __syncthreads();
+    if (n < n_ctas) {
+      const int2 x = *reinterpret_cast<const int2*>(a.meta + n * 4);
+      if (n == c || x.x == item) {     // (a CTA without a share has none)
+        const float2 ml = *reinterpret_cast<const float2*>(part(n) + D);
+        pm = ml.x;
+        pl = ml.y;
+        if (n > c && x.y) atomicMin(&sh_end, n + 1);
+      }
+    }
+    __syncthreads();
+    end = min(end, sh_end);
+    if (n >= end) {
+      pm = -INFINITY;
+      pl = 0.f;
+    }
+    // the new maximum, the parts' weights and their sum
+    float mx = pm;
+    for (int i = 16; i > 0; i >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, i));
+    if ((tid & 31) == 0) sh_red[tid >> 5] = mx;
+    __syncthreads();
+    const float mn = fmaxf(fmaxf(fmaxf(sh_red[0], sh_red[1]), fmaxf(sh_red[2], sh_red[3])), m);
     const float mz = mn == -INFINITY ? 0.f : mn;
-    const float f0 = exp2_approx(m - mz), f1 = exp2_approx(q[D] - mz);
+    const float w = exp2_approx(pm - mz);
+    sh_w[tid] = pl == 0.f ? -1.f : w;  // -1: nothing seen, its output may not be written
+    float sum = pl == 0.f ? 0.f : pl * w;
+    for (int i = 16; i > 0; i >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, i);
+    __syncthreads();
+    if ((tid & 31) == 0) sh_red[tid >> 5] = sum;
+    __syncthreads();
+    const float f = exp2_approx(m - mz);
+    l = l * f + ((sh_red[0] + sh_red[1]) + (sh_red[2] + sh_red[3]));
+    o *= f;
     m = mn;
-    l = l * f0 + q[D + 1] * f1;
-    o = o * f0 + q[d] * f1;
-    if (ends) break;
+    const int count = min(end - n0, kJoin);
+#pragma unroll 8
+    for (int i = sub; i < count; i += kCols) {
+      const float wi = sh_w[i];
+      if (!(wi < 0.f)) o = fmaf(part(n0 + i)[d], wi, o);
+    }
+    __syncthreads();
+  }
+  if constexpr (kCols > 1) {
+    sh_o[tid] = o;
+    __syncthreads();
+    if (sub > 0) return;
+#pragma unroll
+    for (int i = 1; i < kCols; ++i) o += sh_o[i * D + d];
   }
   const __nv_bfloat16 b = __float2bfloat16_rn(l == 0.f ? 0.f : o / l);
   a.out[(static_cast<int64_t>(row) * a.Hq + h0 + r) * D + d] = *reinterpret_cast<const uint16_t*>(&b);
@@ -648,7 +704,8 @@ __global__ void __launch_bounds__(D) k_join_rows(const RowsArgs a, int n_ctas, i
 template <int D, bool FP8, int MT>
 cudaError_t launch_mt(const RowsArgs& a, int grid, cudaStream_t st) {
   using L = Layout<D, FP8, MT>;
-  cudaError_t e = cudaFuncSetAttribute(k_attend_rows<D, FP8, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes);
+  static ReadyOnce ready;
+  const cudaError_t e = ready.shared_memory(k_attend_rows<D, FP8, MT>, L::kBytes);
   if (e != cudaSuccess) return e;
   count_launch();
   k_attend_rows<D, FP8, MT><<<grid, kThreads, L::kBytes, st>>>(a);
@@ -663,9 +720,17 @@ cudaError_t launch_d(const RowsArgs& a, int grid, cudaStream_t st) {
   else if (a.mb_rows <= 32) e = launch_mt<D, FP8, 2>(a, grid, st);
   else e = launch_mt<D, FP8, 4>(a, grid, st);
   if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid, a.mb_rows);
+  cfg.blockDim = dim3(kJoin);
+  cfg.stream = st;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
   count_launch();
-  k_join_rows<D><<<dim3(grid, a.mb_rows), D, 0, st>>>(a, grid, rows_per_slot(a.mb_rows));
-  return cudaGetLastError();
+  return cudaLaunchKernelEx(&cfg, k_join_rows<D>, a, grid, rows_per_slot(a.mb_rows));
 }
 
 int fail(int code, const char* msg) {
@@ -673,15 +738,8 @@ int fail(int code, const char* msg) {
   return code;
 }
 
-int num_sms() {
-  int dev = 0, sms = 148;
-  cudaGetDevice(&dev);
-  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  return sms;
-}
-
 // The largest grid (partial results are sized for it).
-int max_grid() { return num_sms(); }
+int max_grid() { return device_sms(); }
 
 int64_t workspace_for(int Hq, int Hkv, int D) {
   const int G = Hq / Hkv;

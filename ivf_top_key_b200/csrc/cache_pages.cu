@@ -438,13 +438,6 @@ View view_of(const ai_cache* c) {
   return v;
 }
 
-int num_sms() {
-  int dev = 0, sms = 148;
-  cudaGetDevice(&dev);
-  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  return sms;
-}
-
 int launched() {
   const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? AI_OK : fail(AI_ERR_CUDA, cudaGetErrorString(e));
@@ -469,6 +462,28 @@ int check_list(const ai_cache* c, const void* list, int32_t n) {
 }
 
 }  // namespace
+
+int device_sms() {
+  static std::atomic<int> known[kMaxDevices] = {};
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 148;
+  sms = known[dev].load(std::memory_order_relaxed);
+  if (sms == 0) {
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0) return 148;
+    known[dev].store(sms, std::memory_order_relaxed);
+  }
+  return sms;
+}
+
+cudaError_t ReadyOnce::allow(const void* kernel, int bytes) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 0 && dev < kMaxDevices && done[dev].load(std::memory_order_acquire)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && dev >= 0 && dev < kMaxDevices) done[dev].store(true, std::memory_order_release);
+  return e;
+}
 
 int check_cache(const ai_cache* c) {
   const int rc = check_tables(c);
@@ -595,6 +610,6 @@ extern "C" int ai_cache_compact(const ai_cache* c, void* workspace_dev, int64_t 
   count_launch();
   k_compact_plan<<<1, kPlan, 0, st>>>(v, map, from, to, count);
   count_launch();
-  k_compact_move<<<8 * num_sms(), 256, 0, st>>>(v, map, from, to, count);
+  k_compact_move<<<8 * device_sms(), 256, 0, st>>>(v, map, from, to, count);
   return launched();
 }

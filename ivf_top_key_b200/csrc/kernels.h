@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 struct ai_cache;  // include/ai_index.h
 
 namespace aiidx {
@@ -235,6 +237,17 @@ cudaError_t launch_quantize_fp8(const uint16_t* keys_bf16, int64_t n, int d, uin
                                 float* scales, cudaStream_t st);
 cudaError_t launch_fp8_codes_to_bf16(const uint8_t* codes, int64_t n, int d, uint16_t* out,
                                      cudaStream_t st);
+
+// ------------------------------------------------------------- per device
+constexpr int kMaxDevices = 128;
+int device_sms();   // of the current device (looked up once)
+// A kernel's shared-memory limit, raised once per device.
+struct ReadyOnce {
+  std::atomic<bool> done[kMaxDevices] = {};
+  template <typename K>
+  cudaError_t shared_memory(K* kernel, int bytes) { return allow(reinterpret_cast<const void*>(kernel), bytes); }
+  cudaError_t allow(const void* kernel, int bytes);
+};
 
 // ------------------------------------------------------ paged cache checks
 // AI_OK, or AI_ERR_ARG with a message: null or misaligned arrays, sizes out
