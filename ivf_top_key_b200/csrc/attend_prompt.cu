@@ -2,7 +2,10 @@
 //
 //   o_i = sum_{j <= i + Lk - Lq} e^(s_ij - m_i) v_j / sum_j e^(s_ij - m_i)
 //
-// One persistent CTA per SM.  A work item is one key head and a block of
+// One CTA per SM at a time, which takes over the work of CTAs that have not
+// started (cluster launch control), the longest rows first: dealt out in turn
+// instead, the CTA with most to do had 18 to 54 % more than the mean.  A work
+// item is one key head and a block of
 // consecutive queries of one sequence; the G query heads of the key head and
 // the block's tokens are the rows of two 128-row tiles (row = token * G +
 // head), so a short prompt fills a tile with its heads and every key tile is
@@ -124,9 +127,9 @@ struct Smem {
   static constexpr int kHalves = D / 64;          // 64-element (128-byte) column blocks
   static constexpr int kTileBytes = kTile * D * 2;
   static constexpr int kSlots = D == 128 ? 5 : 8; // ring of K and V tiles
-  static constexpr int kBars = 4 + 4 * kSlots + 6;
+  static constexpr int kBars = 4 + 4 * kSlots + 6 + 4;
   static constexpr int kSick = 8;                 // > items that the ring can be ahead
-  static constexpr int kBytes = 1024 + (2 + kSlots) * kTileBytes + kBars * 8 + 8 + kSick * 4;
+  static constexpr int kBytes = 1024 + (2 + kSlots) * kTileBytes + kBars * 8 + 16 + 32 + 8 + kSick * 4;
   static_assert(kBytes <= 227 * 1024, "shared memory");
 };
 
@@ -154,8 +157,8 @@ struct Schedule {
 // sequence has at least as many slots as blocks.
 __device__ Item item_at(const PromptArgs& a, const Schedule& sc, int64_t it) {
   Item x;
-  x.head = static_cast<int>(it / sc.n_slots);
-  const int slot = sc.n_slots - 1 - static_cast<int>(it % sc.n_slots);  // the longest rows first
+  x.head = static_cast<int>(it % a.Hkv);
+  const int slot = sc.n_slots - 1 - static_cast<int>(it / a.Hkv);  // the longest rows first
   int lo = 0, hi = a.n_seqs;
   while (hi - lo > 1) {
     const int mid = (lo + hi) / 2;
@@ -180,10 +183,26 @@ __device__ Item item_at(const PromptArgs& a, const Schedule& sc, int64_t it) {
   return x;
 }
 
-// The r-th item of this CTA; every other round runs backwards, so that costs
-// that fall along the items even out.
-__device__ __forceinline__ int64_t item_of_round(int64_t r) {
-  return r * gridDim.x + ((r & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+// Asks for the work of a CTA that has not started; the answer (16 bytes)
+// completes on the barrier.
+__device__ __forceinline__ void take_request(uint4* answer, uint64_t* bar) {
+  mbar_arrive_expect_tx(bar, 16);
+  asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                   smem_u32(answer)),
+               "r"(smem_u32(bar))
+               : "memory");
+}
+// The item taken over, or -1 where none was left.
+__device__ __forceinline__ int64_t take_answer(const uint4* answer) {
+  uint32_t ok, x;
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b128 h;\n .reg .b32 y, z, w;\n ld.shared.b128 h, [%2];\n mov.u32 %1, 0;\n"
+      " clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n selp.u32 %0, 1, 0, p;\n"
+      " @p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%1, y, z, w}, h;\n}\n"
+      : "=r"(ok), "=r"(x)
+      : "r"(smem_u32(answer))
+      : "memory");
+  return ok ? static_cast<int64_t>(x) : -1;
 }
 
 // Matrix descriptor of an operand that lies N-major (rows of K, 64 elements
@@ -232,6 +251,13 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&b);
 }
 
+// One lane of a converged warp, the same one every time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n selp.u32 %0, 1, 0, q;\n}\n" : "=r"(p));
+  return p != 0;
+}
+
 __device__ int g_no_status;  // where flags go when the caller gives no status word
 
 template <int D>
@@ -254,7 +280,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* s_full = v_clean + kSlots;             // [2] scores in TMEM
   uint64_t* p_full = s_full + 2;                   // [2] weights in TMEM
   uint64_t* o_full = p_full + 2;                   // [2] product with V done
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(o_full + 2);
+  uint64_t* next_full = o_full + 2;                // [2] next item known
+  uint64_t* next_read = next_full + 2;             // [2] and read by every warp
+  uint4* answer = reinterpret_cast<uint4*>((reinterpret_cast<uintptr_t>(next_read + 2) + 15) & ~uintptr_t(15));  // [2]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(answer + 2);
   int* abort = reinterpret_cast<int*>(tmem_slot + 1);
   int* sick = abort + 1;                           // [kSick] by item: its number + 1 where a value is bad
   int* err = a.status ? a.status : &g_no_status;
@@ -267,6 +296,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&s_full[i], 1);
       mbar_init(&p_full[i], 128);
       mbar_init(&o_full[i], 1);
+      mbar_init(&next_full[i], 1);
+      mbar_init(&next_read[i], kThreads / 32);
     }
     for (int s = 0; s < kSlots; ++s) {
       mbar_init(&kv_full[s], 1);
@@ -286,143 +317,184 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  // the item after this warp's r-th; -1: no more
+  auto next_item = [&](uint32_t r) {
+    const uint32_t b = r & 1;
+    if (!__all_sync(0xffffffffu, mbar_wait(&next_full[b], (r >> 1) & 1, err, abort))) return static_cast<int64_t>(-1);
+    const int64_t it = take_answer(&answer[b]);
+    fence_proxy_async_smem();   // before the next answer lands there
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&next_read[b]);
+    return it;
+  };
 
   if (warp == 8) {
     // ---------------------------------------------------------- TMA loads
-    if (lane == 0) {
-      uint32_t g = 0, nq[2] = {0, 0};
-      // by slot: parity of the next phase of its two barriers, and which one
-      // its last load completes on
-      uint32_t kv_next = 0, mx_next = 0, last_mx = 0;
-      bool ok = true;
-      for (int64_t r = 0; ok && item_of_round(r) < sc.n_items; ++r) {
-        const Item x = item_at(a, sc, item_of_round(r));
-        for (int i = 0; ok && i < 2; ++i) {
-          if (x.tiles[i] == 0) continue;
-          if (nq[i] > 0 && !mbar_wait(&q_empty[i], (nq[i] - 1) & 1, err, abort)) {
-            ok = false;
-            break;
-          }
+    const bool leader = elect_one();
+    uint32_t g = 0, nq[2] = {0, 0};
+    // by slot: parity of the next phase of its two barriers, and which one
+    // its last load completes on
+    uint32_t kv_next = 0, mx_next = 0, last_mx = 0;
+    bool ok = true;
+    auto all = [&](bool x) { return __all_sync(0xffffffffu, x); };
+    uint32_t r = 0;
+    for (int64_t it = blockIdx.x; ok && it >= 0; ++r) {
+      // the next item is asked for while this one is loaded
+      if (r >= 2 && !all(mbar_wait(&next_read[r & 1], ((r >> 1) - 1) & 1, err, abort))) break;
+      if (leader) take_request(&answer[r & 1], &next_full[r & 1]);
+      const Item x = item_at(a, sc, it);
+      for (int i = 0; ok && i < 2; ++i) {
+        if (x.tiles[i] == 0) continue;
+        if (nq[i] > 0 && !all(mbar_wait(&q_empty[i], (nq[i] - 1) & 1, err, abort))) {
+          ok = false;
+          break;
+        }
+        if (leader) {
           mbar_arrive_expect_tx(&q_full[i], sc.tpt * a.G * D * 2);
           for (int c = 0; c < L::kHalves; ++c)
             tma_load_3d(sq + i * L::kTileBytes + c * (kTile * 128), &map_q, c * 64, x.head * a.G, x.qtok + i * sc.tpt,
                         &q_full[i]);
-          ++nq[i];
         }
-        const int n = x.n();
-        for (int t = 0; ok && t < 2 * n; ++t, ++g) {  // K 0, V 0, K 1, V 1, ..
-          const int s = g % kSlots;
-          if (g >= kSlots && !mbar_wait(&kv_empty[s], (g / kSlots - 1) & 1, err, abort)) {
-            ok = false;
-            break;
-          }
-          const bool mx = (t & 1) && x.mixed(t >> 1);
-          uint64_t* full = mx ? &mx_full[s] : &kv_full[s];
-          if (mx) {
-            mx_next ^= 1u << s;
-            last_mx |= 1u << s;
-          } else {
-            kv_next ^= 1u << s;
-            last_mx &= ~(1u << s);
-          }
+        ++nq[i];
+      }
+      const int n = x.n();
+      for (int t = 0; ok && t < 2 * n; ++t, ++g) {  // K 0, V 0, K 1, V 1, ..
+        const int s = g % kSlots;
+        if (g >= kSlots && !all(mbar_wait(&kv_empty[s], (g / kSlots - 1) & 1, err, abort))) {
+          ok = false;
+          break;
+        }
+        const bool mx = (t & 1) && x.mixed(t >> 1);
+        uint64_t* full = mx ? &mx_full[s] : &kv_full[s];
+        if (mx) {
+          mx_next ^= 1u << s;
+          last_mx |= 1u << s;
+        } else {
+          kv_next ^= 1u << s;
+          last_mx &= ~(1u << s);
+        }
+        if (leader) {
           mbar_arrive_expect_tx(full, L::kTileBytes);
           for (int c = 0; c < L::kHalves; ++c)
             tma_load_3d(ring + s * L::kTileBytes + c * (kTile * 128), t & 1 ? &map_v : &map_k, c * 64, x.head,
                         x.k0 + (t >> 1) * kTile, full);
         }
       }
-      if (*abort) {  // copies of this thread may still be landing: bounded waits
-        for (uint32_t s = 0; s < min(g, static_cast<uint32_t>(kSlots)); ++s) {
-          const bool mx = (last_mx >> s) & 1;
-          mbar_drain(mx ? &mx_full[s] : &kv_full[s], (((mx ? mx_next : kv_next) >> s) & 1) ^ 1);
-        }
-        for (int i = 0; i < 2; ++i)
-          if (nq[i] > 0) mbar_drain(&q_full[i], (nq[i] - 1) & 1);
-      }
+      if (ok) it = next_item(r);
     }
+    if (*reinterpret_cast<volatile int*>(abort)) {
+      // copies that this warp asked for may still be landing: bounded waits
+      for (uint32_t s = 0; s < min(g, static_cast<uint32_t>(kSlots)); ++s) {
+        const bool mx = (last_mx >> s) & 1;
+        mbar_drain(mx ? &mx_full[s] : &kv_full[s], (((mx ? mx_next : kv_next) >> s) & 1) ^ 1);
+      }
+      for (int i = 0; i < 2; ++i)
+        if (nq[i] > 0) mbar_drain(&q_full[i], (nq[i] - 1) & 1);
+      if (r > 0) mbar_drain(&next_full[(r - 1) & 1], ((r - 1) >> 1) & 1);
+    }
+    __syncwarp();
   } else if (warp == 9) {
     // ----------------------------------------------------------- products
-    if (lane == 0) {
-      constexpr uint32_t id_s = idesc_bf16_f32(kTile, kTile);
-      constexpr uint32_t id_o = idesc_bf16_f32(kTile, D) | (1u << 16);  // B is N-major
-      uint32_t g = 0, nq[2] = {0, 0}, np[2] = {0, 0}, clean = 0, full = 0;  // next parities by slot
-      bool ok = true;
-      auto wait_slot = [&](uint32_t e) {
-        const uint32_t s = e % kSlots, parity = (full >> s) & 1;
-        full ^= 1u << s;
-        return mbar_wait(&kv_full[s], parity, err, abort);
-      };
-      auto scores = [&](int i, uint32_t e) {  // S_i = Q_i K^T
-        const uint32_t qa = smem_u32(sq + i * L::kTileBytes), ka = smem_u32(ring + (e % kSlots) * L::kTileBytes);
+    // The whole warp follows the loop and one elected lane issues: the operands
+    // stay in uniform registers (issued from a one-lane branch, each product
+    // first moved its descriptors there: 4700 cycles a tile pair for what the
+    // tensor cores do in 2048).
+    constexpr uint32_t id_s = idesc_bf16_f32(kTile, kTile);
+    constexpr uint32_t id_o = idesc_bf16_f32(kTile, D) | (1u << 16);  // B is N-major
+    const bool leader = elect_one();
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+    const uint64_t q_desc = sdesc_sw128(smem_u32(sq)), k_desc = sdesc_sw128(smem_u32(ring));
+    const uint64_t v_desc = sdesc_sw128_mn(smem_u32(ring), kTile * 128);
+    constexpr uint32_t kTileStep = L::kTileBytes >> 4;   // in descriptor units
+    uint32_t slot = 0, nq[2] = {0, 0}, np[2] = {0, 0}, clean = 0, full = 0;  // next slot and parities by slot
+    bool ok = true;
+    auto all = [&](bool x) { return __all_sync(0xffffffffu, x); };
+    auto wait_slot = [&](uint32_t s) {
+      const uint32_t parity = (full >> s) & 1;
+      full ^= 1u << s;
+      return all(mbar_wait(&kv_full[s], parity, err, abort));
+    };
+    auto after = [&](uint32_t s) { return s + 1 == kSlots ? 0 : s + 1; };
+    auto scores = [&](int i, uint32_t s) {  // S_i = Q_i K^T
+      if (leader) {
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = (kk >> 2) * (kTile * 128) + (kk & 3) * 32;
-          umma_bf16(tmem + kColS + i * 128, sdesc_sw128(qa + off), sdesc_sw128(ka + off), id_s, kk > 0);
+          constexpr uint32_t kHalf = kTile * 128 >> 4;
+          const uint32_t off = (kk >> 2) * kHalf + (kk & 3) * 2;
+          umma_bf16(tm + kColS + i * 128, q_desc + (i * kTileStep + off), k_desc + (s * kTileStep + off), id_s, kk > 0);
         }
         umma_commit(&s_full[i]);
-      };
-      auto outputs = [&](int i, uint32_t e, bool first) {  // O_i (+)= P_i V
-        const uint32_t va = smem_u32(ring + (e % kSlots) * L::kTileBytes);
+      }
+    };
+    auto outputs = [&](int i, uint32_t s, bool first) {  // O_i (+)= P_i V
+      if (leader) {
 #pragma unroll
         for (int kk = 0; kk < kTile / 16; ++kk)
-          umma_bf16_ta(tmem + kColO + i * 128, tmem + kColS + i * 128 + kk * 8,
-                       sdesc_sw128_mn(va + kk * 16 * 128, kTile * 128), id_o, !first || kk > 0);
+          umma_bf16_ta(tm + kColO + i * 128, tm + kColS + i * 128 + kk * 8,
+                       v_desc + (s * kTileStep + kk * (16 * 128 >> 4)), id_o, !first || kk > 0);
         umma_commit(&o_full[i]);
-      };
-      for (int64_t r = 0; ok && item_of_round(r) < sc.n_items; ++r) {
-        const Item x = item_at(a, sc, item_of_round(r));
-        const int n = x.n();
-        if (n == 0) continue;
-        ok = wait_slot(g);
-        for (int i = 0; ok && i < 2; ++i) {
-          if (x.tiles[i] == 0) continue;
-          if (!mbar_wait(&q_full[i], nq[i] & 1, err, abort)) {
-            ok = false;
-            break;
-          }
-          ++nq[i];
-          tc_fence_after();
-          scores(i, g);
-          if (x.tiles[i] == 1) umma_commit(&q_empty[i]);
-        }
-        if (!ok) break;
-        umma_commit(&kv_empty[g % kSlots]);
-        for (int j = 0; ok && j < n; ++j) {
-          const uint32_t ev = g + 2 * j + 1, ek = ev + 1;
-          if (x.mixed(j)) {
-            const int s = ev % kSlots;
-            ok = mbar_wait(&v_clean[s], (clean >> s) & 1, err, abort);
-            clean ^= 1u << s;
-          } else {
-            ok = wait_slot(ev);
-          }
-          if (ok && j + 1 < n) ok = wait_slot(ek);
-          for (int i = 0; ok && i < 2; ++i) {
-            if (j < x.tiles[i]) {
-              if (!mbar_wait(&p_full[i], np[i] & 1, err, abort)) {
-                ok = false;
-                break;
-              }
-              ++np[i];
-              tc_fence_after();
-              outputs(i, ev, j == 0);
-            }
-            if (i == 1) umma_commit(&kv_empty[ev % kSlots]);
-            if (j + 1 < x.tiles[i]) {
-              scores(i, ek);
-              if (j + 2 == x.tiles[i]) umma_commit(&q_empty[i]);
-            }
-            if (i == 1 && j + 1 < n) umma_commit(&kv_empty[ek % kSlots]);
-          }
-        }
-        g += 2 * n;
       }
-      // every product issued has completed before the TMEM is released
-      for (int i = 0; i < 2; ++i) {
-        if (np[i] > 0) mbar_drain(&o_full[i], (np[i] - 1) & 1);
-        if (*abort && nq[i] > 0) mbar_drain(&s_full[i], np[i] & 1);
+    };
+    auto commit = [&](uint64_t* bar) {
+      if (leader) umma_commit(bar);
+    };
+    uint32_t r = 0;
+    for (int64_t it = blockIdx.x; ok && it >= 0; it = next_item(r++)) {
+      const Item x = item_at(a, sc, it);
+      const int n = x.n();
+      if (n == 0) continue;
+      ok = wait_slot(slot);
+      for (int i = 0; ok && i < 2; ++i) {
+        if (x.tiles[i] == 0) continue;
+        if (!all(mbar_wait(&q_full[i], nq[i] & 1, err, abort))) {
+          ok = false;
+          break;
+        }
+        ++nq[i];
+        tc_fence_after();
+        scores(i, slot);
+        if (x.tiles[i] == 1) commit(&q_empty[i]);
+      }
+      if (!ok) break;
+      commit(&kv_empty[slot]);
+      slot = after(slot);
+      for (int j = 0; ok && j < n; ++j) {
+        const uint32_t sv = slot, sk = after(slot);
+        if (x.mixed(j)) {
+          ok = all(mbar_wait(&v_clean[sv], (clean >> sv) & 1, err, abort));
+          clean ^= 1u << sv;
+        } else {
+          ok = wait_slot(sv);
+        }
+        if (ok && j + 1 < n) ok = wait_slot(sk);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          if (!ok) break;
+          if (j < x.tiles[i]) {
+            if (!all(mbar_wait(&p_full[i], np[i] & 1, err, abort))) {
+              ok = false;
+              break;
+            }
+            ++np[i];
+            tc_fence_after();
+            outputs(i, sv, j == 0);
+          }
+          if (i == 1) commit(&kv_empty[sv]);
+          if (j + 1 < x.tiles[i]) {
+            scores(i, sk);
+            if (j + 2 == x.tiles[i]) commit(&q_empty[i]);
+          }
+          if (i == 1 && j + 1 < n) commit(&kv_empty[sk]);
+        }
+        slot = j + 1 < n ? after(sk) : sk;
       }
     }
+    // every product issued has completed before the TMEM is released
+    for (int i = 0; i < 2; ++i) {
+      if (np[i] > 0) mbar_drain(&o_full[i], (np[i] - 1) & 1);
+      if (*reinterpret_cast<volatile int*>(abort) && nq[i] > 0) mbar_drain(&s_full[i], np[i] & 1);
+    }
+    __syncwarp();
   } else if (warp >= 10) {
     // ------------------------------------------- V tiles that are seen in part
     const int t = threadIdx.x - 320;
@@ -434,8 +506,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         int q0, lq, k0, lk;
         seq_rows(a, b, &q0, &lq, &k0, &lk);
       }
-    for (int64_t r = 0; ok && item_of_round(r) < sc.n_items; ++r) {
-      const Item x = item_at(a, sc, item_of_round(r));
+    uint32_t r = 0;
+    for (int64_t it = blockIdx.x; ok && it >= 0; it = next_item(r++)) {
+      const Item x = item_at(a, sc, it);
       const int n = x.n();
       for (int j = 0; ok && j < n; ++j) {
         if (!x.mixed(j)) continue;
@@ -477,8 +550,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t np = 0;
     int item = 0;
     bool ok = true;
-    for (int64_t r = 0; ok && item_of_round(r) < sc.n_items; ++r) {
-      const Item x = item_at(a, sc, item_of_round(r));
+    uint32_t r = 0;
+    for (int64_t it = blockIdx.x; ok && it >= 0; it = next_item(r++)) {
+      const Item x = item_at(a, sc, it);
       const int n = x.tiles[i];
       const int see = x.see(tok);
       float m = -INFINITY, l = 0.f;
@@ -488,26 +562,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         const int limit = see - j * kTile;
         const bool part = (j + 1) * kTile > x.see(i * sc.tpt);  // warp-uniform
-        float mx = -INFINITY;
+        float v[kTile];
 #pragma unroll
-        for (int c = 0; c < 4; c += 2) {
-          float v[2][32];
-          tmem_ld32(ts + c * 32, v[0]);
-          tmem_ld32(ts + c * 32 + 32, v[1]);
-          tmem_ld_wait();
-          if (part) {
+        for (int c = 0; c < 4; ++c) tmem_ld32(ts + c * 32, v + c * 32);
+        tmem_ld_wait();
+        if (part) {
 #pragma unroll
-            for (int u = 0; u < 64; ++u) mx = c * 32 + u < limit ? fmaxf(mx, v[u >> 5][u & 31]) : mx;
-          } else {
-            float m1 = -INFINITY;
-#pragma unroll
-            for (int u = 0; u < 32; ++u) {
-              mx = fmaxf(mx, v[0][u]);
-              m1 = fmaxf(m1, v[1][u]);
-            }
-            mx = fmaxf(mx, m1);
-          }
+          for (int u = 0; u < kTile; ++u) v[u] = u < limit ? v[u] : -INFINITY;
         }
+        float mx4[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+        for (int u = 4; u < kTile; u += 8) {
+#pragma unroll
+          for (int w = 0; w < 4; ++w)
+            mx4[w] = u + 4 + w < kTile ? fmaxf(fmaxf(v[u + w], v[u + 4 + w]), mx4[w]) : fmaxf(v[u + w], mx4[w]);
+        }
+        const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
         const float want = mx == -INFINITY ? -INFINITY : mx * a.c2;
         const bool move = j == 0 || want > m + kGrow;
         if (j == 0) {
@@ -520,39 +590,32 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_after();
 #pragma unroll
           for (int c = 0; c < D / 16; ++c) {
-            float v[16];
+            float y[16];
             uint32_t w[16];
-            tmem_ld16(to + c * 16, v);
+            tmem_ld16(to + c * 16, y);
             tmem_ld_wait();
 #pragma unroll
-            for (int u = 0; u < 16; ++u) w[u] = __float_as_uint(v[u] * f);
+            for (int u = 0; u < 16; ++u) w[u] = __float_as_uint(y[u] * f);
             tmem_st16(to + c * 16, w);
           }
           l *= f;
           m = mz;
         }
         const float mu = m == -INFINITY ? 0.f : m;
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          float v[32];
           uint32_t w[16];
-          tmem_ld32(ts + c * 32, v);
-          tmem_ld_wait();
-#pragma unroll
-          for (int u = 0; u < 32; ++u) {
-            v[u] = ex2(fmaf(v[u], a.c2, -mu));
-            if (part) v[u] = c * 32 + u < limit ? v[u] : 0.f;
-          }
-          float s0 = 0.f, s1 = 0.f;
 #pragma unroll
           for (int u = 0; u < 32; u += 2) {
-            s0 += v[u];
-            s1 += v[u + 1];
-            w[u / 2] = pack2(v[u], v[u + 1]);
+            const float e0 = ex2(fmaf(v[c * 32 + u], a.c2, -mu)), e1 = ex2(fmaf(v[c * 32 + u + 1], a.c2, -mu));
+            sum[u & 2] += e0;
+            sum[(u & 2) + 1] += e1;
+            w[u / 2] = pack2(e0, e1);
           }
-          l += s0 + s1;
           tmem_st16(ts + c * 16, w);  // over scores that are read already
         }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
         tmem_st_wait();
         tc_fence_before();
         mbar_arrive(&p_full[i]);
@@ -637,12 +700,11 @@ bool map_rows(CUtensorMap* m, const void* p, int64_t tokens, int heads, int D, i
 template <int D>
 cudaError_t launch_prompt(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const PromptArgs& a,
                           const Schedule& sc, cudaStream_t st) {
-  const int sms = device_sms();
   static ReadyOnce ready;
   const cudaError_t e = ready.shared_memory(k_prompt_tc<D>, Smem<D>::kBytes);
   if (e != cudaSuccess) return e;
   count_launch();
-  k_prompt_tc<D><<<static_cast<int>(sc.n_items < sms ? sc.n_items : sms), kThreads, Smem<D>::kBytes, st>>>(mq, mk, mv,
+  k_prompt_tc<D><<<static_cast<unsigned>(sc.n_items), kThreads, Smem<D>::kBytes, st>>>(mq, mk, mv,
                                                                                                          a, sc);
   return cudaGetLastError();
 }
@@ -695,7 +757,8 @@ extern "C" int ai_attend_prompt(const void* q_dev, const int64_t* q_strides, con
   a.Hq = n_heads;
   a.Hkv = n_kv_heads;
   a.G = n_heads / n_kv_heads;
-  a.c2 = scale * kLog2e;
+  // scale 0 weighs all keys alike; a masked score, -inf, stays -inf
+  a.c2 = scale == 0.f ? 1e-30f : scale * kLog2e;
   a.out = static_cast<uint16_t*>(out_dev);
   a.lse = lse_dev;
   a.status = status_dev;
@@ -706,6 +769,7 @@ extern "C" int ai_attend_prompt(const void* q_dev, const int64_t* q_strides, con
   if (slots > 0x7fffffff) return fail(AI_ERR_ARG, "too many query blocks");
   sc.n_slots = static_cast<int>(slots);
   sc.n_items = slots * n_kv_heads;
+  if (sc.n_items > 0x7fffffff) return fail(AI_ERR_ARG, "too many query blocks");
   CUtensorMap mq, mk, mv;
   // without keys nothing is loaded, but a map needs a row
   const bool none = total_k == 0;
