@@ -294,7 +294,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&q_full[i], 1);
       mbar_init(&q_empty[i], 1);
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], 128);
+      mbar_init(&p_full[i], 4);
       mbar_init(&o_full[i], 1);
       mbar_init(&next_full[i], 1);
       mbar_init(&next_read[i], kThreads / 32);
@@ -303,7 +303,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&kv_full[s], 1);
       mbar_init(&kv_empty[s], 1);
       mbar_init(&mx_full[s], 1);
-      mbar_init(&v_clean[s], 64);
+      mbar_init(&v_clean[s], 2);
     }
     *abort = 0;
     for (int i = 0; i < L::kSick; ++i) sick[i] = 0;
@@ -534,7 +534,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (bad & 0x80008000u) reinterpret_cast<volatile int*>(sick)[item % L::kSick] = item + 1;
         fence_proxy_async_smem();
-        mbar_arrive(&v_clean[s]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&v_clean[s]);
       }
       g += 2 * n;
       item += n > 0;
@@ -618,7 +619,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
         tmem_st_wait();
         tc_fence_before();
-        mbar_arrive(&p_full[i]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[i]);  // (128 arrivals on one barrier queue up)
       }
       if (!ok) break;
       if (n > 0) {
