@@ -75,7 +75,7 @@ __device__ __forceinline__ bool seq_rows(const PromptArgs& a, int b, int* q0, in
 
 // One query row of one head by one warp, reading only the keys it sees.
 template <int D>
-__device__ __noinline__ void attend_row(const PromptArgs& a, int qi, int h, int k0, int n_keys) {
+__device__ __forceinline__ void attend_row(const PromptArgs& a, int qi, int h, int k0, int n_keys) {
   const int lane = threadIdx.x & 31;
   const uint16_t* q = a.q + qi * a.q_tok + h * a.q_head;
   const int kh = h / a.G;
@@ -120,6 +120,8 @@ __device__ __noinline__ void attend_row(const PromptArgs& a, int qi, int h, int 
 // ------------------------------------------------------------ tensor cores
 constexpr int kTile = 128;        // rows of a query tile, keys of a key tile
 constexpr int kThreads = 384;
+template <int D>
+constexpr int kPolyOf = D == 64 ? 1 : 0;      // pairs of weights in eight that the FMA pipes compute
 constexpr float kGrow = 8.f;      // log2 by which the maximum may grow before O is rescaled
 
 template <int D>
@@ -246,6 +248,52 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// Pairs of floats in a 64-bit register, for the two-wide fp32 instructions.
+__device__ __forceinline__ uint64_t f2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float lo_of(uint64_t x) { return __uint_as_float(static_cast<uint32_t>(x)); }
+__device__ __forceinline__ float hi_of(uint64_t x) { return __uint_as_float(static_cast<uint32_t>(x >> 32)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t exp2_mufu2(uint64_t x) { return f2(ex2(lo_of(x)), ex2(hi_of(x))); }
+// 2^x for x <= 2^7 on the FMA pipes, which the sixteen exponentials a cycle of
+// the special function units would leave idle: x = n + f with f in [-1/2, 1/2]
+// (rounded by adding 1.5 2^23), 2^f by the polynomial of degree 5 that
+// interpolates it at the Chebyshev nodes (2.1e-7 with its fp32 rounding), 2^n
+// from the exponent bits.  Below -127 the result is 0; NaN stays NaN.
+__device__ __forceinline__ float floor127(float x) {
+  float y;
+  asm("max.NaN.f32 %0, %1, 0fC2FE0000;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint64_t exp2_poly2(uint64_t x) {
+  constexpr float kRound = 12582912.f + 127.f;
+  const uint64_t y = f2(floor127(lo_of(x)), floor127(hi_of(x)));
+  const uint64_t t = add2(y, f2(kRound, kRound));
+  const uint64_t f = add2(y, mul2(add2(t, f2(-kRound, -kRound)), f2(-1.f, -1.f)));
+  uint64_t p = fma2(f, f2(0.00133908634f, 0.00133908634f), f2(0.00967603192f, 0.00967603192f));
+  p = fma2(p, f, f2(0.0555035711f, 0.0555035711f));
+  p = fma2(p, f, f2(0.240221075f, 0.240221075f));
+  p = fma2(p, f, f2(0.693147188f, 0.693147188f));
+  p = fma2(p, f, f2(1.00000008f, 1.00000008f));
+  return mul2(p, f2(__uint_as_float(static_cast<uint32_t>(t) << 23), __uint_as_float(static_cast<uint32_t>(t >> 32) << 23)));
+}
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&b);
@@ -265,7 +313,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     k_prompt_tc(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                 const __grid_constant__ CUtensorMap map_v, const PromptArgs a, const Schedule sc) {
   using L = Smem<D>;
-  constexpr int kSlots = L::kSlots;
+  constexpr int kSlots = L::kSlots, kPoly = kPolyOf<D>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sq = base;                              // [2] query tiles
@@ -328,6 +376,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     return it;
   };
 
+  // the rows' warps take registers that the others do not need (8 x 208 + 4 x
+  // 88 a lane, as many as the block was launched with: 12 x 168)
+  if (warp >= 8) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
   if (warp == 8) {
     // ---------------------------------------------------------- TMA loads
     const bool leader = elect_one();
@@ -495,7 +547,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (*reinterpret_cast<volatile int*>(abort) && nq[i] > 0) mbar_drain(&s_full[i], np[i] & 1);
     }
     __syncwarp();
-  } else if (warp >= 10) {
+  } else {
     // ------------------------------------------- V tiles that are seen in part
     const int t = threadIdx.x - 320;
     uint32_t g = 0, full = 0;
@@ -540,7 +592,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       g += 2 * n;
       item += n > 0;
     }
+  }
   } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     // ------------------------------------------------------------ softmax
     const int i = warp >> 2;                         // query tile
     const int row = (warp & 3) * 32 + lane;          // row of the tile = TMEM lane
@@ -603,20 +657,23 @@ __global__ void __launch_bounds__(kThreads, 1)
           m = mz;
         }
         const float mu = m == -INFINITY ? 0.f : m;
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        // weights: of eight pairs kPoly by polynomial, the rest by ex2
+        uint64_t sum[2] = {0, 0};
+        const uint64_t c2 = f2(a.c2, a.c2), nmu = f2(-mu, -mu);
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           uint32_t w[16];
 #pragma unroll
-          for (int u = 0; u < 32; u += 2) {
-            const float e0 = ex2(fmaf(v[c * 32 + u], a.c2, -mu)), e1 = ex2(fmaf(v[c * 32 + u + 1], a.c2, -mu));
-            sum[u & 2] += e0;
-            sum[(u & 2) + 1] += e1;
-            w[u / 2] = pack2(e0, e1);
+          for (int u = 0; u < 16; ++u) {
+            const uint64_t x = fma2(f2(v[c * 32 + 2 * u], v[c * 32 + 2 * u + 1]), c2, nmu);
+            const uint64_t e = (u % 8) * kPoly / 8 != (u % 8 + 1) * kPoly / 8 ? exp2_poly2(x) : exp2_mufu2(x);
+            sum[u & 1] = add2(sum[u & 1], e);
+            w[u] = pack2(lo_of(e), hi_of(e));
           }
           tmem_st16(ts + c * 16, w);  // over scores that are read already
         }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        const uint64_t total = add2(sum[0], sum[1]);
+        l += lo_of(total) + hi_of(total);
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
