@@ -327,7 +327,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* v_clean = mx_full + kSlots;            // [kSlots] and looked at
   uint64_t* s_full = v_clean + kSlots;             // [2] scores in TMEM
   uint64_t* p_full = s_full + 2;                   // [2] weights in TMEM
-  uint64_t* o_full = p_full + 2;                   // [2] product with V done
+  uint64_t* o_full = p_full + 2;                   // [2] last product with V of an item done
   uint64_t* next_full = o_full + 2;                // [2] next item known
   uint64_t* next_read = next_full + 2;             // [2] and read by every warp
   uint4* answer = reinterpret_cast<uint4*>((reinterpret_cast<uintptr_t>(next_read + 2) + 15) & ~uintptr_t(15));  // [2]
@@ -478,13 +478,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         umma_commit(&s_full[i]);
       }
     };
-    auto outputs = [&](int i, uint32_t s, bool first) {  // O_i (+)= P_i V
+    auto outputs = [&](int i, uint32_t s, bool first, bool last) {  // O_i (+)= P_i V
       if (leader) {
 #pragma unroll
         for (int kk = 0; kk < kTile / 16; ++kk)
           umma_bf16_ta(tm + kColO + i * 128, tm + kColS + i * 128 + kk * 8,
                        v_desc + (s * kTileStep + kk * (16 * 128 >> 4)), id_o, !first || kk > 0);
-        umma_commit(&o_full[i]);
+        if (last) umma_commit(&o_full[i]);
       }
     };
     auto commit = [&](uint64_t* bar) {
@@ -529,7 +529,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             ++np[i];
             tc_fence_after();
-            outputs(i, sv, j == 0);
+            outputs(i, sv, j == 0, j + 1 == x.tiles[i]);
           }
           if (i == 1) commit(&kv_empty[sv]);
           if (j + 1 < x.tiles[i]) {
@@ -543,7 +543,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     // every product issued has completed before the TMEM is released
     for (int i = 0; i < 2; ++i) {
-      if (np[i] > 0) mbar_drain(&o_full[i], (np[i] - 1) & 1);
+      if (nq[i] > 0) mbar_drain(&o_full[i], (nq[i] - 1) & 1);
       if (*reinterpret_cast<volatile int*>(abort) && nq[i] > 0) mbar_drain(&s_full[i], np[i] & 1);
     }
     __syncwarp();
@@ -602,7 +602,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t ts = tmem + kColS + i * 128 + lane_off, to = tmem + kColO + i * 128 + lane_off;
     const int tok = i * sc.tpt + row / a.G, gh = row % a.G;
     const bool used = row < sc.tpt * a.G;
-    uint32_t np = 0;
+    uint32_t np = 0, no = 0;   // score tiles, items with any
     int item = 0;
     bool ok = true;
     uint32_t r = 0;
@@ -640,9 +640,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else if (__any_sync(0xffffffffu, move)) {
           const float mz = move ? want : m;
           const float f = move ? ex2(m - mz) : 1.f;  // m = -inf: nothing seen so far, O and l are 0
-          ok = __all_sync(0xffffffffu, mbar_wait(&o_full[i], (np - 1) & 1, err, abort));
-          if (!ok) break;
-          tc_fence_after();
+          // (these scores were issued after the last product with V and have
+          // arrived, so O is complete)
 #pragma unroll
           for (int c = 0; c < D / 16; ++c) {
             float y[16];
@@ -681,7 +680,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
       if (n > 0) {
-        ok = __all_sync(0xffffffffu, mbar_wait(&o_full[i], (np - 1) & 1, err, abort));
+        ok = __all_sync(0xffffffffu, mbar_wait(&o_full[i], no & 1, err, abort));
+        ++no;
         if (!ok) break;
         tc_fence_after();
       }
