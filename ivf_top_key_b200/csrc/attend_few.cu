@@ -95,10 +95,11 @@ __global__ void __launch_bounds__(Few<D, FP8>::kThreads, 1) k_attend_few(const R
     *abort = 0;
     fence_mbar_init();
   }
+  dependency_wait();
   Walk w;
   begin_walk<L::kThreads, D>(a, reinterpret_cast<int*>(states) /* before the first state */, err, &w);
   // the joining kernel may be set up now; it waits for this one to end
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  dependency_launch();
   Share x;
 
   if (warp >= kComp + kCopiers) {
@@ -561,9 +562,7 @@ cudaError_t launch_few(const RowsArgs& a, int grid, cudaStream_t st) {
   static ReadyOnce ready;
   const cudaError_t e = ready.shared_memory(k_attend_few<D, FP8>, L::kBytes);
   if (e != cudaSuccess) return e;
-  count_launch();
-  k_attend_few<D, FP8><<<grid, L::kThreads, L::kBytes, st>>>(a);
-  return cudaGetLastError();
+  return launch_after(k_attend_few<D, FP8>, dim3(grid), dim3(L::kThreads), L::kBytes, st, a);
 }
 
 }  // namespace

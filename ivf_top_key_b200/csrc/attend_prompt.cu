@@ -364,6 +364,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  dependency_wait();
   const uint32_t tmem = *tmem_slot;
   // the item after this warp's r-th; -1: no more
   auto next_item = [&](uint32_t r) {
@@ -762,10 +763,8 @@ cudaError_t launch_prompt(const CUtensorMap& mq, const CUtensorMap& mk, const CU
   static ReadyOnce ready;
   const cudaError_t e = ready.shared_memory(k_prompt_tc<D>, Smem<D>::kBytes);
   if (e != cudaSuccess) return e;
-  count_launch();
-  k_prompt_tc<D><<<static_cast<unsigned>(sc.n_items), kThreads, Smem<D>::kBytes, st>>>(mq, mk, mv,
-                                                                                                         a, sc);
-  return cudaGetLastError();
+  return launch_after(k_prompt_tc<D>, dim3(static_cast<unsigned>(sc.n_items)), dim3(kThreads), Smem<D>::kBytes, st, mq, mk,
+                      mv, a, sc);
 }
 
 }  // namespace

@@ -119,10 +119,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_mbar_init();
   }
 
+  dependency_wait();
   Walk w;
   begin_walk<kThreads, D>(a, reinterpret_cast<int*>(merge) /* before the first row is joined */, err, &w);
   // the joining kernel may be set up now; it waits for this one to end
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  dependency_launch();
   Share x;
 
   if (warp >= kWarps) {
@@ -626,7 +627,7 @@ template <int D>
 __global__ void __launch_bounds__(kJoin) k_join_rows(const RowsArgs a, int n_ctas, int slot_rows) {
   __shared__ float sh_w[kJoin], sh_red[kJoin / 32], sh_o[kJoin];
   __shared__ int sh_end;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  dependency_wait();
   const int c = blockIdx.x, r = blockIdx.y, tid = threadIdx.x;
   const int item = a.meta[c * 4 + 2];
   if (item < 0) return;
@@ -707,9 +708,7 @@ cudaError_t launch_mt(const RowsArgs& a, int grid, cudaStream_t st) {
   static ReadyOnce ready;
   const cudaError_t e = ready.shared_memory(k_attend_rows<D, FP8, MT>, L::kBytes);
   if (e != cudaSuccess) return e;
-  count_launch();
-  k_attend_rows<D, FP8, MT><<<grid, kThreads, L::kBytes, st>>>(a);
-  return cudaGetLastError();
+  return launch_after(k_attend_rows<D, FP8, MT>, dim3(grid), dim3(kThreads), L::kBytes, st, a);
 }
 
 template <int D, bool FP8>
@@ -720,17 +719,7 @@ cudaError_t launch_d(const RowsArgs& a, int grid, cudaStream_t st) {
   else if (a.mb_rows <= 32) e = launch_mt<D, FP8, 2>(a, grid, st);
   else e = launch_mt<D, FP8, 4>(a, grid, st);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(grid, a.mb_rows);
-  cfg.blockDim = dim3(kJoin);
-  cfg.stream = st;
-  cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  count_launch();
-  return cudaLaunchKernelEx(&cfg, k_join_rows<D>, a, grid, rows_per_slot(a.mb_rows));
+  return launch_after(k_join_rows<D>, dim3(grid, a.mb_rows), dim3(kJoin), 0, st, a, grid, rows_per_slot(a.mb_rows));
 }
 
 int fail(int code, const char* msg) {

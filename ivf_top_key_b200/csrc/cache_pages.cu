@@ -106,6 +106,7 @@ __device__ int lowest_free(const View& c, int want, int32_t* list, int* sums) {
 __global__ void __launch_bounds__(kPlan) k_extend(View c, const int32_t* seqs, const int32_t* counts, int n,
                                                   int32_t* scratch) {
   __shared__ int sums[32];
+  dependency_wait();
   int32_t* rank = scratch;
   int32_t* fresh = scratch + n;
   int64_t before = 0;
@@ -163,6 +164,7 @@ __global__ void __launch_bounds__(kPlan) k_extend(View c, const int32_t* seqs, c
 template <bool FP8>
 __global__ void k_write(View c, int64_t layer_slots, int layer, const uint16_t* kn, const uint16_t* vn,
                         const int32_t* seqs, const int32_t* cu, int n, int n_tokens, int Hkv, int D) {
+  dependency_wait();
   const int64_t wid = (blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x) >> 5;
   const int lane = threadIdx.x & 31;
   if (wid >= static_cast<int64_t>(n_tokens) * Hkv) return;
@@ -222,10 +224,13 @@ __global__ void k_write(View c, int64_t layer_slots, int layer, const uint16_t* 
 
 // --------------------------------------------------------------------- fork
 // All forks read the state before the call.  plan[i]: the fresh page of fork
-// i's part page, -1 where it has none, -2 where the fork is refused.
+// i's part page, -1 where it has none, -2 where the fork is refused; length[i]:
+// the source's length.  What the new sequences own alone is written at once (a
+// source that is another fork's target was empty, so its row is not read).
 __global__ void __launch_bounds__(kPlan) k_fork_plan(View c, const int32_t* src, const int32_t* dst, int n,
-                                                     int32_t* plan, int32_t* fresh) {
+                                                     int32_t* plan, int32_t* length, int32_t* fresh) {
   __shared__ int sums[32];
+  dependency_wait();
   int before = 0;
   for (int i0 = 0; i0 < n; i0 += kPlan) {
     const int i = i0 + threadIdx.x;
@@ -236,7 +241,8 @@ __global__ void __launch_bounds__(kPlan) k_fork_plan(View c, const int32_t* src,
           c.lens[a] < 0 || c.lens[a] > static_cast<int64_t>(c.width) * c.page_size) {
         flag(c, AI_DEVFLAG_RANGE);
       } else {
-        need = c.lens[a] % c.page_size != 0;
+        length[i] = c.lens[a];
+        need = length[i] % c.page_size != 0;
         code = -1;
       }
     }
@@ -248,17 +254,22 @@ __global__ void __launch_bounds__(kPlan) k_fork_plan(View c, const int32_t* src,
   __syncthreads();
   const int have = lowest_free(c, before < c.n_pages ? before : c.n_pages, fresh, sums);
   for (int i = threadIdx.x; i < n; i += kPlan) {
-    if (plan[i] < 0) continue;
-    if (plan[i] < have) {
-      plan[i] = fresh[plan[i]];
-    } else {
+    const int rank = plan[i];
+    if (rank >= have) {
       plan[i] = -2;
       flag(c, AI_DEVFLAG_CAPACITY);
+    } else if (rank != -2) {
+      if (rank >= 0) {
+        plan[i] = fresh[rank];
+        c.tables[static_cast<int64_t>(dst[i]) * c.width + length[i] / c.page_size] = fresh[rank];
+        c.refs[fresh[rank]] = 1;
+      }
+      c.lens[dst[i]] = length[i];
     }
   }
 }
 
-// Copies n 16-byte units, a grid row (blockIdx.x of gridDim.x) at a time.
+// Copies n 16-byte units, block `part` of `parts`.
 __device__ __forceinline__ void copy16(uint8_t* dst, const uint8_t* src, int64_t n, int part, int parts) {
   const uint4* s = reinterpret_cast<const uint4*>(src);
   uint4* d = reinterpret_cast<uint4*>(dst);
@@ -289,15 +300,15 @@ __device__ __forceinline__ void copy_slots(const View& c, int layer, int from, i
   }
 }
 
-// grid (parts of a page, layers, forks).  The lengths of the new sequences
-// are written by the next kernel: every block reads lens[src] here, and a
-// src may be another fork's dst.
+// grid (parts of a page, layers, forks): the filled slots of the part page,
+// and the row's full pages, which gain a holder.
 __global__ void __launch_bounds__(256) k_fork_move(View c, const int32_t* src, const int32_t* dst, const int32_t* plan,
-                                                   int n) {
+                                                   const int32_t* length, int n) {
+  dependency_wait();
   for (int i = blockIdx.z; i < n; i += gridDim.z) {
     const int fresh = plan[i];
     if (fresh == -2) continue;
-    const int len = c.lens[src[i]];
+    const int len = length[i];
     const int full = len / c.page_size;
     const int32_t* from = c.tables + static_cast<int64_t>(src[i]) * c.width;
     if (fresh >= 0) {
@@ -318,26 +329,13 @@ __global__ void __launch_bounds__(256) k_fork_move(View c, const int32_t* src, c
     }
   }
 }
-__global__ void k_fork_end(View c, const int32_t* src, const int32_t* dst, const int32_t* plan, int n,
-                           int32_t* new_len) {
-  // two steps: all lengths are read before the first is written
-  for (int i = threadIdx.x; i < n; i += blockDim.x) new_len[i] = plan[i] == -2 ? 0 : c.lens[src[i]];
-  __syncthreads();
-  for (int i = threadIdx.x; i < n; i += blockDim.x) {
-    if (plan[i] == -2) continue;
-    if (plan[i] >= 0) {
-      c.tables[static_cast<int64_t>(dst[i]) * c.width + new_len[i] / c.page_size] = plan[i];
-      c.refs[plan[i]] = 1;
-    }
-    c.lens[dst[i]] = new_len[i];
-  }
-}
 
 // --------------------------------------------------------------------- free
 // One block per listed sequence; the block that takes the length owns it, so
 // a sequence listed twice is released once.
 __global__ void __launch_bounds__(256) k_free(View c, const int32_t* seqs, int n) {
   __shared__ int sh_len;
+  dependency_wait();
   for (int i = blockIdx.x; i < n; i += gridDim.x) {
     const int s = seqs[i];
     __syncthreads();
@@ -366,6 +364,7 @@ __global__ void __launch_bounds__(256) k_free(View c, const int32_t* seqs, int n
 __global__ void __launch_bounds__(kPlan) k_compact_plan(View c, int32_t* map, int32_t* from, int32_t* to,
                                                         int32_t* count) {
   __shared__ int sums[32];
+  dependency_wait();
   int live = 0;
   for (int p = threadIdx.x; p < c.n_pages; p += kPlan) live += c.refs[p] > 0;
   int n_live;
@@ -397,6 +396,7 @@ __global__ void __launch_bounds__(kPlan) k_compact_plan(View c, int32_t* map, in
 
 __global__ void __launch_bounds__(256) k_compact_move(View c, const int32_t* map, const int32_t* from,
                                                       const int32_t* to, const int32_t* count) {
+  dependency_wait();
   const int n = *count;
   const int64_t units = static_cast<int64_t>(n) * c.n_layers;
   for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
@@ -438,10 +438,7 @@ View view_of(const ai_cache* c) {
   return v;
 }
 
-int launched() {
-  const cudaError_t e = cudaGetLastError();
-  return e == cudaSuccess ? AI_OK : fail(AI_ERR_CUDA, cudaGetErrorString(e));
-}
+int done(cudaError_t e) { return e == cudaSuccess ? AI_OK : fail(AI_ERR_CUDA, cudaGetErrorString(e)); }
 
 int check_tables(const ai_cache* c) {
   if (!c) return fail(AI_ERR_ARG, "null cache");
@@ -526,10 +523,8 @@ extern "C" int ai_cache_extend(const ai_cache* c, const int32_t* seqs_dev, const
   if (!rc && n > 0 && !counts_dev) rc = fail(AI_ERR_ARG, "null counts");
   if (!rc) rc = check_ws(c, n, workspace_dev, workspace_bytes);
   if (rc || n == 0) return rc;
-  count_launch();
-  k_extend<<<1, kPlan, 0, static_cast<cudaStream_t>(cuda_stream)>>>(view_of(c), seqs_dev, counts_dev, n,
-                                                                    static_cast<int32_t*>(workspace_dev));
-  return launched();
+  return done(launch_after(k_extend, dim3(1), dim3(kPlan), 0, static_cast<cudaStream_t>(cuda_stream), view_of(c), seqs_dev,
+                           counts_dev, n, static_cast<int32_t*>(workspace_dev)));
 }
 
 extern "C" int ai_cache_write(const ai_cache* c, int32_t layer, const void* k_dev, const void* v_dev,
@@ -550,14 +545,12 @@ extern "C" int ai_cache_write(const ai_cache* c, int32_t layer, const void* k_de
   cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
   const uint16_t* kn = static_cast<const uint16_t*>(k_dev);
   const uint16_t* vn = static_cast<const uint16_t*>(v_dev);
-  count_launch();
-  if (c->dtype == AI_BF16)
-    k_write<false><<<static_cast<unsigned>(blocks), 256, 0, st>>>(view_of(c), slots, layer, kn, vn, seqs_dev, cu_dev, n,
-                                                                  n_tokens, c->n_kv_heads, c->head_dim);
-  else
-    k_write<true><<<static_cast<unsigned>(blocks), 256, 0, st>>>(view_of(c), slots, layer, kn, vn, seqs_dev, cu_dev, n,
-                                                                 n_tokens, c->n_kv_heads, c->head_dim);
-  return launched();
+  const dim3 grid(static_cast<unsigned>(blocks));
+  return done(c->dtype == AI_BF16
+                  ? launch_after(k_write<false>, grid, dim3(256), 0, st, view_of(c), slots, layer, kn, vn, seqs_dev, cu_dev,
+                                 n, n_tokens, c->n_kv_heads, c->head_dim)
+                  : launch_after(k_write<true>, grid, dim3(256), 0, st, view_of(c), slots, layer, kn, vn, seqs_dev, cu_dev,
+                                 n, n_tokens, c->n_kv_heads, c->head_dim));
 }
 
 extern "C" int ai_cache_fork(const ai_cache* c, const int32_t* src_dev, const int32_t* dst_dev, int32_t n,
@@ -571,18 +564,15 @@ extern "C" int ai_cache_fork(const ai_cache* c, const int32_t* src_dev, const in
   const View v = view_of(c);
   cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
   int32_t* plan = static_cast<int32_t*>(workspace_dev);
-  int32_t* fresh = plan + n;
-  count_launch();
-  k_fork_plan<<<1, kPlan, 0, st>>>(v, src_dev, dst_dev, n, plan, fresh);
+  int32_t* length = plan + n;
+  int32_t* fresh = length + n;
   // parts of 16 KB of a page's K
   const int64_t parts = (v.page_bytes + 16383) / 16384;
   const dim3 grid(static_cast<unsigned>(parts < 64 ? parts : 64), v.n_layers < 1024 ? v.n_layers : 1024,
                   n < 1024 ? n : 1024);
-  count_launch();
-  k_fork_move<<<grid, 256, 0, st>>>(v, src_dev, dst_dev, plan, n);
-  count_launch();
-  k_fork_end<<<1, 1024, 0, st>>>(v, src_dev, dst_dev, plan, n, plan + n);
-  return launched();
+  rc = done(launch_after(k_fork_plan, dim3(1), dim3(kPlan), 0, st, v, src_dev, dst_dev, n, plan, length, fresh));
+  if (rc) return rc;
+  return done(launch_after(k_fork_move, grid, dim3(256), 0, st, v, src_dev, dst_dev, plan, length, n));
 }
 
 extern "C" int ai_cache_free(const ai_cache* c, const int32_t* seqs_dev, int32_t n, void* cuda_stream) {
@@ -590,9 +580,8 @@ extern "C" int ai_cache_free(const ai_cache* c, const int32_t* seqs_dev, int32_t
   int rc = check_tables(c);
   if (!rc) rc = check_list(c, seqs_dev, n);
   if (rc || n == 0) return rc;
-  count_launch();
-  k_free<<<n < 4096 ? n : 4096, 256, 0, static_cast<cudaStream_t>(cuda_stream)>>>(view_of(c), seqs_dev, n);
-  return launched();
+  return done(launch_after(k_free, dim3(n < 4096 ? n : 4096), dim3(256), 0, static_cast<cudaStream_t>(cuda_stream),
+                           view_of(c), seqs_dev, n));
 }
 
 extern "C" int ai_cache_compact(const ai_cache* c, void* workspace_dev, int64_t workspace_bytes, void* cuda_stream) {
@@ -607,9 +596,7 @@ extern "C" int ai_cache_compact(const ai_cache* c, void* workspace_dev, int64_t 
   int32_t* from = map + c->n_pages;
   int32_t* to = from + c->n_pages;
   int32_t* count = to + c->n_pages;
-  count_launch();
-  k_compact_plan<<<1, kPlan, 0, st>>>(v, map, from, to, count);
-  count_launch();
-  k_compact_move<<<8 * device_sms(), 256, 0, st>>>(v, map, from, to, count);
-  return launched();
+  rc = done(launch_after(k_compact_plan, dim3(1), dim3(kPlan), 0, st, v, map, from, to, count));
+  if (rc) return rc;
+  return done(launch_after(k_compact_move, dim3(8 * device_sms()), dim3(256), 0, st, v, map, from, to, count));
 }

@@ -238,6 +238,26 @@ cudaError_t launch_quantize_fp8(const uint16_t* keys_bf16, int64_t n, int d, uin
 cudaError_t launch_fp8_codes_to_bf16(const uint8_t* codes, int64_t n, int d, uint16_t* out,
                                      cudaStream_t st);
 
+// -------------------------------------------------- launches that may overlap
+// Launch with programmatic dependence: the kernel's blocks may be set up while
+// the stream's kernel before it ends, and it calls dependency_wait() before it
+// touches memory.
+template <typename... P, typename... A>
+cudaError_t launch_after(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t st, A... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  count_launch();
+  return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
+
 // ------------------------------------------------------------- per device
 constexpr int kMaxDevices = 128;
 int device_sms();   // of the current device (looked up once)
