@@ -128,6 +128,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp >= kWarps) {
     // ============================================================== copies
+    // the computing warps take registers that copying does not need (8 x 216 +
+    // 4 x 72 a lane, as many as the block was launched with: 12 x 168)
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     const int cw = warp - kWarps;
     constexpr int kChunks = L::kRow / 16;            // 16-byte chunks of a key row
     constexpr int kStep = 32 / kChunks;              // rows that the warp copies at a time
@@ -274,6 +277,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     cp_async_wait_all();
   } else {
     // ============================================================= compute
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
     const int g = lane >> 2, t = lane & 3;
     const int group = warp >> 2, wm = warp % MT, wk = (warp & 3) / MT;
     const int part = group * WK + wk;              // which of the states of its head rows
@@ -366,14 +370,21 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int j = 0; j < NB / 8; ++j) s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
         if constexpr (!FP8) {
+          // a step's keys are loaded while the products of the one before run
+          uint32_t kf[2][NB / 16][4];
+          auto load_k = [&](int kk) {
+#pragma unroll
+            for (int j = 0; j < NB / 16; ++j)
+              ldsm4(kf[kk & 1][j], sk + L::at(k0 + j * 16 + (lane & 7) + ((lane >> 4) << 3), kk * 2 + ((lane >> 3) & 1)));
+          };
+          load_k(0);
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
+            if (kk + 1 < D / 16) load_k(kk + 1);
 #pragma unroll
             for (int j = 0; j < NB / 16; ++j) {
-              uint32_t b[4];
-              ldsm4(b, sk + L::at(k0 + j * 16 + (lane & 7) + ((lane >> 4) << 3), kk * 2 + ((lane >> 3) & 1)));
-              mma<false>(s[2 * j], qf[kk], b[0], b[1]);
-              mma<false>(s[2 * j + 1], qf[kk], b[2], b[3]);
+              mma<false>(s[2 * j], qf[kk], kf[kk & 1][j][0], kf[kk & 1][j][1]);
+              mma<false>(s[2 * j + 1], qf[kk], kf[kk & 1][j][2], kf[kk & 1][j][3]);
             }
           }
         } else {
@@ -486,15 +497,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         // lane i gives the address of row i of an 8 x 8 block, in the keys' order
         const int vr = k0 + (lane & 8) + L::key(lane & 7);
         if constexpr (!FP8) {
+          constexpr int kSteps = NB / 16 * (D / 16);
+          uint32_t vf[3][4];
+          auto load_v = [&](int u) {
+            ldsm4t(vf[u % 3], sv + L::at(vr + u / (D / 16) * 16, u % (D / 16) * 2 + (lane >> 4)));
+          };
+          load_v(0);
+          load_v(1);
 #pragma unroll
-          for (int j = 0; j < NB / 16; ++j) {
-#pragma unroll
-            for (int dd = 0; dd < D / 16; ++dd) {
-              uint32_t b[4];
-              ldsm4t(b, sv + L::at(vr + j * 16, dd * 2 + (lane >> 4)));
-              mma<false>(o[2 * dd], p[j], b[0], b[1]);
-              mma<false>(o[2 * dd + 1], p[j], b[2], b[3]);
-            }
+          for (int u = 0; u < kSteps; ++u) {
+            if (u + 2 < kSteps) load_v(u + 2);
+            const int j = u / (D / 16), dd = u % (D / 16);
+            mma<false>(o[2 * dd], p[j], vf[u % 3][0], vf[u % 3][1]);
+            mma<false>(o[2 * dd + 1], p[j], vf[u % 3][2], vf[u % 3][3]);
           }
         } else {
           // 16-bit transposed loads bring two neighbouring codes of two keys;
