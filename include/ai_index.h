@@ -339,7 +339,7 @@ int ai_refine_kernel_choice(ai_handle h, int32_t C, int32_t* kernel_out);
  *   k, v        [n_layers, n_pages, page_size, n_kv_heads, head_dim] in
  *               dtype (AI_BF16, or AI_FP8E4M3 codes), 16-byte aligned
  *   k_scale,    [n_layers, n_pages, page_size, n_kv_heads] float32, one per
- *   v_scale     token and head (AI_FP8E4M3), else NULL
+ *   v_scale     token and head (AI_FP8E4M3; v_scale not negative), else NULL
  *   tables      [n_seqs, max_pages] int32: page p of a sequence holds its
  *               tokens [p * page_size, (p + 1) * page_size)
  *   lens        [n_seqs] int32: tokens of each sequence

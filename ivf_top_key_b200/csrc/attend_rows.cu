@@ -768,7 +768,7 @@ int run_rows(const ai_cache* c, int32_t layer, const void* q, int32_t R, int32_t
   if (ws_bytes < workspace_for(Hq, c->n_kv_heads, c->head_dim)) return fail(AI_ERR_ARG, "workspace too small");
   const int G = Hq / c->n_kv_heads;
   const int n_mb = (G + 63) / 64;
-  if (static_cast<int64_t>(R) * c->n_kv_heads * n_mb > 0x7fffffff) return fail(AI_ERR_ARG, "too many rows times key heads");
+  if (static_cast<int64_t>(R) * c->n_kv_heads * n_mb > 0x3fffffff) return fail(AI_ERR_ARG, "too many rows times key heads");
   if (R == 0) return AI_OK;
   RowsArgs a{};
   const int64_t tokens = static_cast<int64_t>(c->n_pages) * c->page_size;

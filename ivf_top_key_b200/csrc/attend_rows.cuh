@@ -273,11 +273,11 @@ __device__ void begin_walk(const RowsArgs& a, int* sh_none, int* err, Walk* out)
       w.tile = static_cast<int>(w.b % w.nt_ids);
       w.n_tiles = w.nt_ids;
     } else {
-      const int start = static_cast<int>(w.b - sh_b0);   // within the row's tiles of all heads
+      const int64_t start = w.b - sh_b0;   // within the row's tiles of all heads
       w.row = sh_row;
       w.n_tiles = tiles_of(a, w.row);
-      w.head = start / w.n_tiles;
-      w.tile = start % w.n_tiles;
+      w.head = static_cast<int>(start / w.n_tiles);
+      w.tile = static_cast<int>(start % w.n_tiles);
     }
   }
   *out = w;

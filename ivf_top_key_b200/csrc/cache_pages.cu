@@ -269,58 +269,64 @@ __global__ void __launch_bounds__(kPlan) k_fork_plan(View c, const int32_t* src,
   }
 }
 
-// Copies n 16-byte units, block `part` of `parts`.
-__device__ __forceinline__ void copy16(uint8_t* dst, const uint8_t* src, int64_t n, int part, int parts) {
-  const uint4* s = reinterpret_cast<const uint4*>(src);
-  uint4* d = reinterpret_cast<uint4*>(dst);
-  const int64_t step = static_cast<int64_t>(parts) * blockDim.x;
-  int64_t i = static_cast<int64_t>(part) * blockDim.x + threadIdx.x;
-  for (; i + 3 * step < n; i += 4 * step) {
-    const uint4 x0 = s[i], x1 = s[i + step], x2 = s[i + 2 * step], x3 = s[i + 3 * step];
-    d[i] = x0;
-    d[i + step] = x1;
-    d[i + 2 * step] = x2;
-    d[i + 3 * step] = x3;
-  }
-  for (; i < n; i += step) d[i] = s[i];
+// Copies chunk `chunk` of the first `slots` tokens of a page of one layer: K
+// and V bytes as one run of 16-byte units, kUnits of them a thread, all loaded
+// before the first is stored; scales with chunk 0.  A chunk is 8 KB: 16 blocks
+// an SM keep 128 KB of loads under way (a page of one block's, four units a
+// thread: 64 forks of 16 layers 83 us a call, now 68).
+constexpr int kMoveThreads = 128, kUnits = 4;
+__host__ __device__ constexpr int64_t chunks_of(int64_t bytes) {
+  return (2 * bytes / 16 + kMoveThreads * kUnits - 1) / (kMoveThreads * kUnits);
 }
-
-// The first `slots` tokens of a page of one layer (K, V and scales).
-__device__ __forceinline__ void copy_slots(const View& c, int layer, int from, int to, int slots, int part, int parts) {
+__device__ __forceinline__ void copy_chunk(const View& c, int layer, int from, int to, int slots, int64_t chunk) {
   const int64_t l = static_cast<int64_t>(layer) * c.n_pages;
-  const int64_t n = static_cast<int64_t>(slots) * c.slot_bytes / 16;
-  copy16(c.k + (l + to) * c.page_bytes, c.k + (l + from) * c.page_bytes, n, part, parts);
-  copy16(c.v + (l + to) * c.page_bytes, c.v + (l + from) * c.page_bytes, n, part, parts);
-  if (c.scale_floats) {
+  const int64_t n = static_cast<int64_t>(slots) * c.slot_bytes / 16;  // units of K, and of V
+  const int64_t src = (l + from) * c.page_bytes, dst = (l + to) * c.page_bytes;
+  const int64_t u0 = chunk * (kMoveThreads * kUnits) + threadIdx.x;
+  uint4 x[kUnits];
+#pragma unroll
+  for (int i = 0; i < kUnits; ++i) {
+    const int64_t u = u0 + i * kMoveThreads;
+    if (u < 2 * n) x[i] = *reinterpret_cast<const uint4*>((u < n ? c.k + u * 16 : c.v + (u - n) * 16) + src);
+  }
+#pragma unroll
+  for (int i = 0; i < kUnits; ++i) {
+    const int64_t u = u0 + i * kMoveThreads;
+    if (u < 2 * n) *reinterpret_cast<uint4*>((u < n ? c.k + u * 16 : c.v + (u - n) * 16) + dst) = x[i];
+  }
+  if (chunk == 0 && c.scale_floats) {
     const int64_t ps = static_cast<int64_t>(c.page_size) * c.scale_floats;
-    for (int i = part * blockDim.x + threadIdx.x; i < slots * c.scale_floats; i += parts * blockDim.x) {
+    for (int i = threadIdx.x; i < slots * c.scale_floats; i += kMoveThreads) {
       c.ks[(l + to) * ps + i] = c.ks[(l + from) * ps + i];
       c.vs[(l + to) * ps + i] = c.vs[(l + from) * ps + i];
     }
   }
 }
 
-// grid (parts of a page, layers, forks): the filled slots of the part page,
+// grid (chunks of a page, layers, forks): the filled slots of the part page,
 // and the row's full pages, which gain a holder.
-__global__ void __launch_bounds__(256) k_fork_move(View c, const int32_t* src, const int32_t* dst, const int32_t* plan,
-                                                   const int32_t* length, int n) {
+__global__ void __launch_bounds__(kMoveThreads) k_fork_move(View c, const int32_t* src, const int32_t* dst,
+                                                            const int32_t* plan, const int32_t* length, int n) {
   dependency_wait();
   for (int i = blockIdx.z; i < n; i += gridDim.z) {
     const int fresh = plan[i];
     if (fresh == -2) continue;
     const int len = length[i];
-    const int full = len / c.page_size;
+    const int full = len / c.page_size, slots = len % c.page_size;
     const int32_t* from = c.tables + static_cast<int64_t>(src[i]) * c.width;
     if (fresh >= 0) {
       const int old = from[full];
-      for (int layer = blockIdx.y; layer < c.n_layers; layer += gridDim.y) {
-        if (old >= 0 && old < c.n_pages) copy_slots(c, layer, old, fresh, len % c.page_size, blockIdx.x, gridDim.x);
-        else flag(c, AI_DEVFLAG_RANGE);
+      if (old >= 0 && old < c.n_pages) {
+        const int64_t used = chunks_of(static_cast<int64_t>(slots) * c.slot_bytes);
+        for (int layer = blockIdx.y; layer < c.n_layers; layer += gridDim.y)
+          for (int64_t chunk = blockIdx.x; chunk < used; chunk += gridDim.x) copy_chunk(c, layer, old, fresh, slots, chunk);
+      } else {
+        flag(c, AI_DEVFLAG_RANGE);
       }
     }
     if (blockIdx.y == 0) {
       int32_t* to = c.tables + static_cast<int64_t>(dst[i]) * c.width;
-      for (int p = blockIdx.x * blockDim.x + threadIdx.x; p < full; p += gridDim.x * blockDim.x) {
+      for (int p = blockIdx.x * kMoveThreads + threadIdx.x; p < full; p += gridDim.x * kMoveThreads) {
         const int page = from[p];
         to[p] = page;
         if (page >= 0 && page < c.n_pages) atomicAdd(c.refs + page, 1);
@@ -394,15 +400,16 @@ __global__ void __launch_bounds__(kPlan) k_compact_plan(View c, int32_t* map, in
   if (threadIdx.x == 0) *count = movers;
 }
 
-__global__ void __launch_bounds__(256) k_compact_move(View c, const int32_t* map, const int32_t* from,
-                                                      const int32_t* to, const int32_t* count) {
+__global__ void __launch_bounds__(kMoveThreads) k_compact_move(View c, const int32_t* map, const int32_t* from,
+                                                               const int32_t* to, const int32_t* count) {
   dependency_wait();
   const int n = *count;
-  const int64_t units = static_cast<int64_t>(n) * c.n_layers;
+  const int64_t chunks = chunks_of(c.page_bytes), units = static_cast<int64_t>(n) * c.n_layers * chunks;
   for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
-    const int i = static_cast<int>(u / c.n_layers), layer = static_cast<int>(u % c.n_layers);
-    copy_slots(c, layer, from[i], to[i], c.page_size, 0, 1);
-    if (layer == 0 && threadIdx.x == 0) {
+    const int64_t page = u / chunks, chunk = u - page * chunks;
+    const int i = static_cast<int>(page / c.n_layers), layer = static_cast<int>(page - static_cast<int64_t>(i) * c.n_layers);
+    copy_chunk(c, layer, from[i], to[i], c.page_size, chunk);
+    if (layer == 0 && chunk == 0 && threadIdx.x == 0) {
       c.refs[to[i]] = c.refs[from[i]];
       c.refs[from[i]] = 0;
     }
@@ -566,13 +573,12 @@ extern "C" int ai_cache_fork(const ai_cache* c, const int32_t* src_dev, const in
   int32_t* plan = static_cast<int32_t*>(workspace_dev);
   int32_t* length = plan + n;
   int32_t* fresh = length + n;
-  // parts of 16 KB of a page's K
-  const int64_t parts = (v.page_bytes + 16383) / 16384;
-  const dim3 grid(static_cast<unsigned>(parts < 64 ? parts : 64), v.n_layers < 1024 ? v.n_layers : 1024,
+  const int64_t chunks = chunks_of(v.page_bytes);
+  const dim3 grid(static_cast<unsigned>(chunks < 256 ? chunks : 256), v.n_layers < 1024 ? v.n_layers : 1024,
                   n < 1024 ? n : 1024);
   rc = done(launch_after(k_fork_plan, dim3(1), dim3(kPlan), 0, st, v, src_dev, dst_dev, n, plan, length, fresh));
   if (rc) return rc;
-  return done(launch_after(k_fork_move, grid, dim3(256), 0, st, v, src_dev, dst_dev, plan, length, n));
+  return done(launch_after(k_fork_move, grid, dim3(kMoveThreads), 0, st, v, src_dev, dst_dev, plan, length, n));
 }
 
 extern "C" int ai_cache_free(const ai_cache* c, const int32_t* seqs_dev, int32_t n, void* cuda_stream) {
@@ -598,5 +604,5 @@ extern "C" int ai_cache_compact(const ai_cache* c, void* workspace_dev, int64_t 
   int32_t* count = to + c->n_pages;
   rc = done(launch_after(k_compact_plan, dim3(1), dim3(kPlan), 0, st, v, map, from, to, count));
   if (rc) return rc;
-  return done(launch_after(k_compact_move, dim3(8 * device_sms()), dim3(256), 0, st, v, map, from, to, count));
+  return done(launch_after(k_compact_move, dim3(16 * device_sms()), dim3(kMoveThreads), 0, st, v, map, from, to, count));
 }
