@@ -464,10 +464,11 @@ __global__ void __launch_bounds__(Few<D, FP8>::kThreads, 1) k_attend_few(const R
           begun = true;
           // a head without a finite score so far: exponents against 0 (all e^-inf = 0)
           const float mu[2] = {m_run[0] == -INFINITY ? 0.f : m_run[0], m_run[1] == -INFINITY ? 0.f : m_run[1]};
-          // the weights, rounded once (bf16; fp8: f16) for the product with v;
-          // their sum is taken before that rounding
+          // the weights for the product with v, as two bf16 terms (16 bits; the
+          // products have time left: reading bounds) or, fp8, as one f16 (11
+          // bits); their sum is taken before that rounding
           const float lift = kLift - (e_run == -INFINITY ? 0.f : e_run);
-          uint32_t p[2][2];
+          uint32_t p[2][2], rest[2][2];
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
 #pragma unroll
@@ -480,7 +481,10 @@ __global__ void __launch_bounds__(Few<D, FP8>::kThreads, 1) k_attend_few(const R
                 const float v0 = lv[2 * j + i] + lift;
                 p[j][i] = transposed(pack_f16(exp2_approx(x0 + v0), exp2_approx(x1 + v0)));
               } else {
-                p[j][i] = transposed(pack_bf16(e0, e1));
+                const uint32_t top = pack_bf16(e0, e1);
+                p[j][i] = transposed(top);
+                rest[j][i] = transposed(
+                    pack_bf16(e0 - __uint_as_float(top << 16), e1 - __uint_as_float(top & 0xffff0000u)));
               }
             }
           }
@@ -494,6 +498,7 @@ __global__ void __launch_bounds__(Few<D, FP8>::kThreads, 1) k_attend_few(const R
                 uint32_t v4[4];
                 ldsm4t(v4, sv + L::at(j * 16 + vr, dd * 2 + vc));
                 mma<false>(o[dd], v4, p[j][0], p[j][1]);
+                mma<false>(o[dd], v4, rest[j][0], rest[j][1]);
               }
           } else {
             // 16-bit transposed loads bring two neighbouring codes of two keys: row
