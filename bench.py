@@ -66,6 +66,12 @@ def parse():
     p.add_argument("--decode", type=int, default=0,
                    help="also time N decode steps after the prefill (one key appended, one query "
                         "selected per step) with route+refine and with the exhaustive selection")
+    p.add_argument("--attend", type=int, default=0,
+                   help="also time the attention over the selected keys, with this many query heads: the last "
+                        "chunk selected and attended, the same chunk attended densely, and (with --decode) "
+                        "whole decode steps")
+    p.add_argument("--attend-kv", type=int, default=1, help="key heads of the attention's cache")
+    p.add_argument("--attend-dtype", default="bf16", choices=["bf16", "fp8"], help="type of the attention's cache")
     p.add_argument("--mode", default="replicas", choices=["replicas", "sharded"],
                    help="N > 1: replicas = an independent request per rank (weak scaling); sharded = one "
                         "request, every rank rescoring its share of each candidate list, partial top-k "
@@ -647,6 +653,89 @@ def measure_decode(wl, args, dev, stream, n_steps):
                                                   res["route_refine"]["us_per_token"], 2)}
 
 
+def measure_attend(wl, args, dev, stream, n_steps):
+    """A layer's attention next to its selection: the workload's prefill into an
+    index and a paged cache (random keys and values, head_dim 128, pages of 64),
+    then, with CUDA events: the last chunk selected, selected and attended
+    (AttentionIndex.attend), attended over its whole prefix (attend_prompt), and
+    decode steps (append, seal, extend, write, attend)."""
+    import torch
+    from ivf_top_key_b200 import AttentionIndex, PagedCache, attend_prompt
+    T, L, Hq, Hkv, D, page = wl.T, wl.L, args.attend, args.attend_kv, 128, 64
+    wl_d = S.scaled(wl, L=L + n_steps)
+    idx = AttentionIndex(d=wl.d, H=wl.H, key_dtype=wl.key_dtype, q_dtype=wl.q_dtype,
+                         n_sinks=wl.n_sinks, window=wl.window,
+                         clusters_per_window=wl.clusters_per_window,
+                         refit_period=wl.refit_period, seal_iters=wl.seal_iters, async_refit=True,
+                         max_query_chunk=T, max_budget=wl.budget, max_k=wl.k, max_keys=L + n_steps,
+                         seed=wl.seed, block_routing=wl.block_routing)
+    pages = -(-(L + n_steps) // page)
+    cache = PagedCache(n_pages=pages, page_size=page, n_kv_heads=Hkv, head_dim=D, n_seqs=1, max_pages=pages,
+                       dtype=args.attend_dtype)
+    g = torch.Generator(device=dev)
+    g.manual_seed(1)
+    new = torch.empty(2, L + n_steps, Hkv, D, dtype=torch.bfloat16, device=dev).normal_(generator=g)
+    q = torch.empty(T, Hq, D, dtype=torch.bfloat16, device=dev).normal_(generator=g)
+    one = torch.zeros(1, dtype=torch.int32, device=dev)
+
+    def grow(p0, p1):
+        n = torch.tensor([p1 - p0], dtype=torch.int32, device=dev)
+        cache.extend(one, n)
+        cache.write(one, torch.tensor([0, p1 - p0], dtype=torch.int32, device=dev), new[0, p0:p1], new[1, p0:p1])
+
+    for c in range(wl.n_chunks):
+        kd, ks = chunk_keys_dev(wl, c * T, (c + 1) * T, dev)
+        idx.append_keys(kd, ks)
+        idx.seal()
+        grow(c * T, (c + 1) * T)
+    idx.publish()
+    cache.check()
+    p0 = L - T
+    qd, wd = queries_dev(wl, p0, L, dev)
+    ids = torch.empty((T, wl.k), dtype=torch.int32, device=dev)
+    out = torch.empty_like(q)
+    cu_q = torch.tensor([0, T], dtype=torch.int32, device=dev)
+    cu_k = torch.tensor([0, L], dtype=torch.int32, device=dev)
+
+    def timed(fn, reps=5):
+        fn()
+        e0, e1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        e0.record(stream)
+        for _ in range(reps):
+            fn()
+        e1.record(stream)
+        torch.cuda.synchronize()
+        return round(e0.elapsed_time(e1) / reps, 4)
+
+    res = {"query_heads": Hq, "key_heads": Hkv, "head_dim": D, "cache": args.attend_dtype, "chunk": T, "k": wl.k,
+           "prefix_tokens": L,
+           "select_ms": timed(lambda: idx.route_refine(qd, wd, p0, wl.k, wl.budget, out=ids)),
+           "select_and_attend_ms": timed(lambda: idx.attend(qd, wd, p0, wl.k, wl.budget, q, cache, out=out, out_ids=ids)),
+           "attend_selected_ms": timed(lambda: cache.attend_selected(q, ids, torch.zeros(T, dtype=torch.int32, device=dev),
+                                                                     out=out)),
+           "attend_all_ms": timed(lambda: attend_prompt(q, new[0, :L], new[1, :L], cu_q, cu_k, out=out))}
+    if n_steps:
+        kd, ks = chunk_keys_dev(wl_d, L, L + n_steps, dev)
+        qd, wd = queries_dev(wl_d, L, L + n_steps, dev)
+        cu, n1 = torch.tensor([0, 1], dtype=torch.int32, device=dev), torch.ones(1, dtype=torch.int32, device=dev)
+        e0, e1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        for i in range(n_steps):
+            if i == min(8, n_steps - 1):
+                e0.record(stream)
+                first = i
+            idx.append_keys(kd[i:i + 1], None if ks is None else ks[i:i + 1])
+            idx.seal()
+            cache.extend(one, n1)
+            cache.write(one, cu, new[0, L + i:L + i + 1], new[1, L + i:L + i + 1])
+            idx.attend(qd[i:i + 1], wd[i:i + 1], L + i, wl.k, wl.budget, q[:1], cache, out=out[:1], out_ids=ids[:1])
+        e1.record(stream)
+        idx.sync()
+        res["decode_us_per_token"] = round(e0.elapsed_time(e1) * 1e3 / (n_steps - first), 2)
+    cache.check()
+    idx.close()
+    return res
+
+
 def run_ours(args):
     import torch
     import torch.distributed as dist
@@ -688,6 +777,7 @@ def run_ours(args):
                              "best of 20 (read bytes)",
               "note": f"key store {wl.L * wl.d * 2 >> 20} MiB fits L2: rows are served from L2"}
     dec = measure_decode(wl, args, dev, stream, args.decode) if args.decode else None
+    att = measure_attend(wl, args, dev, stream, args.decode) if args.attend else None
     cpu = None
     if rank == 0 and world == 1 and not args.no_cpu_baseline:
         cpu = oracle_baseline(wl, args.cpu_sample)
@@ -713,6 +803,8 @@ def run_ours(args):
         }
         if dec is not None:
             line["decode"] = dec
+        if att is not None:
+            line["attend"] = att
         if r1m is not None:
             line["at_1m"] = {
                 "workload": "glm_bf16_L1m", "prefix_tokens": wl1.L, "clusters": r1m["nC"],
