@@ -334,14 +334,18 @@ def ai_attend_workspace(n_heads: int, n_kv_heads: int, head_dim: int) -> int:
 
 def ai_attend_cached(cache: AiCache, layer: int, q, n_rows: int, n_heads: int, seqs, scale: float, out, lse,
                      workspace, workspace_bytes: int, stream: int):
-    _check(_lib.ai_attend_cached(ctypes.byref(cache), layer, q, n_rows, n_heads, seqs, scale, out, lse, workspace,
-                                 workspace_bytes, stream))
+    rc = _lib.ai_attend_cached(ctypes.byref(cache), layer, q, n_rows, n_heads, seqs, scale, out, lse, workspace,
+                               workspace_bytes, stream)
+    if rc:
+        _check(rc)
 
 
 def ai_attend_selected(cache: AiCache, layer: int, q, ids, T: int, k: int, n_heads: int, seqs, scale: float, out, lse,
                        workspace, workspace_bytes: int, stream: int):
-    _check(_lib.ai_attend_selected(ctypes.byref(cache), layer, q, ids, T, k, n_heads, seqs, scale, out, lse, workspace,
-                                   workspace_bytes, stream))
+    rc = _lib.ai_attend_selected(ctypes.byref(cache), layer, q, ids, T, k, n_heads, seqs, scale, out, lse, workspace,
+                                 workspace_bytes, stream)
+    if rc:
+        _check(rc)
 
 
 def ai_cache_workspace(cache: AiCache, n: int) -> int:

@@ -23,6 +23,7 @@ from . import _capi as C
 
 _INT, _BF16, _F32 = torch.int32, torch.bfloat16, torch.float32
 _CODES = (torch.uint8, torch.float8_e4m3fn)
+_HERE = contextlib.nullcontext()
 
 
 def _need(ok: bool, what: str):
@@ -44,16 +45,14 @@ def _entered(device: torch.device, stream):
         yield
 
 
-_HERE = contextlib.nullcontext()
-
-
 def _on(device: torch.device, stream):
-    """Context in which the call's memory belongs to its stream, and that stream's handle."""
+    """The handle of the call's stream, and the context in which the call's memory belongs to that stream: None where
+    the caller is in it already."""
     if stream is None:
-        s = torch._C._cuda_getCurrentRawStream(device.index)
-        return (_HERE if device.index == torch._C._cuda_getDevice() else torch.cuda.device(device)), s
+        handle = torch._C._cuda_getCurrentRawStream(device.index)
+        return handle, None if device.index == torch._C._cuda_getDevice() else torch.cuda.device(device)
     _need(stream.device == device, "the stream must be on the tensors' device")
-    return _entered(device, stream), stream.cuda_stream
+    return stream.cuda_stream, _entered(device, stream)
 
 
 @functools.lru_cache(maxsize=None)
@@ -68,26 +67,29 @@ def _gpu(t: torch.Tensor, what: str) -> torch.device:
 
 def _view(k, v, tables, lens, refs=None, k_scale=None, v_scale=None, status=None):
     """The ai_cache of these tensors, and their device."""
-    dev = _gpu(tables, "tables")
-    _need(tables.dim() == 2, "tables must be [n_seqs, max_pages]")
-    shape = k.shape
-    _need(len(shape) in (4, 5), "k must be [n_layers, n_pages, page_size, n_kv_heads, head_dim] or one layer of it")
-    kind = k.dtype
+    dev = tables.device
+    shape, kind, rows = k.shape, k.dtype, tables.shape
     fp8 = kind is not _BF16
-    _need(not fp8 or kind in _CODES, "the cache holds bfloat16, or e4m3 codes")
-    _need(fp8 == (k_scale is not None) and fp8 == (v_scale is not None),
-          "k_scale and v_scale go with e4m3 codes, and only with them")
-    n_seqs, width = tables.shape
+    if not tables.is_cuda:
+        raise ValueError("tables must be on the GPU")
+    if len(rows) != 2:
+        raise ValueError("tables must be [n_seqs, max_pages]")
+    if not 4 <= len(shape) <= 5:
+        raise ValueError("k must be [n_layers, n_pages, page_size, n_kv_heads, head_dim] or one layer of it")
+    if fp8 and kind not in _CODES:
+        raise ValueError("the cache holds bfloat16, or e4m3 codes")
+    if fp8 != (k_scale is not None) or fp8 != (v_scale is not None):
+        raise ValueError("k_scale and v_scale go with e4m3 codes, and only with them")
     n_pages, page, heads, D = shape[-4:]
     return C.AiCache(
         _dense(k, kind, dev, "k"), _dense(v, kind, dev, "v", shape),
         _dense(k_scale, _F32, dev, "k_scale", shape[:-1]) if fp8 else None,
         _dense(v_scale, _F32, dev, "v_scale", shape[:-1]) if fp8 else None,
-        _dense(tables, _INT, dev, "tables"), _dense(lens, _INT, dev, "lens", (n_seqs,)),
+        _dense(tables, _INT, dev, "tables"), _dense(lens, _INT, dev, "lens", rows[:1]),
         None if refs is None else _dense(refs, _INT, dev, "refs", (n_pages,)),
         None if status is None else _dense(status, _INT, dev, "status", (1,)),
-        C.AI_FP8E4M3 if fp8 else C.AI_BF16, shape[0] if len(shape) == 5 else 1, n_pages, page, heads, D, n_seqs,
-        width), dev
+        C.AI_FP8E4M3 if fp8 else C.AI_BF16, shape[0] if len(shape) == 5 else 1, n_pages, page, heads, D, rows[0],
+        rows[1]), dev
 
 
 def _list(t, dev, what: str, n=None):
@@ -109,44 +111,57 @@ def attend_prompt(q, k, v, cu_q, cu_k=None, *, scale=None, out=None, out_lse=Non
     for t in (q, k, v):
         if t.dim() != 3 or t.dtype is not _BF16 or t.device != dev or (t.stride(2) != 1 and t.shape[2] != 1):
             raise ValueError(f"q, k and v must be torch.bfloat16 [tokens, heads, head_dim] on {dev}, the last dimension dense")
-    _need(v.shape == k.shape and k.shape[2] == q.shape[2], "k and v must be [total_k, n_kv_heads, head_dim of q]")
-    _need(cu_q.dim() == 1 and cu_q.shape[0] >= 1, "cu_q must be [n_seqs + 1]")
-    pq, pk = _dense(cu_q, _INT, dev, "cu_q"), _dense(cu_k, _INT, dev, "cu_k", cu_q.shape)
     T, Hq, D = q.shape
-    ctx, st = _on(dev, stream)
-    with ctx:
+    if v.shape != k.shape or k.shape[2] != D:
+        raise ValueError("k and v must be [total_k, n_kv_heads, head_dim of q]")
+    if cu_q.dim() != 1 or cu_q.shape[0] < 1:
+        raise ValueError("cu_q must be [n_seqs + 1]")
+    pq, pk = _dense(cu_q, _INT, dev, "cu_q"), _dense(cu_k, _INT, dev, "cu_k", cu_q.shape)
+    st, ctx = _on(dev, stream)
+    po = None if out is None else _dense(out, _BF16, dev, "out", (T, Hq, D))
+    pl = None if out_lse is None else _dense(out_lse, _F32, dev, "out_lse", (T, Hq))
+    ps = None if status is None else _dense(status, _INT, dev, "status", (1,))
+    with ctx or _HERE:
         if out is None:
-            out = torch.empty((T, Hq, D), dtype=_BF16, device=dev)
+            out = q.new_empty((T, Hq, D))
+            po = out.data_ptr()
         C.ai_attend_prompt(q.data_ptr(), q.stride()[:2], k.data_ptr(), k.stride()[:2], v.data_ptr(), v.stride()[:2],
                            pq, pk, cu_q.shape[0] - 1, T, k.shape[0], Hq, k.shape[1], D,
-                           D ** -0.5 if scale is None else scale, _dense(out, _BF16, dev, "out", (T, Hq, D)),
-                           None if out_lse is None else _dense(out_lse, _F32, dev, "out_lse", (T, Hq)),
-                           None if status is None else _dense(status, _INT, dev, "status", (1,)), st)
+                           D ** -0.5 if scale is None else scale, po, pl, ps, st)
     return out
 
 
 def _rows(q, ids, cache, dev, seqs, layer, scale, out, out_lse, stream):
-    _need(q.dim() == 3, "q must be [rows, heads, head_dim]")
+    shape = q.shape
+    if len(shape) != 3 or shape[2] != cache.head_dim:
+        raise ValueError("q must be [rows, heads, head_dim of the cache]")
+    T, Hq, D = shape
     pq = _dense(q, _BF16, dev, "q")
-    T, Hq, D = q.shape
-    _need(D == cache.head_dim, "q and the cache must have the same head_dim")
     ps = None if seqs is None else _list(seqs, dev, "seqs", T)
+    po = None if out is None else _dense(out, _BF16, dev, "out", shape)
+    pl = None if out_lse is None else _dense(out_lse, _F32, dev, "out_lse", shape[:2])
     if ids is not None:
-        _need(ids.dim() == 2 and ids.shape[0] == T, "ids must be [rows, k]")
+        if ids.dim() != 2 or ids.shape[0] != T:
+            raise ValueError("ids must be [rows, k]")
         pi = _dense(ids, _INT, dev, "ids")
-    scale = D ** -0.5 if scale is None else scale
-    ctx, st = _on(dev, stream)
-    with ctx:
+    if scale is None:
+        scale = D ** -0.5
+    st, ctx = _on(dev, stream)
+    if ctx is not None:
+        ctx.__enter__()
+    try:
         if out is None:
-            out = torch.empty((T, Hq, D), dtype=_BF16, device=dev)
-        po = _dense(out, _BF16, dev, "out", (T, Hq, D))
-        pl = None if out_lse is None else _dense(out_lse, _F32, dev, "out_lse", (T, Hq))
+            out = torch.empty_like(q)
+            po = out.data_ptr()
         n = _attend_workspace(dev.index, Hq, cache.n_kv_heads, D)
-        ws = torch.empty(n, dtype=torch.uint8, device=dev)
+        ws = q.new_empty((n + 1) // 2)
         if ids is None:
             C.ai_attend_cached(cache, layer, pq, T, Hq, ps, scale, po, pl, ws.data_ptr(), n, st)
         else:
             C.ai_attend_selected(cache, layer, pq, pi, T, ids.shape[1], Hq, ps, scale, po, pl, ws.data_ptr(), n, st)
+    finally:
+        if ctx is not None:
+            ctx.__exit__(None, None, None)
     return out
 
 
@@ -184,8 +199,8 @@ def cache_extend(k, v, tables, lens, refs, seqs, counts, *, k_scale=None, v_scal
     c, dev = _view(k, v, tables, lens, refs, k_scale, v_scale, status)
     ps, n = _list(seqs, dev, "seqs"), seqs.shape[0]
     pc = _list(counts, dev, "counts", n)
-    ctx, st = _on(dev, stream)
-    with ctx:
+    st, ctx = _on(dev, stream)
+    with ctx or _HERE:
         ws, need = _workspace(c, n, dev)
         C.ai_cache_extend(c, ps, pc, n, ws.data_ptr(), need, st)
 
@@ -198,8 +213,8 @@ def cache_write(k, v, tables, lens, seqs, cu, new_k, new_v, *, layer: int = 0, k
     pc = _list(cu, dev, "cu", n + 1)
     shape = (new_k.shape[0], c.n_kv_heads, c.head_dim)
     pk, pv = _dense(new_k, _BF16, dev, "new_k", shape), _dense(new_v, _BF16, dev, "new_v", shape)
-    ctx, st = _on(dev, stream)
-    with ctx:
+    st, ctx = _on(dev, stream)
+    with ctx or _HERE:
         C.ai_cache_write(c, layer, pk, pv, ps, pc, n, shape[0], st)
 
 
@@ -208,8 +223,8 @@ def cache_fork(k, v, tables, lens, refs, src, dst, *, k_scale=None, v_scale=None
     c, dev = _view(k, v, tables, lens, refs, k_scale, v_scale, status)
     ps, n = _list(src, dev, "src"), src.shape[0]
     pd = _list(dst, dev, "dst", n)
-    ctx, st = _on(dev, stream)
-    with ctx:
+    st, ctx = _on(dev, stream)
+    with ctx or _HERE:
         ws, need = _workspace(c, n, dev)
         C.ai_cache_fork(c, ps, pd, n, ws.data_ptr(), need, st)
 
@@ -223,16 +238,16 @@ def cache_free(tables, lens, refs, seqs, *, page_size: int, status=None, stream=
                   None if status is None else _dense(status, _INT, dev, "status", (1,)),
                   0, 0, refs.shape[0], page_size, 0, 0, *tables.shape)
     ps = _list(seqs, dev, "seqs")
-    ctx, st = _on(dev, stream)
-    with ctx:
+    st, ctx = _on(dev, stream)
+    with ctx or _HERE:
         C.ai_cache_free(c, ps, seqs.shape[0], st)
 
 
 def cache_compact(k, v, tables, lens, refs, *, k_scale=None, v_scale=None, status=None, stream=None):
     """Move the live pages to the front of the cache (ai_cache_compact)."""
     c, dev = _view(k, v, tables, lens, refs, k_scale, v_scale, status)
-    ctx, st = _on(dev, stream)
-    with ctx:
+    st, ctx = _on(dev, stream)
+    with ctx or _HERE:
         ws, need = _workspace(c, 0, dev)
         C.ai_cache_compact(c, ws.data_ptr(), need, st)
 
