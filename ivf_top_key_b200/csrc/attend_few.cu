@@ -16,7 +16,10 @@
 // hand over their states in two buffers that joining warps read, so that
 // no row waits for the one before it.
 //
-// Bound by reading keys and values: 4 x 131072 tokens, 8 key heads, bf16.
+// Measured: 4 x 131072 tokens of 8 key heads, bf16: 317 us, 6.8 TB/s (a plain
+// read of the same bytes); 48 sequences of up to 8192 tokens, fp8: 109 us, 4.2
+// TB/s.  What bounds fp8 is the widening: half of the issue slots and 46 % of the
+// ALU slots (tiles of 64 keys and ten computing warps measured the same).
 #include "attend_rows.cuh"
 
 namespace aiidx {
@@ -113,45 +116,45 @@ __global__ void __launch_bounds__(Few<D, FP8>::kThreads, 1) k_attend_few(const R
       constexpr int kNext = 8 * L::kState;
 #pragma unroll
       for (int r = j / 8; r < 8; r += kJoiners * 4) {
-      const float* from = states + buf * L::kStates + r * L::kState;
-      float m = -INFINITY, l = 0.f;
+        const float* from = states + buf * L::kStates + r * L::kState;
+        float m = -INFINITY, l = 0.f;
 #pragma unroll
-      for (int i = 0; i < kComp; ++i) m = fmaxf(m, from[i * kNext + D]);
-      const float mz = m == -INFINITY ? 0.f : m;
-      float4 y[D / 32];
+        for (int i = 0; i < kComp; ++i) m = fmaxf(m, from[i * kNext + D]);
+        const float mz = m == -INFINITY ? 0.f : m;
+        float4 y[D / 32];
 #pragma unroll
-      for (int c = 0; c < D / 32; ++c) y[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int c = 0; c < D / 32; ++c) y[c] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int i = 0; i < kComp; ++i) {
-        const float2 ml = *reinterpret_cast<const float2*>(from + i * kNext + D);
-        if (ml.y == 0.f) continue;                  // nothing seen: its output is not written
-        const float f = exp2_approx(ml.x - mz);
-        l += ml.y * f;
+        for (int i = 0; i < kComp; ++i) {
+          const float2 ml = *reinterpret_cast<const float2*>(from + i * kNext + D);
+          if (ml.y == 0.f) continue;                  // nothing seen: its output is not written
+          const float f = exp2_approx(ml.x - mz);
+          l += ml.y * f;
 #pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
-          const float4 z = *reinterpret_cast<const float4*>(from + i * kNext + c * 32 + c0);
-          y[c].x = fmaf(z.x, f, y[c].x);
-          y[c].y = fmaf(z.y, f, y[c].y);
-          y[c].z = fmaf(z.z, f, y[c].z);
-          y[c].w = fmaf(z.w, f, y[c].w);
+          for (int c = 0; c < D / 32; ++c) {
+            const float4 z = *reinterpret_cast<const float4*>(from + i * kNext + c * 32 + c0);
+            y[c].x = fmaf(z.x, f, y[c].x);
+            y[c].y = fmaf(z.y, f, y[c].y);
+            y[c].z = fmaf(z.z, f, y[c].z);
+            y[c].w = fmaf(z.w, f, y[c].w);
+          }
         }
-      }
-      if (r < a.G) {
-        const int64_t at = static_cast<int64_t>(x.row) * a.Hq + x.head * a.G + r;
-        if (x.slot < 0) {
-          const float inv = l == 0.f ? 0.f : 1.f / l;
+        if (r < a.G) {
+          const int64_t at = static_cast<int64_t>(x.row) * a.Hq + x.head * a.G + r;
+          if (x.slot < 0) {
+            const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
-          for (int c = 0; c < D / 32; ++c)
-            *reinterpret_cast<uint2*>(a.out + at * D + c * 32 + c0) =
-                make_uint2(pack_bf16(y[c].x * inv, y[c].y * inv), pack_bf16(y[c].z * inv, y[c].w * inv));
-          if (a.lse && c0 == 0) a.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
-        } else {
-          float* part = a.part + (static_cast<int64_t>(cta * 2 + x.slot) * 8 + r) * L::kState;
+            for (int c = 0; c < D / 32; ++c)
+              *reinterpret_cast<uint2*>(a.out + at * D + c * 32 + c0) =
+                  make_uint2(pack_bf16(y[c].x * inv, y[c].y * inv), pack_bf16(y[c].z * inv, y[c].w * inv));
+            if (a.lse && c0 == 0) a.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+          } else {
+            float* part = a.part + (static_cast<int64_t>(cta * 2 + x.slot) * 8 + r) * L::kState;
 #pragma unroll
-          for (int c = 0; c < D / 32; ++c) *reinterpret_cast<float4*>(part + c * 32 + c0) = y[c];
-          if (c0 == 0) *reinterpret_cast<float2*>(part + D) = make_float2(m, l);
+            for (int c = 0; c < D / 32; ++c) *reinterpret_cast<float4*>(part + c * 32 + c0) = y[c];
+            if (c0 == 0) *reinterpret_cast<float2*>(part + D) = make_float2(m, l);
+          }
         }
-      }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&st_free[buf]);

@@ -27,6 +27,17 @@
 // Rows behind the sequence's end are zeroed there; if a value before it is not
 // finite, the item is computed again by attend_row, which reads only the keys
 // that each row sees.
+//
+// Measured: 16384 tokens, 16 heads on 2, D = 128: 0.89 ms in a short run (1230
+// TFLOP/s, 0.75 of the measured bf16 product), 1.02 ms in a long one; a chunk of
+// 8192 queries of 64 heads on 131072 keys 28 ms (1200 TFLOP/s).  What bounds it:
+// with N = 128 the products with K alone read shared memory as long as they
+// compute, next to the loads' writes and V (2048 cycles of each for the two
+// tiles and 128 keys; measured 3800).  Tried and not kept: two 64-key score
+// buffers a tile (1.11 ms: products with N = 64 read more than they compute), the
+// product with V begun at half of the weights (0.93 ms), waits that spin.
+// D = 64: 4 chunks of up to 2048 queries on up to 4548 keys 137 us; the weights
+// bound it, an eighth of which the FMA pipes take (160 -> 152 us in a short run).
 #include <cudaTypedefs.h>
 
 #include <cmath>
@@ -380,220 +391,220 @@ __global__ void __launch_bounds__(kThreads, 1)
   // the rows' warps take registers that the others do not need (8 x 208 + 4 x
   // 88 a lane, as many as the block was launched with: 12 x 168)
   if (warp >= 8) {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-  if (warp == 8) {
-    // ---------------------------------------------------------- TMA loads
-    const bool leader = elect_one();
-    uint32_t g = 0, nq[2] = {0, 0};
-    // by slot: parity of the next phase of its two barriers, and which one
-    // its last load completes on
-    uint32_t kv_next = 0, mx_next = 0, last_mx = 0;
-    bool ok = true;
-    auto all = [&](bool x) { return __all_sync(0xffffffffu, x); };
-    uint32_t r = 0;
-    for (int64_t it = blockIdx.x; ok && it >= 0; ++r) {
-      // the next item is asked for while this one is loaded
-      if (r >= 2 && !all(mbar_wait(&next_read[r & 1], ((r >> 1) - 1) & 1, err, abort))) break;
-      if (leader) take_request(&answer[r & 1], &next_full[r & 1]);
-      const Item x = item_at(a, sc, it);
-      for (int i = 0; ok && i < 2; ++i) {
-        if (x.tiles[i] == 0) continue;
-        if (nq[i] > 0 && !all(mbar_wait(&q_empty[i], (nq[i] - 1) & 1, err, abort))) {
-          ok = false;
-          break;
-        }
-        if (leader) {
-          mbar_arrive_expect_tx(&q_full[i], sc.tpt * a.G * D * 2);
-          for (int c = 0; c < L::kHalves; ++c)
-            tma_load_3d(sq + i * L::kTileBytes + c * (kTile * 128), &map_q, c * 64, x.head * a.G, x.qtok + i * sc.tpt,
-                        &q_full[i]);
-        }
-        ++nq[i];
-      }
-      const int n = x.n();
-      for (int t = 0; ok && t < 2 * n; ++t, ++g) {  // K 0, V 0, K 1, V 1, ..
-        const int s = g % kSlots;
-        if (g >= kSlots && !all(mbar_wait(&kv_empty[s], (g / kSlots - 1) & 1, err, abort))) {
-          ok = false;
-          break;
-        }
-        const bool mx = (t & 1) && x.mixed(t >> 1);
-        uint64_t* full = mx ? &mx_full[s] : &kv_full[s];
-        if (mx) {
-          mx_next ^= 1u << s;
-          last_mx |= 1u << s;
-        } else {
-          kv_next ^= 1u << s;
-          last_mx &= ~(1u << s);
-        }
-        if (leader) {
-          mbar_arrive_expect_tx(full, L::kTileBytes);
-          for (int c = 0; c < L::kHalves; ++c)
-            tma_load_3d(ring + s * L::kTileBytes + c * (kTile * 128), t & 1 ? &map_v : &map_k, c * 64, x.head,
-                        x.k0 + (t >> 1) * kTile, full);
-        }
-      }
-      if (ok) it = next_item(r);
-    }
-    if (*reinterpret_cast<volatile int*>(abort)) {
-      // copies that this warp asked for may still be landing: bounded waits
-      for (uint32_t s = 0; s < min(g, static_cast<uint32_t>(kSlots)); ++s) {
-        const bool mx = (last_mx >> s) & 1;
-        mbar_drain(mx ? &mx_full[s] : &kv_full[s], (((mx ? mx_next : kv_next) >> s) & 1) ^ 1);
-      }
-      for (int i = 0; i < 2; ++i)
-        if (nq[i] > 0) mbar_drain(&q_full[i], (nq[i] - 1) & 1);
-      if (r > 0) mbar_drain(&next_full[(r - 1) & 1], ((r - 1) >> 1) & 1);
-    }
-    __syncwarp();
-  } else if (warp == 9) {
-    // ----------------------------------------------------------- products
-    // The whole warp follows the loop and one elected lane issues: the operands
-    // stay in uniform registers (issued from a one-lane branch, each product
-    // first moved its descriptors there: 4700 cycles a tile pair for what the
-    // tensor cores do in 2048).
-    constexpr uint32_t id_s = idesc_bf16_f32(kTile, kTile);
-    constexpr uint32_t id_o = idesc_bf16_f32(kTile, D) | (1u << 16);  // B is N-major
-    const bool leader = elect_one();
-    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-    const uint64_t q_desc = sdesc_sw128(smem_u32(sq)), k_desc = sdesc_sw128(smem_u32(ring));
-    const uint64_t v_desc = sdesc_sw128_mn(smem_u32(ring), kTile * 128);
-    constexpr uint32_t kTileStep = L::kTileBytes >> 4;   // in descriptor units
-    uint32_t slot = 0, nq[2] = {0, 0}, np[2] = {0, 0}, clean = 0, full = 0;  // next slot and parities by slot
-    bool ok = true;
-    auto all = [&](bool x) { return __all_sync(0xffffffffu, x); };
-    auto wait_slot = [&](uint32_t s) {
-      const uint32_t parity = (full >> s) & 1;
-      full ^= 1u << s;
-      return all(mbar_wait(&kv_full[s], parity, err, abort));
-    };
-    auto after = [&](uint32_t s) { return s + 1 == kSlots ? 0 : s + 1; };
-    auto scores = [&](int i, uint32_t s) {  // S_i = Q_i K^T
-      if (leader) {
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          constexpr uint32_t kHalf = kTile * 128 >> 4;
-          const uint32_t off = (kk >> 2) * kHalf + (kk & 3) * 2;
-          umma_bf16(tm + kColS + i * 128, q_desc + (i * kTileStep + off), k_desc + (s * kTileStep + off), id_s, kk > 0);
-        }
-        umma_commit(&s_full[i]);
-      }
-    };
-    auto outputs = [&](int i, uint32_t s, bool first, bool last) {  // O_i (+)= P_i V
-      if (leader) {
-#pragma unroll
-        for (int kk = 0; kk < kTile / 16; ++kk)
-          umma_bf16_ta(tm + kColO + i * 128, tm + kColS + i * 128 + kk * 8,
-                       v_desc + (s * kTileStep + kk * (16 * 128 >> 4)), id_o, !first || kk > 0);
-        if (last) umma_commit(&o_full[i]);
-      }
-    };
-    auto commit = [&](uint64_t* bar) {
-      if (leader) umma_commit(bar);
-    };
-    uint32_t r = 0;
-    for (int64_t it = blockIdx.x; ok && it >= 0; it = next_item(r++)) {
-      const Item x = item_at(a, sc, it);
-      const int n = x.n();
-      if (n == 0) continue;
-      ok = wait_slot(slot);
-      for (int i = 0; ok && i < 2; ++i) {
-        if (x.tiles[i] == 0) continue;
-        if (!all(mbar_wait(&q_full[i], nq[i] & 1, err, abort))) {
-          ok = false;
-          break;
-        }
-        ++nq[i];
-        tc_fence_after();
-        scores(i, slot);
-        if (x.tiles[i] == 1) commit(&q_empty[i]);
-      }
-      if (!ok) break;
-      commit(&kv_empty[slot]);
-      slot = after(slot);
-      for (int j = 0; ok && j < n; ++j) {
-        const uint32_t sv = slot, sk = after(slot);
-        if (x.mixed(j)) {
-          ok = all(mbar_wait(&v_clean[sv], (clean >> sv) & 1, err, abort));
-          clean ^= 1u << sv;
-        } else {
-          ok = wait_slot(sv);
-        }
-        if (ok && j + 1 < n) ok = wait_slot(sk);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          if (!ok) break;
-          if (j < x.tiles[i]) {
-            if (!all(mbar_wait(&p_full[i], np[i] & 1, err, abort))) {
-              ok = false;
-              break;
-            }
-            ++np[i];
-            tc_fence_after();
-            outputs(i, sv, j == 0, j + 1 == x.tiles[i]);
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if (warp == 8) {
+      // ---------------------------------------------------------- TMA loads
+      const bool leader = elect_one();
+      uint32_t g = 0, nq[2] = {0, 0};
+      // by slot: parity of the next phase of its two barriers, and which one
+      // its last load completes on
+      uint32_t kv_next = 0, mx_next = 0, last_mx = 0;
+      bool ok = true;
+      auto all = [&](bool x) { return __all_sync(0xffffffffu, x); };
+      uint32_t r = 0;
+      for (int64_t it = blockIdx.x; ok && it >= 0; ++r) {
+        // the next item is asked for while this one is loaded
+        if (r >= 2 && !all(mbar_wait(&next_read[r & 1], ((r >> 1) - 1) & 1, err, abort))) break;
+        if (leader) take_request(&answer[r & 1], &next_full[r & 1]);
+        const Item x = item_at(a, sc, it);
+        for (int i = 0; ok && i < 2; ++i) {
+          if (x.tiles[i] == 0) continue;
+          if (nq[i] > 0 && !all(mbar_wait(&q_empty[i], (nq[i] - 1) & 1, err, abort))) {
+            ok = false;
+            break;
           }
-          if (i == 1) commit(&kv_empty[sv]);
-          if (j + 1 < x.tiles[i]) {
-            scores(i, sk);
-            if (j + 2 == x.tiles[i]) commit(&q_empty[i]);
+          if (leader) {
+            mbar_arrive_expect_tx(&q_full[i], sc.tpt * a.G * D * 2);
+            for (int c = 0; c < L::kHalves; ++c)
+              tma_load_3d(sq + i * L::kTileBytes + c * (kTile * 128), &map_q, c * 64, x.head * a.G, x.qtok + i * sc.tpt,
+                          &q_full[i]);
           }
-          if (i == 1 && j + 1 < n) commit(&kv_empty[sk]);
+          ++nq[i];
         }
-        slot = j + 1 < n ? after(sk) : sk;
+        const int n = x.n();
+        for (int t = 0; ok && t < 2 * n; ++t, ++g) {  // K 0, V 0, K 1, V 1, ..
+          const int s = g % kSlots;
+          if (g >= kSlots && !all(mbar_wait(&kv_empty[s], (g / kSlots - 1) & 1, err, abort))) {
+            ok = false;
+            break;
+          }
+          const bool mx = (t & 1) && x.mixed(t >> 1);
+          uint64_t* full = mx ? &mx_full[s] : &kv_full[s];
+          if (mx) {
+            mx_next ^= 1u << s;
+            last_mx |= 1u << s;
+          } else {
+            kv_next ^= 1u << s;
+            last_mx &= ~(1u << s);
+          }
+          if (leader) {
+            mbar_arrive_expect_tx(full, L::kTileBytes);
+            for (int c = 0; c < L::kHalves; ++c)
+              tma_load_3d(ring + s * L::kTileBytes + c * (kTile * 128), t & 1 ? &map_v : &map_k, c * 64, x.head,
+                          x.k0 + (t >> 1) * kTile, full);
+          }
+        }
+        if (ok) it = next_item(r);
       }
-    }
-    // every product issued has completed before the TMEM is released
-    for (int i = 0; i < 2; ++i) {
-      if (nq[i] > 0) mbar_drain(&o_full[i], (nq[i] - 1) & 1);
-      if (*reinterpret_cast<volatile int*>(abort) && nq[i] > 0) mbar_drain(&s_full[i], np[i] & 1);
-    }
-    __syncwarp();
-  } else {
-    // ------------------------------------------- V tiles that are seen in part
-    const int t = threadIdx.x - 320;
-    uint32_t g = 0, full = 0;
-    int item = 0;
-    bool ok = true;
-    if (blockIdx.x == 0)  // every sequence's offsets, whatever the schedule reaches
-      for (int b = t; b < a.n_seqs; b += 64) {
-        int q0, lq, k0, lk;
-        seq_rows(a, b, &q0, &lq, &k0, &lk);
+      if (*reinterpret_cast<volatile int*>(abort)) {
+        // copies that this warp asked for may still be landing: bounded waits
+        for (uint32_t s = 0; s < min(g, static_cast<uint32_t>(kSlots)); ++s) {
+          const bool mx = (last_mx >> s) & 1;
+          mbar_drain(mx ? &mx_full[s] : &kv_full[s], (((mx ? mx_next : kv_next) >> s) & 1) ^ 1);
+        }
+        for (int i = 0; i < 2; ++i)
+          if (nq[i] > 0) mbar_drain(&q_full[i], (nq[i] - 1) & 1);
+        if (r > 0) mbar_drain(&next_full[(r - 1) & 1], ((r - 1) >> 1) & 1);
       }
-    uint32_t r = 0;
-    for (int64_t it = blockIdx.x; ok && it >= 0; it = next_item(r++)) {
-      const Item x = item_at(a, sc, it);
-      const int n = x.n();
-      for (int j = 0; ok && j < n; ++j) {
-        if (!x.mixed(j)) continue;
-        const uint32_t e = g + 2 * j + 1;
-        const int s = e % kSlots;
-        ok = __all_sync(0xffffffffu, mbar_wait(&mx_full[s], (full >> s) & 1, err, abort));
-        if (!ok) break;
+      __syncwarp();
+    } else if (warp == 9) {
+      // ----------------------------------------------------------- products
+      // The whole warp follows the loop and one elected lane issues: the operands
+      // stay in uniform registers (issued from a one-lane branch, each product
+      // first moved its descriptors there: 4700 cycles a tile pair for what the
+      // tensor cores do in 2048).
+      constexpr uint32_t id_s = idesc_bf16_f32(kTile, kTile);
+      constexpr uint32_t id_o = idesc_bf16_f32(kTile, D) | (1u << 16);  // B is N-major
+      const bool leader = elect_one();
+      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+      const uint64_t q_desc = sdesc_sw128(smem_u32(sq)), k_desc = sdesc_sw128(smem_u32(ring));
+      const uint64_t v_desc = sdesc_sw128_mn(smem_u32(ring), kTile * 128);
+      constexpr uint32_t kTileStep = L::kTileBytes >> 4;   // in descriptor units
+      uint32_t slot = 0, nq[2] = {0, 0}, np[2] = {0, 0}, clean = 0, full = 0;  // next slot and parities by slot
+      bool ok = true;
+      auto all = [&](bool x) { return __all_sync(0xffffffffu, x); };
+      auto wait_slot = [&](uint32_t s) {
+        const uint32_t parity = (full >> s) & 1;
         full ^= 1u << s;
-        const int lo = max(0, x.see(0) - j * kTile), hi = min(kTile, x.lk - j * kTile);
-        uint32_t bad = 0;
-        // 16-byte unit u of the tile: row (u / 8) % 128; the swizzle stays within a row
-        for (int u = t; u < L::kTileBytes / 16; u += 64) {
-          const int row = (u >> 3) & (kTile - 1);
-          uint4* p = reinterpret_cast<uint4*>(ring + s * L::kTileBytes) + u;
-          if (row >= hi) {
-            *p = make_uint4(0, 0, 0, 0);
-          } else if (row >= lo) {
-            const uint4 w = *p;
-            // the carry out of an exponent of ones: infinity or NaN
-            bad |= ((w.x & 0x7f807f80u) + 0x00800080u) | ((w.y & 0x7f807f80u) + 0x00800080u) |
-                   ((w.z & 0x7f807f80u) + 0x00800080u) | ((w.w & 0x7f807f80u) + 0x00800080u);
+        return all(mbar_wait(&kv_full[s], parity, err, abort));
+      };
+      auto after = [&](uint32_t s) { return s + 1 == kSlots ? 0 : s + 1; };
+      auto scores = [&](int i, uint32_t s) {  // S_i = Q_i K^T
+        if (leader) {
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            constexpr uint32_t kHalf = kTile * 128 >> 4;
+            const uint32_t off = (kk >> 2) * kHalf + (kk & 3) * 2;
+            umma_bf16(tm + kColS + i * 128, q_desc + (i * kTileStep + off), k_desc + (s * kTileStep + off), id_s, kk > 0);
           }
+          umma_commit(&s_full[i]);
         }
-        if (bad & 0x80008000u) reinterpret_cast<volatile int*>(sick)[item % L::kSick] = item + 1;
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&v_clean[s]);
+      };
+      auto outputs = [&](int i, uint32_t s, bool first, bool last) {  // O_i (+)= P_i V
+        if (leader) {
+#pragma unroll
+          for (int kk = 0; kk < kTile / 16; ++kk)
+            umma_bf16_ta(tm + kColO + i * 128, tm + kColS + i * 128 + kk * 8,
+                         v_desc + (s * kTileStep + kk * (16 * 128 >> 4)), id_o, !first || kk > 0);
+          if (last) umma_commit(&o_full[i]);
+        }
+      };
+      auto commit = [&](uint64_t* bar) {
+        if (leader) umma_commit(bar);
+      };
+      uint32_t r = 0;
+      for (int64_t it = blockIdx.x; ok && it >= 0; it = next_item(r++)) {
+        const Item x = item_at(a, sc, it);
+        const int n = x.n();
+        if (n == 0) continue;
+        ok = wait_slot(slot);
+        for (int i = 0; ok && i < 2; ++i) {
+          if (x.tiles[i] == 0) continue;
+          if (!all(mbar_wait(&q_full[i], nq[i] & 1, err, abort))) {
+            ok = false;
+            break;
+          }
+          ++nq[i];
+          tc_fence_after();
+          scores(i, slot);
+          if (x.tiles[i] == 1) commit(&q_empty[i]);
+        }
+        if (!ok) break;
+        commit(&kv_empty[slot]);
+        slot = after(slot);
+        for (int j = 0; ok && j < n; ++j) {
+          const uint32_t sv = slot, sk = after(slot);
+          if (x.mixed(j)) {
+            ok = all(mbar_wait(&v_clean[sv], (clean >> sv) & 1, err, abort));
+            clean ^= 1u << sv;
+          } else {
+            ok = wait_slot(sv);
+          }
+          if (ok && j + 1 < n) ok = wait_slot(sk);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            if (!ok) break;
+            if (j < x.tiles[i]) {
+              if (!all(mbar_wait(&p_full[i], np[i] & 1, err, abort))) {
+                ok = false;
+                break;
+              }
+              ++np[i];
+              tc_fence_after();
+              outputs(i, sv, j == 0, j + 1 == x.tiles[i]);
+            }
+            if (i == 1) commit(&kv_empty[sv]);
+            if (j + 1 < x.tiles[i]) {
+              scores(i, sk);
+              if (j + 2 == x.tiles[i]) commit(&q_empty[i]);
+            }
+            if (i == 1 && j + 1 < n) commit(&kv_empty[sk]);
+          }
+          slot = j + 1 < n ? after(sk) : sk;
+        }
       }
-      g += 2 * n;
-      item += n > 0;
+      // every product issued has completed before the TMEM is released
+      for (int i = 0; i < 2; ++i) {
+        if (nq[i] > 0) mbar_drain(&o_full[i], (nq[i] - 1) & 1);
+        if (*reinterpret_cast<volatile int*>(abort) && nq[i] > 0) mbar_drain(&s_full[i], np[i] & 1);
+      }
+      __syncwarp();
+    } else {
+      // ------------------------------------------- V tiles that are seen in part
+      const int t = threadIdx.x - 320;
+      uint32_t g = 0, full = 0;
+      int item = 0;
+      bool ok = true;
+      if (blockIdx.x == 0)  // every sequence's offsets, whatever the schedule reaches
+        for (int b = t; b < a.n_seqs; b += 64) {
+          int q0, lq, k0, lk;
+          seq_rows(a, b, &q0, &lq, &k0, &lk);
+        }
+      uint32_t r = 0;
+      for (int64_t it = blockIdx.x; ok && it >= 0; it = next_item(r++)) {
+        const Item x = item_at(a, sc, it);
+        const int n = x.n();
+        for (int j = 0; ok && j < n; ++j) {
+          if (!x.mixed(j)) continue;
+          const uint32_t e = g + 2 * j + 1;
+          const int s = e % kSlots;
+          ok = __all_sync(0xffffffffu, mbar_wait(&mx_full[s], (full >> s) & 1, err, abort));
+          if (!ok) break;
+          full ^= 1u << s;
+          const int lo = max(0, x.see(0) - j * kTile), hi = min(kTile, x.lk - j * kTile);
+          uint32_t bad = 0;
+          // 16-byte unit u of the tile: row (u / 8) % 128; the swizzle stays within a row
+          for (int u = t; u < L::kTileBytes / 16; u += 64) {
+            const int row = (u >> 3) & (kTile - 1);
+            uint4* p = reinterpret_cast<uint4*>(ring + s * L::kTileBytes) + u;
+            if (row >= hi) {
+              *p = make_uint4(0, 0, 0, 0);
+            } else if (row >= lo) {
+              const uint4 w = *p;
+              // the carry out of an exponent of ones: infinity or NaN
+              bad |= ((w.x & 0x7f807f80u) + 0x00800080u) | ((w.y & 0x7f807f80u) + 0x00800080u) |
+                     ((w.z & 0x7f807f80u) + 0x00800080u) | ((w.w & 0x7f807f80u) + 0x00800080u);
+            }
+          }
+          if (bad & 0x80008000u) reinterpret_cast<volatile int*>(sick)[item % L::kSick] = item + 1;
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&v_clean[s]);
+        }
+        g += 2 * n;
+        item += n > 0;
+      }
     }
-  }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     // ------------------------------------------------------------ softmax

@@ -11,12 +11,19 @@
 // key and value is read once per group.  What bounds it is reading the keys
 // and values; the products are mma.sync m16n8k16 (G <= 64 rows would leave a
 // 128-row tcgen05 tile half empty or worse, and fp8 codes are widened in
-// registers, between shared memory and the product).
+// registers, between shared memory and the product).  Up to eight heads go to
+// attend_few.cu: 4 x 131072 tokens of 8 key heads 317 us there, 356 us here.
 //
-// Work: tiles of 64 or 128 keys (32 KB of keys and values, at most 128 keys).  The CTAs (one per SM) divide all tiles of the
-// batch evenly, whatever the lengths; a row whose tiles lie in several CTAs
-// is joined by a second kernel from per-CTA partial results, always in tile
-// order (no atomics: results do not depend on timing).  With several rows
+// Measured: 8192 rows of 2048 of 131072 keys, one key head of 32 query heads:
+// 1.35 ms, 8.6 GB of rows from L2 (6.4 TB/s) and 204 TFLOP/s.  It is the
+// computing warps' latency that bounds it (two an SM quarter, what their
+// registers leave): without the products the same copies take 1.06 ms.
+//
+// Work: tiles of keys (here 64, or 128 where that is at most 32 KB).  The CTAs
+// (one per SM) divide all tiles of the batch evenly, whatever the lengths; a
+// row whose tiles lie in several CTAs is joined by a second kernel from
+// per-CTA partial results, always in tile order (no atomics on results: they
+// do not depend on timing).  With several rows
 // per CTA (prefill) whole rows are dealt out in turn, heads outermost, so
 // that rows running at the same time read the same head's keys (L2), and
 // only the last part wave is divided.
@@ -352,189 +359,189 @@ __global__ void __launch_bounds__(kThreads, 1)
         begun = false;
       }
       for (int tile = x.t0; tile < x.t1; ++tile, ++n) {
-      const uint32_t st = n % S;
-      if (!__all_sync(0xffffffffu, mbar_wait(&full[st], (n / S) & 1, err, abort))) {
-        ok = false;
-        break;
-      }
-      const uint8_t* stage = stages + st * 2 * L::kKV;
-      const uint32_t sk = smem_u32(stage), sv = sk + L::kKV;
-      if ((n & 1) == group) {
+        const uint32_t st = n % S;
+        if (!__all_sync(0xffffffffu, mbar_wait(&full[st], (n / S) & 1, err, abort))) {
+          ok = false;
+          break;
+        }
+        const uint8_t* stage = stages + st * 2 * L::kKV;
+        const uint32_t sk = smem_u32(stage), sv = sk + L::kKV;
+        if ((n & 1) == group) {
 #pragma unroll
-      for (int blk = 0; blk < NK / NB; ++blk) {
-        const int k0 = wk * NK + blk * NB;      // first key of the block
-        constexpr uint32_t kAll = NB == 32 ? 0xffffffffu : (1u << (NB % 32)) - 1;
-        const uint32_t real = (reals[st * 4 + k0 / 32] >> (k0 % 32)) & kAll;  // its keys, one bit each
-        if (real == 0) continue;
-        float s[NB / 8][4];
+          for (int blk = 0; blk < NK / NB; ++blk) {
+            const int k0 = wk * NK + blk * NB;      // first key of the block
+            constexpr uint32_t kAll = NB == 32 ? 0xffffffffu : (1u << (NB % 32)) - 1;
+            const uint32_t real = (reals[st * 4 + k0 / 32] >> (k0 % 32)) & kAll;  // its keys, one bit each
+            if (real == 0) continue;
+            float s[NB / 8][4];
 #pragma unroll
-        for (int j = 0; j < NB / 8; ++j) s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
-        if constexpr (!FP8) {
-          // a step's keys are loaded while the products of the one before run
-          uint32_t kf[2][NB / 16][4];
-          auto load_k = [&](int kk) {
+            for (int j = 0; j < NB / 8; ++j) s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
+            if constexpr (!FP8) {
+              // a step's keys are loaded while the products of the one before run
+              uint32_t kf[2][NB / 16][4];
+              auto load_k = [&](int kk) {
 #pragma unroll
-            for (int j = 0; j < NB / 16; ++j)
-              ldsm4(kf[kk & 1][j], sk + L::at(k0 + j * 16 + (lane & 7) + ((lane >> 4) << 3), kk * 2 + ((lane >> 3) & 1)));
-          };
-          load_k(0);
+                for (int j = 0; j < NB / 16; ++j)
+                  ldsm4(kf[kk & 1][j], sk + L::at(k0 + j * 16 + (lane & 7) + ((lane >> 4) << 3), kk * 2 + ((lane >> 3) & 1)));
+              };
+              load_k(0);
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            if (kk + 1 < D / 16) load_k(kk + 1);
+              for (int kk = 0; kk < D / 16; ++kk) {
+                if (kk + 1 < D / 16) load_k(kk + 1);
 #pragma unroll
-            for (int j = 0; j < NB / 16; ++j) {
-              mma<false>(s[2 * j], qf[kk], kf[kk & 1][j][0], kf[kk & 1][j][1]);
-              mma<false>(s[2 * j + 1], qf[kk], kf[kk & 1][j][2], kf[kk & 1][j][3]);
+                for (int j = 0; j < NB / 16; ++j) {
+                  mma<false>(s[2 * j], qf[kk], kf[kk & 1][j][0], kf[kk & 1][j][1]);
+                  mma<false>(s[2 * j + 1], qf[kk], kf[kk & 1][j][2], kf[kk & 1][j][3]);
+                }
+              }
+            } else {
+#pragma unroll
+              for (int c4 = 0; c4 < D / 64; ++c4) {
+#pragma unroll
+                for (int j = 0; j < NB / 8; ++j) {
+                  const uint4 x =
+                      *reinterpret_cast<const uint4*>(stage + L::at(k0 + j * 8 + L::key(g), c4 * 4 + t));
+                  const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                  for (int i = 0; i < 4; ++i) {
+                    uint32_t b0, b1;
+                    e4m3x4_to_f16x4(u[i], &b0, &b1);
+                    mma<true>(s[j], qf[c4 * 4 + i], b0, b1);
+                  }
+                }
+              }
             }
-          }
-        } else {
-#pragma unroll
-          for (int c4 = 0; c4 < D / 64; ++c4) {
+            // scale, mask and the running maximum
+            const float* ksc = scales + st * 2 * kTile + k0;
+            float mx[2] = {-INFINITY, -INFINITY};
+            float lv[FP8 ? NB / 4 : 1], e_max = e_run;
 #pragma unroll
             for (int j = 0; j < NB / 8; ++j) {
-              const uint4 x =
-                  *reinterpret_cast<const uint4*>(stage + L::at(k0 + j * 8 + L::key(g), c4 * 4 + t));
-              const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+              if constexpr (FP8) {
+                const int i0 = j * 8 + L::key(2 * t), i1 = j * 8 + L::key(2 * t + 1);
+                const float f0 = ksc[i0], f1 = ksc[i1];
+                s[j][0] *= c2[0] * f0;
+                s[j][1] *= c2[0] * f1;
+                s[j][2] *= c2[1] * f0;
+                s[j][3] *= c2[1] * f1;
+                lv[2 * j] = __log2f(ksc[kTile + i0]);
+                lv[2 * j + 1] = __log2f(ksc[kTile + i1]);
+                e_max = fmaxf(e_max, fmaxf(lv[2 * j], lv[2 * j + 1]));
+              } else {
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                uint32_t b0, b1;
-                e4m3x4_to_f16x4(u[i], &b0, &b1);
-                mma<true>(s[j], qf[c4 * 4 + i], b0, b1);
+                for (int i = 0; i < 4; ++i) s[j][i] *= a.c2;
+              }
+            }
+            if (real != kAll) {
+#pragma unroll
+              for (int j = 0; j < NB / 8; ++j) {
+                const uint32_t bits = real >> (j * 8);
+                const bool r0 = (bits >> L::key(2 * t)) & 1, r1 = (bits >> L::key(2 * t + 1)) & 1;
+                s[j][0] = r0 ? s[j][0] : -INFINITY;
+                s[j][1] = r1 ? s[j][1] : -INFINITY;
+                s[j][2] = r0 ? s[j][2] : -INFINITY;
+                s[j][3] = r1 ? s[j][3] : -INFINITY;
+              }
+            }
+#pragma unroll
+            for (int j = 0; j < NB / 8; ++j) {
+              mx[0] = fmaxf(mx[0], fmaxf(s[j][0], s[j][1]));
+              mx[1] = fmaxf(mx[1], fmaxf(s[j][2], s[j][3]));
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 1));
+              mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 2));
+            }
+            if constexpr (FP8) {
+              e_max = fmaxf(e_max, __shfl_xor_sync(0xffffffffu, e_max, 1));
+              e_max = fmaxf(e_max, __shfl_xor_sync(0xffffffffu, e_max, 2));
+            }
+            const bool move0 = !begun ? mx[0] > -INFINITY : mx[0] > m_run[0] + kGrow || (m_run[0] == -INFINITY && mx[0] > -INFINITY);
+            const bool move1 = !begun ? mx[1] > -INFINITY : mx[1] > m_run[1] + kGrow || (m_run[1] == -INFINITY && mx[1] > -INFINITY);
+            if (__any_sync(0xffffffffu, move0 || move1) || (FP8 && e_max > e_run)) {
+              const float m0 = move0 ? mx[0] : m_run[0], m1 = move1 ? mx[1] : m_run[1];
+              const float f0 = move0 ? exp2_approx(m_run[0] - m0) : 1.f, f1 = move1 ? exp2_approx(m_run[1] - m1) : 1.f;
+              m_run[0] = m0;
+              m_run[1] = m1;
+              if (begun) {
+                l_run[0] *= f0;
+                l_run[1] *= f1;
+                const float fe = FP8 && e_max > e_run ? exp2_approx(e_run - e_max) : 1.f;
+                const float g0 = f0 * fe, g1 = f1 * fe;
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i) {
+                  o[i][0] *= g0;
+                  o[i][1] *= g0;
+                  o[i][2] *= g1;
+                  o[i][3] *= g1;
+                }
+              }
+              e_run = e_max;
+            }
+            begun = true;
+            // a row without a finite score so far: exponents against 0 (all e^-inf = 0)
+            const float mu[2] = {m_run[0] == -INFINITY ? 0.f : m_run[0], m_run[1] == -INFINITY ? 0.f : m_run[1]};
+            // the weights, rounded once (bf16; fp8: f16) for the product with v;
+            // their sum is taken before that rounding
+            uint32_t p[NB / 16][4];
+            const float lift = kLift - (e_run == -INFINITY ? 0.f : e_run);
+#pragma unroll
+            for (int j = 0; j < NB / 8; ++j) {
+              const float x0 = s[j][0] - mu[0], x1 = s[j][1] - mu[0], x2 = s[j][2] - mu[1], x3 = s[j][3] - mu[1];
+              const float e0 = exp2_approx(x0), e1 = exp2_approx(x1), e2 = exp2_approx(x2), e3 = exp2_approx(x3);
+              l_run[0] += e0 + e1;
+              l_run[1] += e2 + e3;
+              if constexpr (FP8) {
+                const float v0 = lv[2 * j] + lift, v1 = lv[2 * j + 1] + lift;
+                p[j / 2][(j & 1) * 2 + 0] = pack_f16(exp2_approx(x0 + v0), exp2_approx(x1 + v1));
+                p[j / 2][(j & 1) * 2 + 1] = pack_f16(exp2_approx(x2 + v0), exp2_approx(x3 + v1));
+              } else {
+                p[j / 2][(j & 1) * 2 + 0] = pack_bf16(e0, e1);
+                p[j / 2][(j & 1) * 2 + 1] = pack_bf16(e2, e3);
+              }
+            }
+            // lane i gives the address of row i of an 8 x 8 block, in the keys' order
+            const int vr = k0 + (lane & 8) + L::key(lane & 7);
+            if constexpr (!FP8) {
+              constexpr int kSteps = NB / 16 * (D / 16);
+              uint32_t vf[3][4];
+              auto load_v = [&](int u) {
+                ldsm4t(vf[u % 3], sv + L::at(vr + u / (D / 16) * 16, u % (D / 16) * 2 + (lane >> 4)));
+              };
+              load_v(0);
+              load_v(1);
+#pragma unroll
+              for (int u = 0; u < kSteps; ++u) {
+                if (u + 2 < kSteps) load_v(u + 2);
+                const int j = u / (D / 16), dd = u % (D / 16);
+                mma<false>(o[2 * dd], p[j], vf[u % 3][0], vf[u % 3][1]);
+                mma<false>(o[2 * dd + 1], p[j], vf[u % 3][2], vf[u % 3][3]);
+              }
+            } else {
+              // 16-bit transposed loads bring two neighbouring codes of two keys;
+              // accumulator 2 i holds the even, 2 i + 1 the odd d of 16-code chunk i
+#pragma unroll
+              for (int j = 0; j < NB / 16; ++j) {
+#pragma unroll
+                for (int cc = 0; cc < D / 32; ++cc) {
+                  uint32_t b[4];
+                  ldsm4t(b, sv + L::at(vr + j * 16, cc * 2 + (lane >> 4)));
+#pragma unroll
+                  for (int i = 0; i < 2; ++i) {
+                    uint32_t even[2], odd[2];   // by key half
+                    e4m3x4_to_f16x4(__byte_perm(b[2 * i], 0, 0x3120), &even[0], &odd[0]);
+                    e4m3x4_to_f16x4(__byte_perm(b[2 * i + 1], 0, 0x3120), &even[1], &odd[1]);
+                    mma<true>(o[(cc * 2 + i) * 2], p[j], even[0], even[1]);
+                    mma<true>(o[(cc * 2 + i) * 2 + 1], p[j], odd[0], odd[1]);
+                  }
+                }
               }
             }
           }
-        }
-        // scale, mask and the running maximum
-        const float* ksc = scales + st * 2 * kTile + k0;
-        float mx[2] = {-INFINITY, -INFINITY};
-        float lv[FP8 ? NB / 4 : 1], e_max = e_run;
-#pragma unroll
-        for (int j = 0; j < NB / 8; ++j) {
-          if constexpr (FP8) {
-            const int i0 = j * 8 + L::key(2 * t), i1 = j * 8 + L::key(2 * t + 1);
-            const float f0 = ksc[i0], f1 = ksc[i1];
-            s[j][0] *= c2[0] * f0;
-            s[j][1] *= c2[0] * f1;
-            s[j][2] *= c2[1] * f0;
-            s[j][3] *= c2[1] * f1;
-            lv[2 * j] = __log2f(ksc[kTile + i0]);
-            lv[2 * j + 1] = __log2f(ksc[kTile + i1]);
-            e_max = fmaxf(e_max, fmaxf(lv[2 * j], lv[2 * j + 1]));
-          } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) s[j][i] *= a.c2;
           }
-        }
-        if (real != kAll) {
-#pragma unroll
-          for (int j = 0; j < NB / 8; ++j) {
-            const uint32_t bits = real >> (j * 8);
-            const bool r0 = (bits >> L::key(2 * t)) & 1, r1 = (bits >> L::key(2 * t + 1)) & 1;
-            s[j][0] = r0 ? s[j][0] : -INFINITY;
-            s[j][1] = r1 ? s[j][1] : -INFINITY;
-            s[j][2] = r0 ? s[j][2] : -INFINITY;
-            s[j][3] = r1 ? s[j][3] : -INFINITY;
-          }
-        }
-#pragma unroll
-        for (int j = 0; j < NB / 8; ++j) {
-          mx[0] = fmaxf(mx[0], fmaxf(s[j][0], s[j][1]));
-          mx[1] = fmaxf(mx[1], fmaxf(s[j][2], s[j][3]));
-        }
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 1));
-          mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 2));
-        }
-        if constexpr (FP8) {
-          e_max = fmaxf(e_max, __shfl_xor_sync(0xffffffffu, e_max, 1));
-          e_max = fmaxf(e_max, __shfl_xor_sync(0xffffffffu, e_max, 2));
-        }
-        const bool move0 = !begun ? mx[0] > -INFINITY : mx[0] > m_run[0] + kGrow || (m_run[0] == -INFINITY && mx[0] > -INFINITY);
-        const bool move1 = !begun ? mx[1] > -INFINITY : mx[1] > m_run[1] + kGrow || (m_run[1] == -INFINITY && mx[1] > -INFINITY);
-        if (__any_sync(0xffffffffu, move0 || move1) || (FP8 && e_max > e_run)) {
-          const float m0 = move0 ? mx[0] : m_run[0], m1 = move1 ? mx[1] : m_run[1];
-          const float f0 = move0 ? exp2_approx(m_run[0] - m0) : 1.f, f1 = move1 ? exp2_approx(m_run[1] - m1) : 1.f;
-          m_run[0] = m0;
-          m_run[1] = m1;
-          if (begun) {
-            l_run[0] *= f0;
-            l_run[1] *= f1;
-            const float fe = FP8 && e_max > e_run ? exp2_approx(e_run - e_max) : 1.f;
-            const float g0 = f0 * fe, g1 = f1 * fe;
-#pragma unroll
-            for (int i = 0; i < D / 8; ++i) {
-              o[i][0] *= g0;
-              o[i][1] *= g0;
-              o[i][2] *= g1;
-              o[i][3] *= g1;
-            }
-          }
-          e_run = e_max;
-        }
-        begun = true;
-        // a row without a finite score so far: exponents against 0 (all e^-inf = 0)
-        const float mu[2] = {m_run[0] == -INFINITY ? 0.f : m_run[0], m_run[1] == -INFINITY ? 0.f : m_run[1]};
-        // the weights, rounded once (bf16; fp8: f16) for the product with v;
-        // their sum is taken before that rounding
-        uint32_t p[NB / 16][4];
-        const float lift = kLift - (e_run == -INFINITY ? 0.f : e_run);
-#pragma unroll
-        for (int j = 0; j < NB / 8; ++j) {
-          const float x0 = s[j][0] - mu[0], x1 = s[j][1] - mu[0], x2 = s[j][2] - mu[1], x3 = s[j][3] - mu[1];
-          const float e0 = exp2_approx(x0), e1 = exp2_approx(x1), e2 = exp2_approx(x2), e3 = exp2_approx(x3);
-          l_run[0] += e0 + e1;
-          l_run[1] += e2 + e3;
-          if constexpr (FP8) {
-            const float v0 = lv[2 * j] + lift, v1 = lv[2 * j + 1] + lift;
-            p[j / 2][(j & 1) * 2 + 0] = pack_f16(exp2_approx(x0 + v0), exp2_approx(x1 + v1));
-            p[j / 2][(j & 1) * 2 + 1] = pack_f16(exp2_approx(x2 + v0), exp2_approx(x3 + v1));
-          } else {
-            p[j / 2][(j & 1) * 2 + 0] = pack_bf16(e0, e1);
-            p[j / 2][(j & 1) * 2 + 1] = pack_bf16(e2, e3);
-          }
-        }
-        // lane i gives the address of row i of an 8 x 8 block, in the keys' order
-        const int vr = k0 + (lane & 8) + L::key(lane & 7);
-        if constexpr (!FP8) {
-          constexpr int kSteps = NB / 16 * (D / 16);
-          uint32_t vf[3][4];
-          auto load_v = [&](int u) {
-            ldsm4t(vf[u % 3], sv + L::at(vr + u / (D / 16) * 16, u % (D / 16) * 2 + (lane >> 4)));
-          };
-          load_v(0);
-          load_v(1);
-#pragma unroll
-          for (int u = 0; u < kSteps; ++u) {
-            if (u + 2 < kSteps) load_v(u + 2);
-            const int j = u / (D / 16), dd = u % (D / 16);
-            mma<false>(o[2 * dd], p[j], vf[u % 3][0], vf[u % 3][1]);
-            mma<false>(o[2 * dd + 1], p[j], vf[u % 3][2], vf[u % 3][3]);
-          }
-        } else {
-          // 16-bit transposed loads bring two neighbouring codes of two keys;
-          // accumulator 2 i holds the even, 2 i + 1 the odd d of 16-code chunk i
-#pragma unroll
-          for (int j = 0; j < NB / 16; ++j) {
-#pragma unroll
-            for (int cc = 0; cc < D / 32; ++cc) {
-              uint32_t b[4];
-              ldsm4t(b, sv + L::at(vr + j * 16, cc * 2 + (lane >> 4)));
-#pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                uint32_t even[2], odd[2];   // by key half
-                e4m3x4_to_f16x4(__byte_perm(b[2 * i], 0, 0x3120), &even[0], &odd[0]);
-                e4m3x4_to_f16x4(__byte_perm(b[2 * i + 1], 0, 0x3120), &even[1], &odd[1]);
-                mma<true>(o[(cc * 2 + i) * 2], p[j], even[0], even[1]);
-                mma<true>(o[(cc * 2 + i) * 2 + 1], p[j], odd[0], odd[1]);
-              }
-            }
-          }
-        }
-      }
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&empty[st]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&empty[st]);
       }
       if (!ok) break;
       {

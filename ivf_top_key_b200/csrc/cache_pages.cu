@@ -9,8 +9,9 @@
 // Pages that hold more than one sequence's tokens are full (a fork copies the
 // part page), so a page is written only while one sequence owns it.
 //
-// What bounds them: a call is one CTA that plans (reads the reference counts
-// once; a few us) and a grid that moves pages at the copy rate of HBM.
+// What bounds them: a call is one CTA that plans (reads the reference counts;
+// about 4 us) and a grid that moves pages at the copy rate of HBM: 256 pages of
+// 4 layers (474 MB read and written) 80 us, 5.9 TB/s.
 #include "../../include/ai_index.h"
 #include "common.cuh"
 #include "kernels.h"
@@ -272,8 +273,8 @@ __global__ void __launch_bounds__(kPlan) k_fork_plan(View c, const int32_t* src,
 // Copies chunk `chunk` of the first `slots` tokens of a page of one layer: K
 // and V bytes as one run of 16-byte units, kUnits of them a thread, all loaded
 // before the first is stored; scales with chunk 0.  A chunk is 8 KB: 16 blocks
-// an SM keep 128 KB of loads under way (a page of one block's, four units a
-// thread: 64 forks of 16 layers 83 us a call, now 68).
+// an SM keep 128 KB of loads under way (with a page's 16 KB parts of K, then V,
+// to a block, 64 forks of 16 layers and their release took 84 us, now 71).
 constexpr int kMoveThreads = 128, kUnits = 4;
 __host__ __device__ constexpr int64_t chunks_of(int64_t bytes) {
   return (2 * bytes / 16 + kMoveThreads * kUnits - 1) / (kMoveThreads * kUnits);
