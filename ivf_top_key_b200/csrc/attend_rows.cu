@@ -539,7 +539,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
           }
-          }
+        }
         __syncwarp();
         if (lane == 0) mbar_arrive(&empty[st]);
       }
