@@ -809,6 +809,9 @@ int run_rows(const ai_cache* c, int32_t layer, const void* q, int32_t R, int32_t
   a.page_shift = 31 + s;
   a.page_mul = ((uint64_t(1) << a.page_shift) + c->page_size - 1) / c->page_size;
   a.tile = a.mb_rows <= kFewHeads ? rows_few_tile() : (c->head_dim * es >= 256 ? 64 : 128);  // Layout::kTile
+  // measured: about 1.5 us an item; 0.2 us a tile of 32 keys, 0.4 to 0.7 us a
+  // larger one
+  a.over = a.mb_rows <= kFewHeads ? 7 : 3;
   a.nt_ids = (n_ids + a.tile - 1) / a.tile;
   a.c2 = scale * kLog2e;
   a.out = static_cast<uint16_t*>(out);

@@ -26,6 +26,7 @@ struct RowsArgs {
   int n_mb, mb_rows;        // row blocks per key head, query heads per block
   int n_seqs, width, n_pages, page_size;
   int tile;                 // keys of a tile
+  int over;                 // what an item costs besides its tiles, in tiles
   uint64_t page_mul;        // token / page_size = token * page_mul >> page_shift
   int page_shift;
   float c2;                 // scale * log2 e
@@ -198,8 +199,8 @@ __device__ int64_t block_scan(int64_t x, int64_t* total, int64_t* warp_sums) {
 template <int kThreads, int D>
 __device__ void begin_walk(const RowsArgs& a, int* sh_none, int* err, Walk* out) {
   __shared__ int64_t sh_scan[kThreads / 32];
-  __shared__ int64_t sh_b0;
-  __shared__ int sh_row, sh_n_none;
+  __shared__ int64_t sh_b[2];
+  __shared__ int sh_row, sh_head, sh_tile, sh_n_none;
   const int tid = threadIdx.x, grid = gridDim.x, cta = blockIdx.x;
   const int n_heads = a.Hkv * a.n_mb;
   if (tid == 0) sh_n_none = 0;
@@ -217,35 +218,99 @@ __device__ void begin_walk(const RowsArgs& a, int* sh_none, int* err, Walk* out)
     total = (items - w.n_whole) * w.nt_ids;
     w.b = total * cta / grid;
     w.b1 = total * (cta + 1) / grid;
-  } else {
-    // the number of tiles, then the row where this CTA's share begins (a
-    // second pass over the lengths where there are more rows than threads)
-    int64_t mine = tid < a.R ? tiles_of(a, tid) : 0, before;
-    before = block_scan<kThreads>(mine, &total, sh_scan);
-    for (int r0 = kThreads; r0 < a.R; r0 += kThreads) {
-      int64_t sum;
-      block_scan<kThreads>(r0 + tid < a.R ? tiles_of(a, r0 + tid) : 0, &sum, sh_scan);
-      total += sum;
+  } else if (a.R <= 32) {
+    // as below, every warp by itself
+    const int lane = tid & 31;
+    const int64_t mine = lane < a.R ? tiles_of(a, lane) : 0;
+    const uint32_t some = __ballot_sync(0xffffffffu, mine > 0);
+    int64_t inc = mine;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += y;
     }
-    total *= n_heads;
-    w.b = total * cta / grid;
-    w.b1 = total * (cta + 1) / grid;
-    int64_t seen = 0;
+    total = __shfl_sync(0xffffffffu, inc, 31);
+    const int64_t cost = (total + static_cast<int64_t>(__popc(some)) * a.over) * n_heads, n = mine + a.over;
+    const int64_t t0 = (inc - mine) * n_heads;
+    const int64_t c0 = t0 + static_cast<int64_t>(__popc(some & ((1u << lane) - 1))) * a.over * n_heads;
+    int64_t b[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int64_t at = cost * (cta + u) / grid - c0;
+      const bool here = mine > 0 && at >= 0 && at < n * n_heads;
+      const int64_t head = here ? at / n : 0, rest = at - head * n - a.over;
+      const int tile = here && rest > 0 ? static_cast<int>(rest) : 0;
+      const uint32_t who = __ballot_sync(0xffffffffu, here);
+      const int src = who ? __ffs(who) - 1 : 0;
+      b[u] = __shfl_sync(0xffffffffu, t0 + head * mine + tile, src);
+      if (!who) b[u] = total * n_heads;
+      if (u == 0) {
+        w.row = src;
+        w.head = static_cast<int>(__shfl_sync(0xffffffffu, head, src));
+        w.tile = __shfl_sync(0xffffffffu, tile, src);
+        w.n_tiles = static_cast<int>(__shfl_sync(0xffffffffu, mine, src));
+      }
+    }
+    w.b = b[0];
+    w.b1 = b[1];
+    for (uint32_t none = __ballot_sync(0xffffffffu, lane < a.R && mine == 0 && lane % grid == cta); tid < 32 && none;
+         none &= none - 1) {
+      const int r = __ffs(none) - 1;
+      const int64_t at = static_cast<int64_t>(r) * a.Hq;
+      for (int j = lane; j < a.Hq * D / 8; j += 32) reinterpret_cast<uint4*>(a.out + at * D)[j] = make_uint4(0, 0, 0, 0);
+      if (a.lse)
+        for (int j = lane; j < a.Hq; j += 32) a.lse[at + j] = -INFINITY;
+      const int s = seq_of(a, r);
+      if (lane == 0 && (s < 0 || s >= a.n_seqs)) atomicOr(err, AI_DEVFLAG_RANGE);
+    }
+  } else {
+    // An item costs its tiles and, once, about a.over more (queries, states,
+    // results): the CTAs divide that sum evenly, and a CTA's tiles are those
+    // whose cost lies in its part.  First the sum, then the rows where this
+    // CTA's part begins and ends (a second pass over the lengths where there
+    // are more rows than threads).
+    int64_t mine = tid < a.R ? tiles_of(a, tid) : 0, before = 0, rows_before = 0, n_rows = 0;
+    total = 0;
     for (int r0 = 0; r0 < a.R; r0 += kThreads) {
-      int64_t sum = 0;
+      int64_t tiles, rows;
+      const int64_t x = r0 == 0 ? mine : (r0 + tid < a.R ? tiles_of(a, r0 + tid) : 0);
+      const int64_t p = block_scan<kThreads>(x, &tiles, sh_scan), q = block_scan<kThreads>(x > 0, &rows, sh_scan);
+      if (r0 == 0) {
+        before = p;
+        rows_before = q;
+      }
+      total += tiles;
+      n_rows += rows;
+    }
+    const int64_t cost = (total + n_rows * a.over) * n_heads;
+    const int64_t part[2] = {cost * cta / grid, cost * (cta + 1) / grid};
+    if (tid < 2) sh_b[tid] = total * n_heads;   // a part that begins or ends behind the last tile
+    __syncthreads();
+    int64_t tiles_seen = 0, rows_seen = 0;
+    for (int r0 = 0; r0 < a.R; r0 += kThreads) {
       const int r = r0 + tid;
-      if (r0 > 0) {
+      int64_t tiles = 0, rows = 0;
+      if (a.R > kThreads) {
         mine = r < a.R ? tiles_of(a, r) : 0;
-        before = block_scan<kThreads>(mine, &sum, sh_scan);
-      } else if (a.R > kThreads) {
-        block_scan<kThreads>(mine, &sum, sh_scan);
+        before = block_scan<kThreads>(mine, &tiles, sh_scan);
+        rows_before = block_scan<kThreads>(mine > 0, &rows, sh_scan);
       }
-      const int64_t n = mine * n_heads, p = seen + before * n_heads;
-      if (n > 0 && p <= w.b && w.b < p + n) {
-        sh_row = r;
-        sh_b0 = p;
+      const int64_t n = mine + a.over;              // cost of one of the row's items
+      const int64_t t0 = (tiles_seen + before) * n_heads, c0 = t0 + (rows_seen + rows_before) * a.over * n_heads;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int64_t at = part[u] - c0;
+        if (mine == 0 || at < 0 || at >= n * n_heads) continue;
+        const int64_t head = at / n, rest = at - head * n - a.over;
+        const int tile = rest > 0 ? static_cast<int>(rest) : 0;
+        sh_b[u] = t0 + head * mine + tile;
+        if (u == 0) {
+          sh_row = r;
+          sh_head = static_cast<int>(head);
+          sh_tile = tile;
+        }
       }
-      seen += sum * n_heads;
+      tiles_seen += tiles;
+      rows_seen += rows;
       // rows that see nothing: zeros, and the log of an empty sum
       if (r < a.R && mine == 0 && r % grid == cta) {
         sh_none[atomicAdd(&sh_n_none, 1)] = r;
@@ -265,6 +330,10 @@ __device__ void begin_walk(const RowsArgs& a, int* sh_none, int* err, Walk* out)
     }
   }
   __syncthreads();
+  if (!a.ids && a.R > 32) {
+    w.b = sh_b[0];
+    w.b1 = sh_b[1];
+  }
   if (w.b < w.b1) {
     if (a.ids) {
       const int64_t item = w.n_whole + w.b / w.nt_ids;
@@ -272,12 +341,11 @@ __device__ void begin_walk(const RowsArgs& a, int* sh_none, int* err, Walk* out)
       w.row = static_cast<int>(item % a.R);
       w.tile = static_cast<int>(w.b % w.nt_ids);
       w.n_tiles = w.nt_ids;
-    } else {
-      const int64_t start = w.b - sh_b0;   // within the row's tiles of all heads
+    } else if (a.R > 32) {
       w.row = sh_row;
       w.n_tiles = tiles_of(a, w.row);
-      w.head = static_cast<int>(start / w.n_tiles);
-      w.tile = static_cast<int>(start % w.n_tiles);
+      w.head = sh_head;
+      w.tile = sh_tile;
     }
   }
   *out = w;

@@ -110,6 +110,21 @@ def test_cached_long_uneven_batch_divides_rows_among_ctas():
     assert torch.equal(out, again)   # no order of arrival in it
 
 
+@pytest.mark.parametrize("n,Hq,Hkv", [(33, 4, 2), (300, 2, 1), (700, 20, 1)])
+def test_cached_many_sequences_with_empty_ones(n, Hq, Hkv):
+    """A padded batch: more sequences than a warp, and than a block, looks up at once; some are empty."""
+    r = random.Random(n)
+    lens = [r.choice([0, 1, 31, 33, 64, 100]) for _ in range(n)]
+    lens[n // 2] = 900
+    args, kd, vd = _cache(lens, 32, Hkv, 64, "bf16", seed=n, layers=1, layer=0)
+    q = _q(n, Hq, 64, 15)
+    lse = torch.empty(n, Hq, device=DEV)
+    status = _i32([0])
+    out = attend_cached(q.to(DEV), out_lse=lse, status=status, **args)
+    R.check(out, lse, [R.attend(q[i].double(), kd[i], vd[i], 0.125) for i in range(n)])
+    assert status.item() == 0
+
+
 def test_cached_rows_of_chosen_sequences_and_other_scales():
     lens = [40, 200, 3]
     args, kd, vd = _cache(lens, 16, 2, 64, "bf16", seed=4)
