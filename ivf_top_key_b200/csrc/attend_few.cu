@@ -104,6 +104,8 @@ __global__ void __launch_bounds__(Few<D, FP8>::kThreads, 1) k_attend_few(const R
   // the joining kernel may be set up now; it waits for this one to end
   dependency_launch();
   Share x;
+  // an item of one tile is finished by the warp that computes it
+  auto single = [](const Share& s) { return s.slot < 0 && s.t1 - s.t0 == 1; };
 
   if (warp >= kComp + kCopiers) {
     // ============================================================= joining
@@ -111,6 +113,7 @@ __global__ void __launch_bounds__(Few<D, FP8>::kThreads, 1) k_attend_few(const R
     const int c0 = (j % 8) * 4;                     // columns c0 + 32 i
     uint32_t share = 0;
     while (w.next(a, &x)) {
+      if (single(x)) continue;
       const uint32_t buf = share & 1;
       if (!__all_sync(0xffffffffu, mbar_wait(&st_full[buf], (share >> 1) & 1, err, abort))) break;
       constexpr int kNext = 8 * L::kState;
@@ -310,19 +313,29 @@ __global__ void __launch_bounds__(Few<D, FP8>::kThreads, 1) k_attend_few(const R
     // 11 bits down to 2^-25 of the largest, and at most 2^15.
     constexpr float kGrow = FP8 ? 4.f : 8.f, kLift = 11.f;
     uint32_t n0 = 0, share = 0;
+    // this warp's first tile of a share whose first tile is the CTA's n-th
+    auto first_tile = [&](uint32_t n) { return x.t0 + static_cast<int>((warp + kComp - n % kComp) % kComp); };
     bool more = w.next(a, &x), ok = true;
-    if (more) fetch();
+    int tile = 0;
+    if (more) {
+      tile = first_tile(0);
+      if (tile < x.t1) fetch();
+    }
     while (ok && more) {
-      const int t0 = x.t0, t1 = x.t1;
+      const int t0 = x.t0, t1 = x.t1, own = tile;
+      const bool alone = single(x);
+      const int64_t out_row = static_cast<int64_t>(x.row) * a.Hq + x.head * a.G;
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
         qf[kk][0] = qn[kk][0];
         qf[kk][1] = qn[kk][1];
       }
       more = w.next(a, &x);
-      if (more) fetch();
-      int tile = t0 + static_cast<int>((warp + kComp - n0 % kComp) % kComp);
-      const bool mine = tile < t1;
+      if (more) {
+        tile = first_tile(n0 + (t1 - t0));
+        if (tile < x.t1) fetch();
+      }
+      const bool mine = own < t1;
       float c2[2] = {a.c2, a.c2};        // by head 2 t, 2 t + 1
       float o[D / 16][4], m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
       float e_run = -INFINITY;           // fp8: log2 of the largest value scale so far
@@ -357,8 +370,8 @@ __global__ void __launch_bounds__(Few<D, FP8>::kThreads, 1) k_attend_few(const R
         }
       }
       bool begun = false;
-      for (; tile < t1; tile += kComp) {
-        const uint32_t n = n0 + (tile - t0), st = n % S;
+      for (int at = own; at < t1; at += kComp) {
+        const uint32_t n = n0 + (at - t0), st = n % S;
         if (!__all_sync(0xffffffffu, mbar_wait(&full[st], (n / S) & 1, err, abort))) {
           ok = false;
           break;
@@ -528,16 +541,42 @@ __global__ void __launch_bounds__(Few<D, FP8>::kThreads, 1) k_attend_few(const R
       }
       if (!ok) break;
       n0 += t1 - t0;
-      // this warp's state of the row
-      const uint32_t buf = share & 1;
-      if (share >= 2 && !__all_sync(0xffffffffu, mbar_wait(&st_free[buf], ((share >> 1) - 1) & 1, err, abort))) break;
-      float* to = states + buf * L::kStates + warp * 8 * L::kState;
       if (begun) {
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
           for (int d = 4; d < 32; d *= 2) l_run[i] += __shfl_xor_sync(0xffffffffu, l_run[i], d);
-        const float f = !FP8 ? 1.f : (e_run == -INFINITY ? 0.f : exp2_approx(e_run - kLift));
+      }
+      const float unlift = !FP8 ? 1.f : (e_run == -INFINITY ? 0.f : exp2_approx(e_run - kLift));
+      if (alone) {
+        if (mine) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int h = 2 * t + i;
+            if (h >= a.G) continue;
+            const float inv = l_run[i] == 0.f ? 0.f : unlift / l_run[i];
+            uint16_t* to = a.out + (out_row + h) * D;
+#pragma unroll
+            for (int dd = 0; dd < D / 16; ++dd) {
+              const uint32_t y = begun ? pack_bf16(o[dd][i] * inv, o[dd][2 + i] * inv) : 0;
+              if constexpr (!FP8) {
+                to[dd * 16 + g] = static_cast<uint16_t>(y & 0xffff);
+                to[dd * 16 + 8 + g] = static_cast<uint16_t>(y >> 16);
+              } else {
+                *reinterpret_cast<uint32_t*>(to + dd * 16 + 2 * g) = y;
+              }
+            }
+            if (a.lse && g == 0)
+              a.lse[out_row + h] = l_run[i] == 0.f ? -INFINITY : (m_run[i] + log2f(l_run[i])) * kLn2;
+          }
+        }
+        continue;
+      }
+      // this warp's state of the row
+      const uint32_t buf = share & 1;
+      if (share >= 2 && !__all_sync(0xffffffffu, mbar_wait(&st_free[buf], ((share >> 1) - 1) & 1, err, abort))) break;
+      float* to = states + buf * L::kStates + warp * 8 * L::kState;
+      if (begun) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           float* h = to + (2 * t + i) * L::kState;
@@ -547,7 +586,7 @@ __global__ void __launch_bounds__(Few<D, FP8>::kThreads, 1) k_attend_few(const R
               h[dd * 16 + g] = o[dd][i];
               h[dd * 16 + 8 + g] = o[dd][2 + i];
             } else {
-              *reinterpret_cast<float2*>(h + dd * 16 + 2 * g) = make_float2(o[dd][i] * f, o[dd][2 + i] * f);
+              *reinterpret_cast<float2*>(h + dd * 16 + 2 * g) = make_float2(o[dd][i] * unlift, o[dd][2 + i] * unlift);
             }
           }
         }

@@ -108,7 +108,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   int* err = a.status ? a.status : &g_no_status;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int n_heads = a.Hkv * a.n_mb;
+  const int n_heads = a.n_heads;
   const int cta = blockIdx.x;
 
   if (tid == 0) {
@@ -800,6 +800,7 @@ int run_rows(const ai_cache* c, int32_t layer, const void* q, int32_t R, int32_t
   a.G = G;
   a.n_mb = n_mb;
   a.mb_rows = (G + n_mb - 1) / n_mb;
+  a.n_heads = a.Hkv * n_mb;
   a.n_seqs = c->n_seqs;
   a.width = c->max_pages;
   a.n_pages = c->n_pages;

@@ -24,6 +24,7 @@ struct RowsArgs {
   const int32_t* ids;       // [R, n_ids] or nullptr (cached)
   int R, n_ids, nt_ids, Hq, Hkv, G;
   int n_mb, mb_rows;        // row blocks per key head, query heads per block
+  int n_heads;              // Hkv * n_mb
   int n_seqs, width, n_pages, page_size;
   int tile;                 // keys of a tile
   int over;                 // what an item costs besides its tiles, in tiles
@@ -127,26 +128,23 @@ struct Share {
 // grid, .. < n_whole; heads outermost), then the tiles [b, b1) of the divided
 // items, which follow one another.  Every warp runs its own.
 struct Walk {
-  int it, n_whole, grid;
-  int64_t b, b1;
-  bool by_head;        // heads outermost (selected), else rows (cached)
+  int it, n_whole;
+  int64_t left;        // tiles of the divided items that are still to come
   int row, head;       // of the next divided item
   int tile, n_tiles;   // its next tile, and its tiles
-  int nt_ids, n_heads;
 
   __device__ bool next(const RowsArgs& a, Share* s) {
     if (it < n_whole) {
       s->head = it / a.R;
       s->row = it - s->head * a.R;
       s->t0 = 0;
-      s->t1 = nt_ids;
+      s->t1 = a.nt_ids;
       s->slot = -1;
       s->ends = true;
-      it += grid;
+      it += gridDim.x;
       return true;
     }
-    if (b >= b1) return false;
-    const int64_t left = b1 - b;
+    if (left <= 0) return false;
     s->row = row;
     s->head = head;
     s->t0 = tile;
@@ -154,16 +152,16 @@ struct Walk {
     s->t1 = s->ends ? n_tiles : tile + static_cast<int>(left);
     // begun in an earlier CTA: its first slot; goes on in a later one: its second
     s->slot = tile > 0 ? 0 : (s->ends ? -1 : 1);
-    b += s->t1 - tile;
+    left -= s->t1 - tile;
     tile = 0;
-    if (by_head) {
+    if (a.ids) {       // heads outermost
       if (++row == a.R) {
         row = 0;
         ++head;
       }
-    } else if (++head == n_heads) {
+    } else if (++head == a.n_heads) {
       head = 0;
-      if (b < b1) {
+      if (left > 0) {
         do ++row;
         while (row < a.R && tiles_of(a, row) == 0);
         n_tiles = row < a.R ? tiles_of(a, row) : 1;
@@ -199,156 +197,117 @@ __device__ int64_t block_scan(int64_t x, int64_t* total, int64_t* warp_sums) {
 template <int kThreads, int D>
 __device__ void begin_walk(const RowsArgs& a, int* sh_none, int* err, Walk* out) {
   __shared__ int64_t sh_scan[kThreads / 32];
-  __shared__ int64_t sh_b[2];
-  __shared__ int sh_row, sh_head, sh_tile, sh_n_none;
+  __shared__ int64_t sh_part[2];   // this CTA's tiles of the divided items: first, end
+  __shared__ Walk sh_w;
+  __shared__ int sh_n_none;
   const int tid = threadIdx.x, grid = gridDim.x, cta = blockIdx.x;
-  const int n_heads = a.Hkv * a.n_mb;
-  if (tid == 0) sh_n_none = 0;
-  Walk w;
-  w.grid = grid;
-  w.it = cta;
-  w.n_whole = 0;
-  w.by_head = a.ids != nullptr;
-  w.nt_ids = a.nt_ids;
-  w.n_heads = n_heads;
-  int64_t total;
+  const int n_heads = a.n_heads;
+  auto nothing = [&](int row, int first, int step) {   // zeros, and the log of an empty sum
+    const int64_t at = static_cast<int64_t>(row) * a.Hq;
+    for (int j = first; j < a.Hq * D / 8; j += step)
+      reinterpret_cast<uint4*>(a.out + at * D)[j] = make_uint4(0, 0, 0, 0);
+    if (a.lse)
+      for (int j = first; j < a.Hq; j += step) a.lse[at + j] = -INFINITY;
+    const int s = seq_of(a, row);
+    if (first == 0 && (s < 0 || s >= a.n_seqs)) atomicOr(err, AI_DEVFLAG_RANGE);
+  };
+  if (tid == 0) {
+    sh_w.it = cta;
+    sh_w.n_whole = 0;
+    sh_n_none = 0;
+  }
   if (a.ids) {
-    const int64_t items = static_cast<int64_t>(a.R) * n_heads;
-    w.n_whole = static_cast<int>(items / grid) * grid;
-    total = (items - w.n_whole) * w.nt_ids;
-    w.b = total * cta / grid;
-    w.b1 = total * (cta + 1) / grid;
-  } else if (a.R <= 32) {
-    // as below, every warp by itself
-    const int lane = tid & 31;
-    const int64_t mine = lane < a.R ? tiles_of(a, lane) : 0;
-    const uint32_t some = __ballot_sync(0xffffffffu, mine > 0);
-    int64_t inc = mine;
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += y;
+    if (tid == 0) {
+      const int64_t items = static_cast<int64_t>(a.R) * n_heads;
+      const int n_whole = static_cast<int>(items / grid) * grid;
+      const int64_t total = (items - n_whole) * a.nt_ids;
+      const int64_t first = total * cta / grid, item = n_whole + first / a.nt_ids;
+      sh_part[0] = first;
+      sh_part[1] = total * (cta + 1) / grid;
+      sh_w.n_whole = n_whole;
+      sh_w.head = static_cast<int>(item / a.R);
+      sh_w.row = static_cast<int>(item % a.R);
+      sh_w.tile = static_cast<int>(first % a.nt_ids);
+      sh_w.n_tiles = a.nt_ids;
     }
-    total = __shfl_sync(0xffffffffu, inc, 31);
-    const int64_t cost = (total + static_cast<int64_t>(__popc(some)) * a.over) * n_heads, n = mine + a.over;
-    const int64_t t0 = (inc - mine) * n_heads;
-    const int64_t c0 = t0 + static_cast<int64_t>(__popc(some & ((1u << lane) - 1))) * a.over * n_heads;
-    int64_t b[2];
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int64_t at = cost * (cta + u) / grid - c0;
-      const bool here = mine > 0 && at >= 0 && at < n * n_heads;
-      const int64_t head = here ? at / n : 0, rest = at - head * n - a.over;
-      const int tile = here && rest > 0 ? static_cast<int>(rest) : 0;
-      const uint32_t who = __ballot_sync(0xffffffffu, here);
-      const int src = who ? __ffs(who) - 1 : 0;
-      b[u] = __shfl_sync(0xffffffffu, t0 + head * mine + tile, src);
-      if (!who) b[u] = total * n_heads;
-      if (u == 0) {
-        w.row = src;
-        w.head = static_cast<int>(__shfl_sync(0xffffffffu, head, src));
-        w.tile = __shfl_sync(0xffffffffu, tile, src);
-        w.n_tiles = static_cast<int>(__shfl_sync(0xffffffffu, mine, src));
-      }
-    }
-    w.b = b[0];
-    w.b1 = b[1];
-    for (uint32_t none = __ballot_sync(0xffffffffu, lane < a.R && mine == 0 && lane % grid == cta); tid < 32 && none;
-         none &= none - 1) {
-      const int r = __ffs(none) - 1;
-      const int64_t at = static_cast<int64_t>(r) * a.Hq;
-      for (int j = lane; j < a.Hq * D / 8; j += 32) reinterpret_cast<uint4*>(a.out + at * D)[j] = make_uint4(0, 0, 0, 0);
-      if (a.lse)
-        for (int j = lane; j < a.Hq; j += 32) a.lse[at + j] = -INFINITY;
-      const int s = seq_of(a, r);
-      if (lane == 0 && (s < 0 || s >= a.n_seqs)) atomicOr(err, AI_DEVFLAG_RANGE);
-    }
+    __syncthreads();
   } else {
     // An item costs its tiles and, once, about a.over more (queries, states,
     // results): the CTAs divide that sum evenly, and a CTA's tiles are those
-    // whose cost lies in its part.  First the sum, then the rows where this
-    // CTA's part begins and ends (a second pass over the lengths where there
-    // are more rows than threads).
-    int64_t mine = tid < a.R ? tiles_of(a, tid) : 0, before = 0, rows_before = 0, n_rows = 0;
-    total = 0;
-    for (int r0 = 0; r0 < a.R; r0 += kThreads) {
-      int64_t tiles, rows;
-      const int64_t x = r0 == 0 ? mine : (r0 + tid < a.R ? tiles_of(a, r0 + tid) : 0);
-      const int64_t p = block_scan<kThreads>(x, &tiles, sh_scan), q = block_scan<kThreads>(x > 0, &rows, sh_scan);
-      if (r0 == 0) {
-        before = p;
-        rows_before = q;
-      }
-      total += tiles;
-      n_rows += rows;
-    }
-    const int64_t cost = (total + n_rows * a.over) * n_heads;
-    const int64_t part[2] = {cost * cta / grid, cost * (cta + 1) / grid};
-    if (tid < 2) sh_b[tid] = total * n_heads;   // a part that begins or ends behind the last tile
-    __syncthreads();
-    int64_t tiles_seen = 0, rows_seen = 0;
-    for (int r0 = 0; r0 < a.R; r0 += kThreads) {
-      const int r = r0 + tid;
-      int64_t tiles = 0, rows = 0;
-      if (a.R > kThreads) {
-        mine = r < a.R ? tiles_of(a, r) : 0;
-        before = block_scan<kThreads>(mine, &tiles, sh_scan);
-        rows_before = block_scan<kThreads>(mine > 0, &rows, sh_scan);
-      }
-      const int64_t n = mine + a.over;              // cost of one of the row's items
-      const int64_t t0 = (tiles_seen + before) * n_heads, c0 = t0 + (rows_seen + rows_before) * a.over * n_heads;
+    // whose cost lies in its part.  `mine` tiles of row r behind t0 tiles and c0
+    // cost of all heads: where the part's ends lie in the row.
+    auto locate = [&](int r, int64_t mine, int64_t t0, int64_t c0, int64_t cost) {
+      const int64_t n = mine + a.over;
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        const int64_t at = part[u] - c0;
+        const int64_t at = cost * (cta + u) / grid - c0;
         if (mine == 0 || at < 0 || at >= n * n_heads) continue;
         const int64_t head = at / n, rest = at - head * n - a.over;
         const int tile = rest > 0 ? static_cast<int>(rest) : 0;
-        sh_b[u] = t0 + head * mine + tile;
+        sh_part[u] = t0 + head * mine + tile;
         if (u == 0) {
-          sh_row = r;
-          sh_head = static_cast<int>(head);
-          sh_tile = tile;
+          sh_w.row = r;
+          sh_w.head = static_cast<int>(head);
+          sh_w.tile = tile;
+          sh_w.n_tiles = static_cast<int>(mine);
         }
       }
-      tiles_seen += tiles;
-      rows_seen += rows;
-      // rows that see nothing: zeros, and the log of an empty sum
-      if (r < a.R && mine == 0 && r % grid == cta) {
-        sh_none[atomicAdd(&sh_n_none, 1)] = r;
-        const int s = seq_of(a, r);
-        if (s < 0 || s >= a.n_seqs) atomicOr(err, AI_DEVFLAG_RANGE);
+    };
+    if (a.R <= 32) {
+      if (tid < 32) {   // by one warp, without the block's barriers
+        const int64_t mine = tid < a.R ? tiles_of(a, tid) : 0;
+        const uint32_t some = __ballot_sync(0xffffffffu, mine > 0);
+        int64_t inc = mine;
+        for (int o = 1; o < 32; o <<= 1) {
+          const int64_t y = __shfl_up_sync(0xffffffffu, inc, o);
+          if (tid >= o) inc += y;
+        }
+        const int64_t total = __shfl_sync(0xffffffffu, inc, 31);
+        const int64_t cost = (total + static_cast<int64_t>(__popc(some)) * a.over) * n_heads;
+        if (tid < 2) sh_part[tid] = total * n_heads;   // a part that begins or ends behind the last tile
+        __syncwarp();
+        const int64_t t0 = (inc - mine) * n_heads;
+        locate(tid, mine, t0, t0 + static_cast<int64_t>(__popc(some & ((1u << tid) - 1))) * a.over * n_heads, cost);
+        for (uint32_t none = __ballot_sync(0xffffffffu, tid < a.R && mine == 0 && tid % grid == cta); none;
+             none &= none - 1)
+          nothing(__ffs(none) - 1, tid, 32);
       }
       __syncthreads();
-      for (int i = 0; i < sh_n_none; ++i) {
-        const int64_t at = static_cast<int64_t>(sh_none[i]) * a.Hq;
-        for (int j = tid; j < a.Hq * D / 8; j += kThreads)
-          reinterpret_cast<uint4*>(a.out + at * D)[j] = make_uint4(0, 0, 0, 0);
-        if (a.lse)
-          for (int j = tid; j < a.Hq; j += kThreads) a.lse[at + j] = -INFINITY;
+    } else {
+      // the sums, then the rows (a second pass over the lengths)
+      int64_t total = 0, n_rows = 0;
+      for (int r0 = 0; r0 < a.R; r0 += kThreads) {
+        int64_t tiles, rows;
+        const int64_t x = r0 + tid < a.R ? tiles_of(a, r0 + tid) : 0;
+        block_scan<kThreads>(x, &tiles, sh_scan);
+        block_scan<kThreads>(x > 0, &rows, sh_scan);
+        total += tiles;
+        n_rows += rows;
+      }
+      const int64_t cost = (total + n_rows * a.over) * n_heads;
+      if (tid < 2) sh_part[tid] = total * n_heads;
+      __syncthreads();
+      int64_t tiles_seen = 0, rows_seen = 0;
+      for (int r0 = 0; r0 < a.R; r0 += kThreads) {
+        const int r = r0 + tid;
+        int64_t tiles, rows;
+        const int64_t mine = r < a.R ? tiles_of(a, r) : 0;
+        const int64_t t0 = (tiles_seen + block_scan<kThreads>(mine, &tiles, sh_scan)) * n_heads;
+        const int64_t before = rows_seen + block_scan<kThreads>(mine > 0, &rows, sh_scan);
+        locate(r, mine, t0, t0 + before * a.over * n_heads, cost);
+        tiles_seen += tiles;
+        rows_seen += rows;
+        if (r < a.R && mine == 0 && r % grid == cta) sh_none[atomicAdd(&sh_n_none, 1)] = r;
+        __syncthreads();
+        for (int i = 0; i < sh_n_none; ++i) nothing(sh_none[i], tid, kThreads);
+        __syncthreads();
+        if (tid == 0) sh_n_none = 0;
       }
       __syncthreads();
-      if (tid == 0) sh_n_none = 0;
     }
   }
-  __syncthreads();
-  if (!a.ids && a.R > 32) {
-    w.b = sh_b[0];
-    w.b1 = sh_b[1];
-  }
-  if (w.b < w.b1) {
-    if (a.ids) {
-      const int64_t item = w.n_whole + w.b / w.nt_ids;
-      w.head = static_cast<int>(item / a.R);
-      w.row = static_cast<int>(item % a.R);
-      w.tile = static_cast<int>(w.b % w.nt_ids);
-      w.n_tiles = w.nt_ids;
-    } else if (a.R > 32) {
-      w.row = sh_row;
-      w.n_tiles = tiles_of(a, w.row);
-      w.head = sh_head;
-      w.tile = sh_tile;
-    }
-  }
-  *out = w;
+  *out = sh_w;
+  out->left = sh_part[1] - sh_part[0];
 }
 
 }  // namespace
