@@ -525,6 +525,24 @@ def test_calls_on_another_stream_and_in_graphs():
     R.check(out, lse, want)
 
 
+def test_two_streams_at_once():
+    """Cached rows, divided among CTAs and joined, and prompts, on two streams that overlap: as one after the other."""
+    args, _, _ = _cache([5000, 17, 3000], 64, 2, 128, "bf16", seed=41, layers=1, layer=0)
+    qc = [_q(3, 16, 128, 42 + i).to(DEV) for i in range(2)]
+    q, k, v, cu, _ = _prompt([700, 900], [700, 900], 8, 2, 128, seed=43)
+    dq, dk, dv, dcu = q.to(DEV), k.to(DEV), v.to(DEV), _i32(cu)
+    alone = [attend_cached(x, **args) for x in qc], attend_prompt(dq, dk, dv, dcu)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(30):
+        for i, s in enumerate(streams):
+            got.append((i, attend_cached(qc[i], stream=s, **args), attend_prompt(dq, dk, dv, dcu, stream=s)))
+    torch.cuda.synchronize()
+    for i, c, p in got:
+        assert torch.equal(c, alone[0][i]) and torch.equal(p, alone[1])
+
+
 def test_prompt_in_a_graph():
     ql = [50, 140]
     q, k, v, cu, _ = _prompt(ql, ql, 4, 2, 64, seed=40)
