@@ -99,7 +99,8 @@ class AttentionIndex:
         """route_refine, then attention of the same rows over the selected keys: the layer's step for a chunk.
 
         q [T, Hq, D] are the attention queries of the rows at pos0 ..; cache is the PagedCache whose sequence
-        `seq` holds the keys and values of the index's keys.  Returns the attention output [T, Hq, D]."""
+        `seq` holds the keys and values of the index's keys.  Both run on the index's stream: cache.extend and
+        cache.write before it belong there too.  Returns the attention output [T, Hq, D]."""
         with torch.cuda.stream(self.stream):
             ids = self.route_refine(q_index, w, pos0, k, C_budget, out=out_ids)
             return attend_selected(q, ids, cache.k, cache.v, cache.tables[seq:seq + 1], cache.lens[seq:seq + 1],

@@ -578,7 +578,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!x.mixed(j)) continue;
           const uint32_t e = g + 2 * j + 1;
           const int s = e % kSlots;
-          ok = __all_sync(0xffffffffu, mbar_wait(&mx_full[s], (full >> s) & 1, err, abort));
+          // (these warps have nothing to do until an item's last tiles: a long row's time)
+          ok = __all_sync(0xffffffffu, mbar_wait(&mx_full[s], (full >> s) & 1, err, abort, kSpinLimit << 6));
           if (!ok) break;
           full ^= 1u << s;
           const int lo = max(0, x.see(0) - j * kTile), hi = min(kTile, x.lk - j * kTile);

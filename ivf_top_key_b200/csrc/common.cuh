@@ -67,10 +67,10 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
 }
 // Wait for the phase with the given parity to complete.  Gives up (and
 // records DEV_ERR_TIMEOUT, and raises *abort so the other warps stop
-// waiting) after kSpinLimit polls.  Returns false on give-up.
+// waiting) after `limit` polls.  Returns false on give-up.
 __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, int* err,
-                                          volatile int* abort) {
-  for (uint32_t i = 0; i < kSpinLimit; ++i) {
+                                          volatile int* abort, uint32_t limit = kSpinLimit) {
+  for (uint32_t i = 0; i < limit; ++i) {
     if (mbar_try_wait(bar, parity)) return true;
     if ((i & 1023u) == 1023u && *abort) return false;
   }
