@@ -432,6 +432,44 @@ def test_pages_many_sequences_and_pages():
     c.check()
 
 
+def test_pages_behind_four_gib():
+    """Written, forked, attended and moved where byte offsets pass 32 bits (4.7 GB of keys and of values)."""
+    n_pages, page, Hkv, D, n = 36000, 64, 8, 128, 300
+    c = PagedCache(n_pages=n_pages, page_size=page, n_kv_heads=Hkv, head_dim=D, n_seqs=3, max_pages=n_pages)
+    c.extend(_i32([0, 1]), _i32([(n_pages - 8) * page, n]))
+    k, v = (torch.randn(n, Hkv, D, generator=_gen(s)).bfloat16() for s in (60, 61))
+    c.write(_i32([1]), _i32([0, n]), k.to(DEV), v.to(DEV))
+    c.fork(_i32([1]), _i32([2]))
+    assert c.tables[1, :5].tolist() == list(range(n_pages - 8, n_pages - 3))
+    q = _q(2, 16, D, 62)
+    ids = [list(range(0, n, 3)), list(range(n - 1, n - 101, -1))]
+    all_keys = [R.attend(q[i].double(), k.double(), v.double(), D ** -0.5) for i in range(2)]
+    some = [R.attend(q[i].double(), k[ids[i]].double(), v[ids[i]].double(), D ** -0.5) for i in range(2)]
+    for moved in (False, True):
+        if moved:
+            c.free(_i32([0]))
+            c.compact()
+            assert sorted(c.tables[1, :5].tolist() + c.tables[2, 4:5].tolist()) == list(range(6))
+        lse = torch.empty(2, 16, device=DEV)
+        out = c.attend(q.to(DEV), _i32([2, 1]), out_lse=lse)
+        R.check(out, lse, all_keys)
+        out = c.attend_selected(q.to(DEV), _i32(ids), _i32([1, 2]), out_lse=lse)
+        R.check(out, lse, some)
+    c.check()
+
+
+def test_prompt_few_queries_behind_a_long_prefix():
+    L, T, Hq, Hkv, D = 400_000, 3, 2, 1, 64
+    g = torch.Generator(device=DEV).manual_seed(63)
+    k, v = (torch.randn(L, Hkv, D, generator=g, device=DEV).bfloat16() for _ in range(2))
+    q = torch.randn(T, Hq, D, generator=g, device=DEV).bfloat16()
+    lse = torch.empty(T, Hq, device=DEV)
+    out = attend_prompt(q, k, v, _i32([0, T]), _i32([0, L]), out_lse=lse)
+    want = [R.attend(q[i].cpu().double(), k[:L - T + i + 1].cpu().double(), v[:L - T + i + 1].cpu().double(), D ** -0.5)
+            for i in range(T)]
+    R.check(out, lse, want)
+
+
 def test_write_quantises_like_the_key_store():
     from ivf_top_key_b200 import quantize_fp8
     c = PagedCache(n_pages=8, page_size=4, n_kv_heads=3, head_dim=64, n_seqs=2, max_pages=4, dtype="fp8", n_layers=2)
