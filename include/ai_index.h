@@ -382,7 +382,14 @@ int ai_attend_prompt(const void* q_dev, const int64_t* q_strides, const void* k_
                      const int32_t* cu_q_dev, const int32_t* cu_k_dev, int32_t n_seqs,
                      int32_t total_q, int32_t total_k, int32_t n_heads, int32_t n_kv_heads,
                      int32_t head_dim, float scale, void* out_dev, float* lse_dev,
-                     int32_t* status_dev, void* cuda_stream);
+                     int32_t* status_dev, void* workspace_dev, int64_t workspace_bytes,
+                     void* cuda_stream);
+
+/* Bytes of workspace that ai_attend_prompt needs for these sizes, on the
+ * current device: 0 unless there are too few queries to fill it and the
+ * sequences average 1024 keys or more; then the keys are divided.         */
+int ai_attend_prompt_workspace(int32_t n_seqs, int32_t total_q, int32_t total_k, int32_t n_heads,
+                               int32_t n_kv_heads, int32_t head_dim, int64_t* bytes_out);
 
 /* Bytes of workspace that ai_attend_cached and ai_attend_selected need for
  * these heads (whatever the lengths).                                     */

@@ -32,7 +32,7 @@ EXPORTED = [
     "ai_kernel_launches", "ai_select_exhaustive_noalloc", "ai_debug_wait_timeout",
     "ai_route_refine_shard", "ai_merge_topk",
     "ai_debug_refine_kernel", "ai_refine_kernel_choice", "ai_debug_refine_split",
-    "ai_attend_prompt", "ai_attend_workspace", "ai_attend_cached", "ai_attend_selected",
+    "ai_attend_prompt", "ai_attend_prompt_workspace", "ai_attend_workspace", "ai_attend_cached", "ai_attend_selected",
     "ai_cache_workspace", "ai_cache_extend", "ai_cache_write", "ai_cache_fork", "ai_cache_free",
     "ai_cache_compact",
 ]
@@ -106,7 +106,8 @@ def _load():
         "ai_debug_refine_split": [vp, i32],
         "ai_refine_kernel_choice": [vp, i32, ctypes.POINTER(i32)],
         "ai_attend_prompt": [vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, ctypes.c_float,
-                             vp, vp, vp, vp],
+                             vp, vp, vp, vp, i64, vp],
+        "ai_attend_prompt_workspace": [i32, i32, i32, i32, i32, i32, ctypes.POINTER(i64)],
         "ai_attend_workspace": [i32, i32, i32, ctypes.POINTER(i64)],
         "ai_attend_cached": [vp, i32, vp, i32, i32, vp, ctypes.c_float, vp, vp, vp, i64, vp],
         "ai_attend_selected": [vp, i32, vp, vp, i32, i32, i32, vp, ctypes.c_float, vp, vp, vp, i64, vp],
@@ -321,9 +322,18 @@ _Pair = ctypes.c_int64 * 2
 # None) because the callers below check them and strides go separately
 
 def ai_attend_prompt(q, q_strides, k, k_strides, v, v_strides, cu_q, cu_k, n_seqs: int, total_q: int, total_k: int,
-                     n_heads: int, n_kv_heads: int, head_dim: int, scale: float, out, lse, status, stream: int):
+                     n_heads: int, n_kv_heads: int, head_dim: int, scale: float, out, lse, status, workspace,
+                     workspace_bytes: int, stream: int):
     _check(_lib.ai_attend_prompt(q, _Pair(*q_strides), k, _Pair(*k_strides), v, _Pair(*v_strides), cu_q, cu_k, n_seqs,
-                                 total_q, total_k, n_heads, n_kv_heads, head_dim, scale, out, lse, status, stream))
+                                 total_q, total_k, n_heads, n_kv_heads, head_dim, scale, out, lse, status, workspace,
+                                 workspace_bytes, stream))
+
+
+def ai_attend_prompt_workspace(n_seqs: int, total_q: int, total_k: int, n_heads: int, n_kv_heads: int,
+                               head_dim: int) -> int:
+    v = ctypes.c_int64()
+    _check(_lib.ai_attend_prompt_workspace(n_seqs, total_q, total_k, n_heads, n_kv_heads, head_dim, ctypes.byref(v)))
+    return v.value
 
 
 def ai_attend_workspace(n_heads: int, n_kv_heads: int, head_dim: int) -> int:

@@ -125,9 +125,13 @@ def attend_prompt(q, k, v, cu_q, cu_k=None, *, scale=None, out=None, out_lse=Non
         if out is None:
             out = q.new_empty((T, Hq, D))
             po = out.data_ptr()
+        Tk, Hkv = k.shape[0], k.shape[1]
+        B = cu_q.shape[0] - 1
+        n = C.ai_attend_prompt_workspace(B, T, Tk, Hq, Hkv, D) if Tk >= 1024 * B else 0   # (the call costs 1.5 us)
+        ws = q.new_empty((n + 1) // 2) if n else None
         C.ai_attend_prompt(q.data_ptr(), q.stride()[:2], k.data_ptr(), k.stride()[:2], v.data_ptr(), v.stride()[:2],
-                           pq, pk, cu_q.shape[0] - 1, T, k.shape[0], Hq, k.shape[1], D,
-                           D ** -0.5 if scale is None else scale, po, pl, ps, st)
+                           pq, pk, B, T, Tk, Hq, Hkv, D, D ** -0.5 if scale is None else scale, po, pl,
+                           ps, ws.data_ptr() if n else None, n, st)
     return out
 
 

@@ -310,7 +310,8 @@ __global__ void __launch_bounds__(Few<D, FP8>::kThreads, 1) k_attend_few(const R
     // The maximum moves only when it grows by more than 2^kGrow: the weights
     // stay in range and most tiles leave o as it is.  fp8: weights are
     // 2^kLift e^(s - m) * (value scale / largest value scale so far), in f16:
-    // 11 bits down to 2^-25 of the largest, and at most 2^15.
+    // 11 bits down to 2^-25 of the largest, smaller ones to within 2^-36 of
+    // it, and at most 2^15.
     constexpr float kGrow = FP8 ? 4.f : 8.f, kLift = 11.f;
     uint32_t n0 = 0, share = 0;
     // this warp's first tile of a share whose first tile is the CTA's n-th

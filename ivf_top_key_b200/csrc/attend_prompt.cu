@@ -22,6 +22,12 @@
 // the sum inside fp32's range, and the quotient is the same), so the rescale
 // through TMEM is rare.
 //
+// With too few blocks for the SMs (few queries behind a long prefix) an item's
+// key tiles are divided among several CTAs, whose outputs, maxima and sums a
+// second kernel joins, a warp a row: 64 queries of 32 heads on 8, D = 128,
+// behind 131072 keys 1854 -> 228 us, one query 1723 -> 122 us (its keys' and
+// values' bytes alone 81 us), one query behind 2048 keys 38 -> 21 us.
+//
 // Rows that do not see a key must not feel its value, but 0 * NaN is NaN in a
 // matrix product: warps 10-11 look at the V tiles that some row sees in part.
 // Rows behind the sequence's end are zeroed there; if a value before it is not
@@ -154,22 +160,29 @@ struct Item {
   int head, qtok, n_tok;      // key head, first query row, queries in the block (0: nothing to do)
   int k0, lk;                 // first key row, keys of the sequence
   int see0;                   // keys that the block's first query sees (may be <= 0)
-  int tiles[2];               // key tiles that each query tile needs
+  int j0;                     // first key tile of this CTA's part
+  int tiles[2];               // key tiles of the part that each query tile needs
   __device__ int see(int tok) const { return max(0, min(lk, see0 + tok)); }
   __device__ int n() const { return max(tiles[0], tiles[1]); }
-  // whether some row does not see all of key tile j
-  __device__ bool mixed(int j) const { return (j + 1) * kTile > see(0); }
+  // whether some row does not see all of the part's key tile j
+  __device__ bool mixed(int j) const { return (j0 + j + 1) * kTile > see(0); }
 };
 
 struct Schedule {
   int n_slots, qb, tpt;       // slots per key head, queries per block and per tile
   int64_t n_items;
+  int n_split;                // parts of an item's key tiles
+  int* sick;                  // n_split > 1: [n_items][n_split][8] by warp of rows: a value was not finite
+  float2* ml;                 //              [n_items][n_split][256] maximum, sum
+  float* o;                   //              [n_items][n_split][256][D] output before the division
 };
+constexpr int kMaxSplit = 128;
 
 // Slot s belongs to the last sequence b with cu_q[b] / qb + b <= s: each
 // sequence has at least as many slots as blocks.
-__device__ Item item_at(const PromptArgs& a, const Schedule& sc, int64_t it) {
+__device__ Item whole_item(const PromptArgs& a, const Schedule& sc, int64_t it) {
   Item x;
+  x.j0 = 0;
   x.head = static_cast<int>(it % a.Hkv);
   const int slot = sc.n_slots - 1 - static_cast<int>(it / a.Hkv);  // the longest rows first
   int lo = 0, hi = a.n_seqs;
@@ -193,6 +206,19 @@ __device__ Item item_at(const PromptArgs& a, const Schedule& sc, int64_t it) {
     const int last = min((i + 1) * sc.tpt, x.n_tok) - 1;
     x.tiles[i] = last >= i * sc.tpt ? (x.see(last) + kTile - 1) / kTile : 0;
   }
+  return x;
+}
+// The work of block `it`: part it % n_split of item it / n_split.
+template <bool kSplit>
+__device__ Item item_at(const PromptArgs& a, const Schedule& sc, int64_t it) {
+  if (!kSplit) return whole_item(a, sc, it);
+  const int part = static_cast<int>(it % sc.n_split);
+  Item x = whole_item(a, sc, it / sc.n_split);
+  const int64_t n = x.n();
+  x.j0 = static_cast<int>(n * part / sc.n_split);
+  const int j1 = static_cast<int>(n * (part + 1) / sc.n_split);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) x.tiles[i] = max(0, min(x.tiles[i], j1) - x.j0);
   return x;
 }
 
@@ -319,7 +345,7 @@ __device__ __forceinline__ bool elect_one() {
 
 __device__ int g_no_status;  // where flags go when the caller gives no status word
 
-template <int D>
+template <int D, bool kSplit>
 __global__ void __launch_bounds__(kThreads, 1)
     k_prompt_tc(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                 const __grid_constant__ CUtensorMap map_v, const PromptArgs a, const Schedule sc) {
@@ -406,7 +432,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // the next item is asked for while this one is loaded
         if (r >= 2 && !all(mbar_wait(&next_read[r & 1], ((r >> 1) - 1) & 1, err, abort))) break;
         if (leader) take_request(&answer[r & 1], &next_full[r & 1]);
-        const Item x = item_at(a, sc, it);
+        const Item x = item_at<kSplit>(a, sc, it);
         for (int i = 0; ok && i < 2; ++i) {
           if (x.tiles[i] == 0) continue;
           if (nq[i] > 0 && !all(mbar_wait(&q_empty[i], (nq[i] - 1) & 1, err, abort))) {
@@ -441,7 +467,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_arrive_expect_tx(full, L::kTileBytes);
             for (int c = 0; c < L::kHalves; ++c)
               tma_load_3d(ring + s * L::kTileBytes + c * (kTile * 128), t & 1 ? &map_v : &map_k, c * 64, x.head,
-                          x.k0 + (t >> 1) * kTile, full);
+                          x.k0 + (x.j0 + (t >> 1)) * kTile, full);
           }
         }
         if (ok) it = next_item(r);
@@ -504,7 +530,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       uint32_t r = 0;
       for (int64_t it = blockIdx.x; ok && it >= 0; it = next_item(r++)) {
-        const Item x = item_at(a, sc, it);
+        const Item x = item_at<kSplit>(a, sc, it);
         const int n = x.n();
         if (n == 0) continue;
         ok = wait_slot(slot);
@@ -572,7 +598,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       uint32_t r = 0;
       for (int64_t it = blockIdx.x; ok && it >= 0; it = next_item(r++)) {
-        const Item x = item_at(a, sc, it);
+        const Item x = item_at<kSplit>(a, sc, it);
         const int n = x.n();
         for (int j = 0; ok && j < n; ++j) {
           if (!x.mixed(j)) continue;
@@ -582,7 +608,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = __all_sync(0xffffffffu, mbar_wait(&mx_full[s], (full >> s) & 1, err, abort, kSpinLimit << 6));
           if (!ok) break;
           full ^= 1u << s;
-          const int lo = max(0, x.see(0) - j * kTile), hi = min(kTile, x.lk - j * kTile);
+          const int lo = max(0, x.see(0) - (x.j0 + j) * kTile), hi = min(kTile, x.lk - (x.j0 + j) * kTile);
           uint32_t bad = 0;
           // 16-byte unit u of the tile: row (u / 8) % 128; the swizzle stays within a row
           for (int u = t; u < L::kTileBytes / 16; u += 64) {
@@ -620,7 +646,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     uint32_t r = 0;
     for (int64_t it = blockIdx.x; ok && it >= 0; it = next_item(r++)) {
-      const Item x = item_at(a, sc, it);
+      const Item x = item_at<kSplit>(a, sc, it);
       const int n = x.tiles[i];
       const int see = x.see(tok);
       float m = -INFINITY, l = 0.f;
@@ -628,8 +654,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = __all_sync(0xffffffffu, mbar_wait(&s_full[i], np & 1, err, abort));
         if (!ok) break;
         tc_fence_after();
-        const int limit = see - j * kTile;
-        const bool part = (j + 1) * kTile > x.see(i * sc.tpt);  // warp-uniform
+        const int limit = see - (x.j0 + j) * kTile;
+        const bool part = (x.j0 + j + 1) * kTile > x.see(i * sc.tpt);  // warp-uniform
         float v[kTile];
 #pragma unroll
         for (int c = 0; c < 4; ++c) tmem_ld32(ts + c * 32, v + c * 32);
@@ -700,7 +726,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const bool mine = used && tok < x.n_tok;
       const bool again = reinterpret_cast<volatile int*>(sick)[item % L::kSick] == item + 1;
-      if (n > 0 && __any_sync(0xffffffffu, again)) {
+      const bool redo = n > 0 && __any_sync(0xffffffffu, again);
+      if (kSplit) {
+        // this part's share of the rows, for the joining kernel
+        if (lane == 0) sc.sick[it * 8 + warp] = redo;
+        const int64_t at = it * (2 * kTile) + i * kTile + row;
+        if (mine) sc.ml[at] = make_float2(m, l);
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          float v[32];
+          if (n == 0) break;
+          tmem_ld32(to + c * 32, v);
+          tmem_ld_wait();
+          if (mine && l != 0.f) {
+#pragma unroll
+            for (int u = 0; u < 32; u += 4)
+              *reinterpret_cast<float4*>(sc.o + at * D + c * 32 + u) = make_float4(v[u], v[u + 1], v[u + 2], v[u + 3]);
+          }
+        }
+      } else if (redo) {
         // each warp its own rows: the other tile's keys may be looked at meanwhile
         for (int rr = (warp & 3) * 32; rr < min(sc.tpt * a.G, (warp & 3) * 32 + 32); ++rr) {
           const int tt = i * sc.tpt + rr / a.G;
@@ -744,6 +788,78 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
+// Joins the parts of items (n_split > 1): a warp per row.
+template <int D>
+__global__ void __launch_bounds__(256) k_prompt_join(const PromptArgs a, const Schedule sc) {
+  dependency_wait();
+  const int lane = threadIdx.x & 31;
+  const int64_t w = blockIdx.x * 8ll + (threadIdx.x >> 5), id = w / (2 * kTile);
+  const int r = static_cast<int>(w % (2 * kTile)), row = r % kTile;
+  if (id >= sc.n_items || row >= sc.tpt * a.G) return;
+  const Item x = whole_item(a, sc, id);
+  const int tok = r / kTile * sc.tpt + row / a.G;
+  if (tok >= x.n_tok) return;
+  const int64_t part0 = id * sc.n_split;
+  float2 ml[kMaxSplit / 32];
+  float m = -INFINITY, l = 0.f;
+  bool sick = false;
+#pragma unroll
+  for (int u = 0; u < kMaxSplit / 32; ++u) {
+    const int s = u * 32 + lane;
+    ml[u] = make_float2(-INFINITY, 0.f);
+    if (s < sc.n_split) {
+      ml[u] = sc.ml[(part0 + s) * (2 * kTile) + r];
+      sick |= sc.sick[(part0 + s) * 8 + r / 32] != 0;
+    }
+    m = fmaxf(m, ml[u].x);
+  }
+  const int head = x.head * a.G + row % a.G;
+  if (__any_sync(0xffffffffu, sick)) {
+    attend_row<D>(a, x.qtok + tok, head, x.k0, x.see(tok));
+    return;
+  }
+  for (int i = 16; i > 0; i >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, i));
+  const float mz = m == -INFINITY ? 0.f : m;
+  float o[D / 32];
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) o[i] = 0.f;
+#pragma unroll
+  for (int u = 0; u < kMaxSplit / 32; ++u) {
+    const float f = ex2(ml[u].x - mz);
+    if (ml[u].y != 0.f) l += ml[u].y * f;
+    for (uint32_t some = __ballot_sync(0xffffffffu, ml[u].y != 0.f); some; some &= some - 1) {
+      const int s = __ffs(some) - 1;
+      const float fs = __shfl_sync(0xffffffffu, f, s);
+      const float* from = sc.o + ((part0 + u * 32 + s) * (2 * kTile) + r) * D;
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) o[i] = fmaf(from[i * 32 + lane], fs, o[i]);
+    }
+  }
+  for (int i = 16; i > 0; i >>= 1) l += __shfl_xor_sync(0xffffffffu, l, i);
+  const int64_t at = static_cast<int64_t>(x.qtok + tok) * a.Hq + head;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) {
+    const __nv_bfloat16 b = __float2bfloat16_rn(o[i] * inv);
+    a.out[at * D + i * 32 + lane] = *reinterpret_cast<const uint16_t*>(&b);
+  }
+  if (a.lse && lane == 0) a.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+}
+
+// Parts of an item: none where the items fill half of the SMs, else as many as
+// fill them with at least 512 keys of an average sequence each (a shorter part
+// is over before the join pays).
+int parts_of(int64_t n_items, int64_t total_k, int64_t n_seqs) {
+  const int64_t sms = device_sms(), keys = total_k / (n_seqs > 0 ? n_seqs : 1);
+  if (n_items <= 0 || 2 * n_items > sms || keys < 1024) return 1;
+  int64_t s = sms / n_items;
+  s = s < keys / 512 ? s : keys / 512;
+  return static_cast<int>(s < kMaxSplit ? s : kMaxSplit);
+}
+int64_t part_bytes(int64_t n_items, int n_split, int D) {
+  return n_split == 1 ? 0 : n_items * n_split * (8 * 4 + 2 * kTile * (8 + 4ll * D));
+}
+
 // Tensor map of [tokens, heads, D] bf16 with a box of 64 elements x
 // box_heads x box_tokens, 128-byte swizzle; out-of-range rows read 0.
 bool map_rows(CUtensorMap* m, const void* p, int64_t tokens, int heads, int D, int64_t tok_stride, int64_t head_stride,
@@ -769,24 +885,43 @@ bool map_rows(CUtensorMap* m, const void* p, int64_t tokens, int heads, int D, i
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D>
+template <int D, bool kSplit>
 cudaError_t launch_prompt(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const PromptArgs& a,
                           const Schedule& sc, cudaStream_t st) {
   static ReadyOnce ready;
-  const cudaError_t e = ready.shared_memory(k_prompt_tc<D>, Smem<D>::kBytes);
+  cudaError_t e = ready.shared_memory(k_prompt_tc<D, kSplit>, Smem<D>::kBytes);
   if (e != cudaSuccess) return e;
-  return launch_after(k_prompt_tc<D>, dim3(static_cast<unsigned>(sc.n_items)), dim3(kThreads), Smem<D>::kBytes, st, mq, mk,
-                      mv, a, sc);
+  e = launch_after(k_prompt_tc<D, kSplit>, dim3(static_cast<unsigned>(sc.n_items * sc.n_split)), dim3(kThreads),
+                   Smem<D>::kBytes, st, mq, mk, mv, a, sc);
+  if (e != cudaSuccess || !kSplit) return e;
+  return launch_after(k_prompt_join<D>, dim3(static_cast<unsigned>(sc.n_items * (2 * kTile / 8))), dim3(256), 0, st, a, sc);
+}
+template <int D>
+cudaError_t launch_prompt(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const PromptArgs& a,
+                          const Schedule& sc, cudaStream_t st) {
+  return sc.n_split > 1 ? launch_prompt<D, true>(mq, mk, mv, a, sc, st) : launch_prompt<D, false>(mq, mk, mv, a, sc, st);
 }
 
 }  // namespace
 }  // namespace aiidx
 
+extern "C" int ai_attend_prompt_workspace(int32_t n_seqs, int32_t total_q, int32_t total_k, int32_t n_heads,
+                                          int32_t n_kv_heads, int32_t head_dim, int64_t* bytes_out) {
+  using namespace aiidx;
+  if (!bytes_out || n_seqs < 0 || total_q < 0 || total_k < 0 || n_heads <= 0 || n_kv_heads <= 0 ||
+      n_heads % n_kv_heads != 0 || n_heads / n_kv_heads > kTile || head_dim <= 0)
+    return fail(AI_ERR_ARG, "bad sizes or null output");
+  const int64_t items = (static_cast<int64_t>(total_q) / (2 * (kTile / (n_heads / n_kv_heads))) + n_seqs) * n_kv_heads;
+  *bytes_out = part_bytes(items, parts_of(items, total_k, n_seqs), head_dim);
+  return AI_OK;
+}
+
 extern "C" int ai_attend_prompt(const void* q_dev, const int64_t* q_strides, const void* k_dev,
                                 const int64_t* k_strides, const void* v_dev, const int64_t* v_strides,
                                 const int32_t* cu_q_dev, const int32_t* cu_k_dev, int32_t n_seqs, int32_t total_q,
                                 int32_t total_k, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim, float scale,
-                                void* out_dev, float* lse_dev, int32_t* status_dev, void* cuda_stream) {
+                                void* out_dev, float* lse_dev, int32_t* status_dev, void* workspace_dev,
+                                int64_t workspace_bytes, void* cuda_stream) {
   using namespace aiidx;
   if (!q_strides || !k_strides || !v_strides || !cu_q_dev || !cu_k_dev) return fail(AI_ERR_ARG, "null pointer argument");
   if (n_seqs < 0 || total_q < 0 || total_k < 0) return fail(AI_ERR_ARG, "negative sequence or token count");
@@ -840,6 +975,19 @@ extern "C" int ai_attend_prompt(const void* q_dev, const int64_t* q_strides, con
   sc.n_slots = static_cast<int>(slots);
   sc.n_items = slots * n_kv_heads;
   if (sc.n_items > 0x7fffffff) return fail(AI_ERR_ARG, "too many query blocks");
+  sc.n_split = parts_of(sc.n_items, total_k, n_seqs);
+  sc.sick = nullptr;
+  sc.ml = nullptr;
+  sc.o = nullptr;
+  if (sc.n_split > 1) {
+    if (!workspace_dev || reinterpret_cast<uintptr_t>(workspace_dev) % 16 != 0 ||
+        workspace_bytes < part_bytes(sc.n_items, sc.n_split, head_dim))
+      return fail(AI_ERR_ARG, "workspace too small or not 16-byte aligned");
+    const int64_t parts = sc.n_items * sc.n_split;
+    sc.o = static_cast<float*>(workspace_dev);
+    sc.ml = reinterpret_cast<float2*>(sc.o + parts * 2 * kTile * head_dim);
+    sc.sick = reinterpret_cast<int*>(sc.ml + parts * 2 * kTile);
+  }
   CUtensorMap mq, mk, mv;
   // without keys nothing is loaded, but a map needs a row
   const bool none = total_k == 0;

@@ -297,7 +297,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // The maximum moves only when it grows by more than 2^kGrow: the weights
     // stay in range and most tiles leave o as it is.  fp8: weights are
     // 2^kLift e^(s - m) * (value scale / largest value scale so far), in f16:
-    // 11 bits down to 2^-25 of the largest, and at most 2^15.
+    // 11 bits down to 2^-25 of the largest, smaller ones to within 2^-36 of
+    // it, and at most 2^15.
     constexpr float kGrow = FP8 ? 4.f : 8.f, kLift = 11.f;
 
     uint32_t n = 0, n_shares = 0;

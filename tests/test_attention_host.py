@@ -87,8 +87,22 @@ def test_bad_prompt_arguments_are_refused(args, match):
              ks=(256, 128), vs=(256, 128)) | args
     with pytest.raises(C.AiError, match=match) as e:
         C.ai_attend_prompt(a["q"], a["qs"], a["k"], a["ks"], a["v"], a["vs"], a["cu_q"], P, a["n_seqs"], a["total_q"],
-                           a["total_k"], a["Hq"], 2, a["D"], a["scale"], a["out"], None, None, 0)
+                           a["total_k"], a["Hq"], 2, a["D"], a["scale"], a["out"], None, None, None, 0, 0)
     assert e.value.code == -1
+
+
+def test_prompt_workspace_is_needed_only_where_keys_are_divided():
+    assert C.ai_attend_prompt_workspace(4, 8192, 8192, 32, 8, 128) == 0    # enough blocks
+    assert C.ai_attend_prompt_workspace(1, 3, 900, 4, 2, 128) == 0         # few keys
+    need = C.ai_attend_prompt_workspace(1, 3, 100000, 4, 2, 128)
+    assert need > 0
+    for ws, n in ((None, need), (P, need - 1), (P + 8, need)):
+        with pytest.raises(C.AiError, match="workspace"):
+            C.ai_attend_prompt(P, (512, 128), P, (256, 128), P, (256, 128), P, P, 1, 3, 100000, 4, 2, 128, 1.0, P, None,
+                               None, ws, n, 0)
+    for bad in ((-1, 3, 9, 4, 2, 128), (1, 3, 9, 5, 2, 128), (1, 3, 9, 258, 2, 128), (1, 3, 9, 4, 2, 0)):
+        with pytest.raises(C.AiError, match="sizes"):
+            C.ai_attend_prompt_workspace(*bad)
 
 
 def test_bad_lists_and_workspaces_are_refused():
@@ -117,7 +131,8 @@ def test_calls_with_nothing_to_do_launch_nothing():
     C.ai_cache_free(_cache(), None, 0, 0)
     C.ai_cache_write(_cache(), 0, None, None, None, None, 0, 0, 0)
     C.ai_attend_cached(_cache(), 0, P, 0, 4, P, 1.0, P, None, P, 1 << 40, 0)
-    C.ai_attend_prompt(None, (512, 128), P, (256, 128), P, (256, 128), P, P, 3, 0, 4, 4, 2, 128, 1.0, None, None, None, 0)
+    C.ai_attend_prompt(None, (512, 128), P, (256, 128), P, (256, 128), P, P, 3, 0, 4, 4, 2, 128, 1.0, None, None, None, None, 0,
+                       0)
     assert C.ai_kernel_launches() == before
 
 

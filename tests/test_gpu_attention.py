@@ -281,6 +281,30 @@ def test_prompt_matches_float64(Hq, Hkv, D, ql, kl):
     assert status.item() == 0
 
 
+@pytest.mark.parametrize("Hq,Hkv,D,ql,kl", [
+    (2, 1, 128, [1], [3000]),
+    (8, 2, 64, [40, 0, 3], [3000, 2000, 5000]),
+    (6, 2, 128, [5, 30], [100, 9000]),
+    (128, 1, 64, [4], [4000]),
+])
+def test_prompt_few_queries_divide_the_keys(Hq, Hkv, D, ql, kl):
+    q, k, v, cu_q, cu_k = _prompt(ql, kl, Hq, Hkv, D, seed=sum(kl), pad=2)
+    n = len(q)
+    for bad in (None, torch.nan):
+        if bad is not None:   # a value that the last sequence's last query alone sees
+            v[cu_k[-1] - 1, 0, 5] = bad
+        out = torch.full((n, Hq, D), 7.0, dtype=torch.bfloat16, device=DEV)
+        lse = torch.full((n, Hq), 7.0, device=DEV)
+        attend_prompt(q.to(DEV), k.to(DEV), v.to(DEV), _i32(cu_q), _i32(cu_k), out=out, out_lse=lse)
+        want = _prompt_want(q, k, v, cu_q, cu_k, D ** -0.5)
+        rows = len(want) if bad is None else len(want) - 1
+        if rows:
+            R.check(out[2:2 + rows], lse[2:2 + rows], want[:rows])
+        assert (out[:2] == 7).all() and (out[-2:] == 7).all() and (lse[-2:] == 7).all()
+        if bad is not None:
+            assert out[n - 3, :Hq // Hkv, 5].isnan().all()
+
+
 def test_prompt_long_sampled_rows():
     L, Hq, Hkv, D = 5000, 4, 1, 128
     q, k, v, cu_q, _ = _prompt([L], [L], Hq, Hkv, D, seed=21)
@@ -597,6 +621,32 @@ def test_prompt_in_a_graph():
     g.replay()
     torch.cuda.synchronize()
     R.check(out, lse, _prompt_want(q, k, v, cu, cu, 0.125))
+
+
+def test_divided_prompts_in_graphs_and_between_them():
+    # each call has its own workspace: two graphs, and eager calls of other sizes between their replays
+    shapes = [([3], [4000]), ([17, 2], [2500, 3100])]
+    graphs, s = [], torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    for ql, kl in shapes:
+        q, k, v, cu_q, cu_k = _prompt(ql, kl, 8, 2, 64, seed=kl[0])
+        d = [x.to(DEV) for x in (q, k, v)] + [_i32(cu_q), _i32(cu_k)]
+        lse = torch.empty(len(q), 8, device=DEV)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            out = attend_prompt(*d, out_lse=lse)
+        graphs.append((g, d, out, lse, (q, k, v, cu_q, cu_k)))
+    for turn in range(3):
+        for g, d, out, lse, host in graphs:
+            out.fill_(7), lse.fill_(7)
+            g.replay()
+        eager = [attend_prompt(*d) for _, d, _, _, _ in graphs]
+        torch.cuda.synchronize()
+        for (g, d, out, lse, host), e in zip(graphs, eager):
+            assert torch.equal(out, e)
+            if turn == 0:
+                R.check(out, lse, _prompt_want(*host, 0.125))
 
 
 def test_empty_calls():
