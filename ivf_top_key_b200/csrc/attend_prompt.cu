@@ -22,11 +22,11 @@
 // the sum inside fp32's range, and the quotient is the same), so the rescale
 // through TMEM is rare.
 //
-// With too few blocks for the SMs (few queries behind a long prefix) an item's
-// key tiles are divided among several CTAs, whose outputs, maxima and sums a
+// With too few blocks to fill the SMs evenly (few queries behind a long prefix)
+// an item's key tiles are divided among several CTAs, whose outputs, maxima and sums a
 // second kernel joins, a warp a row: 64 queries of 32 heads on 8, D = 128,
-// behind 131072 keys 1854 -> 228 us, one query 1723 -> 122 us (its keys' and
-// values' bytes alone 81 us), one query behind 2048 keys 38 -> 21 us.
+// behind 131072 keys 1851 -> 139 us, one query 1696 -> 121 us (its keys' and
+// values' bytes alone 81 us), one query behind 2048 keys 37 -> 21 us.
 //
 // Rows that do not see a key must not feel its value, but 0 * NaN is NaN in a
 // matrix product: warps 10-11 look at the V tiles that some row sees in part.
@@ -846,15 +846,32 @@ __global__ void __launch_bounds__(256) k_prompt_join(const PromptArgs a, const S
   if (a.lse && lane == 0) a.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
-// Parts of an item: none where the items fill half of the SMs, else as many as
-// fill them with at least 512 keys of an average sequence each (a shorter part
-// is over before the join pays).
-int parts_of(int64_t n_items, int64_t total_k, int64_t n_seqs) {
-  const int64_t sms = device_sms(), keys = total_k / (n_seqs > 0 ? n_seqs : 1);
-  if (n_items <= 0 || 2 * n_items > sms || keys < 1024) return 1;
-  int64_t s = sms / n_items;
-  s = s < keys / 512 ? s : keys / 512;
-  return static_cast<int>(s < kMaxSplit ? s : kMaxSplit);
+// Blocks that sequences of total_q queries can take: each starts at slot
+// cu_q[b] / qb + b, so the last one ends by total_q / qb, rounded up, + n_seqs - 1.
+int64_t slots_of(int64_t total_q, int64_t n_seqs, int64_t qb) { return (total_q + qb - 1) / qb + n_seqs - 1; }
+
+// Parts of an item, by the time that the sequences' average lengths suggest, in
+// key tiles (1.75 us at D = 128): the rounds of CTAs that the items take, or the
+// longest item, with 6 tiles to begin and end an item, 2 for the second launch
+// and what the parts' outputs take to write and read.  A part has at least 512
+// keys, and the parts' workspace ends at four parts an SM (78 MB).  Divided only
+// where a tenth is gained: 32 heads on 8 behind 65536 keys, 256 queries 938 ->
+// 256 us, 600 queries 942 -> 612, 1200 queries (152 items) 1925 -> 1305.
+int parts_of(int64_t n_slots, int64_t total_q, int64_t total_k, int64_t n_seqs, int64_t n_kv_heads) {
+  const int64_t sms = device_sms();
+  if (n_seqs <= 0 || n_slots <= 0 || total_k / n_seqs < 1024) return 1;
+  const double keys = static_cast<double>(total_k) / n_seqs, queries = static_cast<double>(total_q) / n_seqs;
+  const double longest = keys / kTile, mean = fmax(keys - queries / 2, keys / 2) / kTile;
+  // half of the sequences' last blocks are taken to be there
+  const int64_t items = (n_slots - (n_seqs - 1) / 2) * n_kv_heads;
+  auto cost = [&](int64_t s) {
+    const int64_t rounds = (items * s + sms - 1) / sms;
+    return fmax(longest, rounds * mean) / s + 6 * rounds + (s > 1 ? 2 + 3.0 * items * s / sms : 0);
+  };
+  int64_t best = 1;
+  for (int64_t s = 2; s <= kMaxSplit && s * 512 <= keys && s * n_slots * n_kv_heads <= 4 * sms; ++s)
+    if (cost(s) < cost(best)) best = s;
+  return cost(best) < 0.9 * cost(1) ? static_cast<int>(best) : 1;
 }
 int64_t part_bytes(int64_t n_items, int n_split, int D) {
   return n_split == 1 ? 0 : n_items * n_split * (8 * 4 + 2 * kTile * (8 + 4ll * D));
@@ -911,8 +928,8 @@ extern "C" int ai_attend_prompt_workspace(int32_t n_seqs, int32_t total_q, int32
   if (!bytes_out || n_seqs < 0 || total_q < 0 || total_k < 0 || n_heads <= 0 || n_kv_heads <= 0 ||
       n_heads % n_kv_heads != 0 || n_heads / n_kv_heads > kTile || head_dim <= 0)
     return fail(AI_ERR_ARG, "bad sizes or null output");
-  const int64_t items = (static_cast<int64_t>(total_q) / (2 * (kTile / (n_heads / n_kv_heads))) + n_seqs) * n_kv_heads;
-  *bytes_out = part_bytes(items, parts_of(items, total_k, n_seqs), head_dim);
+  const int64_t slots = slots_of(total_q, n_seqs, 2 * (kTile / (n_heads / n_kv_heads)));
+  *bytes_out = part_bytes(slots * n_kv_heads, parts_of(slots, total_q, total_k, n_seqs, n_kv_heads), head_dim);
   return AI_OK;
 }
 
@@ -970,12 +987,12 @@ extern "C" int ai_attend_prompt(const void* q_dev, const int64_t* q_strides, con
   Schedule sc;
   sc.tpt = kTile / a.G;
   sc.qb = 2 * sc.tpt;
-  const int64_t slots = static_cast<int64_t>(total_q) / sc.qb + n_seqs;
+  const int64_t slots = slots_of(total_q, n_seqs, sc.qb);
   if (slots > 0x7fffffff) return fail(AI_ERR_ARG, "too many query blocks");
   sc.n_slots = static_cast<int>(slots);
   sc.n_items = slots * n_kv_heads;
   if (sc.n_items > 0x7fffffff) return fail(AI_ERR_ARG, "too many query blocks");
-  sc.n_split = parts_of(sc.n_items, total_k, n_seqs);
+  sc.n_split = parts_of(slots, total_q, total_k, n_seqs, n_kv_heads);
   sc.sick = nullptr;
   sc.ml = nullptr;
   sc.o = nullptr;
