@@ -424,9 +424,9 @@ int ai_attend_selected(const ai_cache* cache, int32_t layer, const void* q_dev,
 int ai_cache_workspace(const ai_cache* cache, int32_t n, int64_t* bytes_out);
 
 /* Lengthen sequence seqs[i] by counts[i] tokens, taking pages as needed.  A
- * sequence is lengthened if the pages it and the listed ones before it need
- * are there.  The new tokens' contents come with ai_cache_write, once per
- * layer.                                                                  */
+ * sequence is lengthened if it needs no page, or if the pages it and the
+ * listed ones before it need are there.  The new tokens' contents come with
+ * ai_cache_write, once per layer.                                         */
 int ai_cache_extend(const ai_cache* cache, const int32_t* seqs_dev, const int32_t* counts_dev,
                     int32_t n, void* workspace_dev, int64_t workspace_bytes, void* cuda_stream);
 

@@ -102,8 +102,8 @@ __device__ int lowest_free(const View& c, int want, int32_t* list, int* sums) {
 
 // ------------------------------------------------------------------- extend
 // Two passes over the list: pages each sequence needs with their prefix,
-// then the assignment.  scratch: [n] first page rank (-1: refused), then the
-// free pages.
+// then the assignment.  scratch: [n] first page rank (-1: refused, -2: more
+// pages than the cache has), then the free pages.
 __global__ void __launch_bounds__(kPlan) k_extend(View c, const int32_t* seqs, const int32_t* counts, int n,
                                                   int32_t* scratch) {
   __shared__ int sums[32];
@@ -135,7 +135,8 @@ __global__ void __launch_bounds__(kPlan) k_extend(View c, const int32_t* seqs, c
     const int p = plan_scan(need, &total, sums);
     if (i < n) {
       const int64_t at = before + p;
-      rank[i] = !ok ? -1 : (at + need > c.n_pages ? -2 : static_cast<int>(at));
+      // an entry that needs no page is lengthened whatever the ones before it ask for
+      rank[i] = !ok ? -1 : (need > 0 && at + need > c.n_pages ? -2 : static_cast<int>(at));
     }
     before = before + total > most ? most : before + total;
   }
