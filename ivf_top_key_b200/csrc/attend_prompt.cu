@@ -29,10 +29,11 @@
 // values' bytes alone 81 us), one query behind 2048 keys 37 -> 21 us.
 //
 // Rows that do not see a key must not feel its value, but 0 * NaN is NaN in a
-// matrix product: warps 10-11 look at the V tiles that some row sees in part.
-// Rows behind the sequence's end are zeroed there; if a value before it is not
-// finite, the item is computed again by attend_row, which reads only the keys
-// that each row sees.
+// matrix product: warps 10-11 look at the V tiles that not every row sees whole.
+// Rows behind the sequence's end are zeroed there, and so are values that are
+// not finite, whose keys are listed; the rows that see such a key add its
+// infinity or NaN to their outputs at the end.  So the bits of every other
+// output are what they would be without it.
 //
 // Measured: 16384 tokens, 16 heads on 2, D = 128: 0.89 ms in a short run (1230
 // TFLOP/s, 0.75 of the measured bf16 product), 1.02 ms in a long one; a chunk of
@@ -90,50 +91,6 @@ __device__ __forceinline__ bool seq_rows(const PromptArgs& a, int b, int* q0, in
   return ok;
 }
 
-// One query row of one head by one warp, reading only the keys it sees.
-template <int D>
-__device__ __forceinline__ void attend_row(const PromptArgs& a, int qi, int h, int k0, int n_keys) {
-  const int lane = threadIdx.x & 31;
-  const uint16_t* q = a.q + qi * a.q_tok + h * a.q_head;
-  const int kh = h / a.G;
-  float m = -INFINITY, l = 0.f, o[D / 32];
-#pragma unroll
-  for (int i = 0; i < D / 32; ++i) o[i] = 0.f;
-  for (int j0 = 0; j0 < n_keys; j0 += 32) {
-    const int j = j0 + lane;
-    float s = -INFINITY;
-    if (j < n_keys) {
-      const uint16_t* k = a.k + static_cast<int64_t>(k0 + j) * a.k_tok + kh * a.k_head;
-      float x = 0.f;
-      for (int d = 0; d < D; ++d) x = fmaf(bf16_bits_to_f32(q[d]), bf16_bits_to_f32(k[d]), x);
-      s = x * a.c2;
-    }
-    float mx = s;
-    for (int i = 16; i > 0; i >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, i));
-    const float mn = fmaxf(m, mx), mz = mn == -INFINITY ? 0.f : mn;
-    const float f = exp2f(m - mz), p = exp2f(s - mz);
-    m = mn;
-    l = l * f + p;
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i) o[i] *= f;
-    const int n = min(32, n_keys - j0);
-    for (int jj = 0; jj < n; ++jj) {
-      const float pj = __shfl_sync(0xffffffffu, p, jj);
-      const uint16_t* v = a.v + static_cast<int64_t>(k0 + j0 + jj) * a.v_tok + kh * a.v_head;
-#pragma unroll
-      for (int i = 0; i < D / 32; ++i) o[i] = fmaf(pj, bf16_bits_to_f32(v[i * 32 + lane]), o[i]);
-    }
-  }
-  for (int i = 16; i > 0; i >>= 1) l += __shfl_xor_sync(0xffffffffu, l, i);
-  uint16_t* out = a.out + (static_cast<int64_t>(qi) * a.Hq + h) * D;
-#pragma unroll
-  for (int i = 0; i < D / 32; ++i) {
-    const __nv_bfloat16 b = __float2bfloat16_rn(l == 0.f ? 0.f : o[i] / l);
-    out[i * 32 + lane] = *reinterpret_cast<const uint16_t*>(&b);
-  }
-  if (a.lse && lane == 0) a.lse[static_cast<int64_t>(qi) * a.Hq + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
-}
-
 // ------------------------------------------------------------ tensor cores
 constexpr int kTile = 128;        // rows of a query tile, keys of a key tile
 constexpr int kThreads = 384;
@@ -147,8 +104,11 @@ struct Smem {
   static constexpr int kTileBytes = kTile * D * 2;
   static constexpr int kSlots = D == 128 ? 5 : 8; // ring of K and V tiles
   static constexpr int kBars = 4 + 4 * kSlots + 6 + 4;
-  static constexpr int kSick = 8;                 // > items that the ring can be ahead
-  static constexpr int kBytes = 1024 + (2 + kSlots) * kTileBytes + kBars * 8 + 16 + 32 + 8 + kSick * 4;
+  // lists of values that are not finite: of so many items (next_read holds the
+  // loads to two items ahead of the slowest warp) and, of each, so many tiles that
+  // not every row sees whole (its queries see up to 255 keys more than its first)
+  static constexpr int kLists = 4, kPartly = 3;
+  static constexpr int kBytes = 1024 + (2 + kSlots) * kTileBytes + kBars * 8 + 16 + 32 + kLists * kPartly * 16 + 8;
   static_assert(kBytes <= 227 * 1024, "shared memory");
 };
 
@@ -164,7 +124,8 @@ struct Item {
   int tiles[2];               // key tiles of the part that each query tile needs
   __device__ int see(int tok) const { return max(0, min(lk, see0 + tok)); }
   __device__ int n() const { return max(tiles[0], tiles[1]); }
-  // whether some row does not see all of the part's key tile j
+  // the part's first key tile that some row does not see all of
+  __device__ int first_mixed() const { return max(0, see(0) / kTile - j0); }
   __device__ bool mixed(int j) const { return (j0 + j + 1) * kTile > see(0); }
 };
 
@@ -172,8 +133,7 @@ struct Schedule {
   int n_slots, qb, tpt;       // slots per key head, queries per block and per tile
   int64_t n_items;
   int n_split;                // parts of an item's key tiles
-  int* sick;                  // n_split > 1: [n_items][n_split][8] by warp of rows: a value was not finite
-  float2* ml;                 //              [n_items][n_split][256] maximum, sum
+  float2* ml;                 // n_split > 1: [n_items][n_split][256] maximum, sum
   float* o;                   //              [n_items][n_split][256][D] output before the division
 };
 constexpr int kMaxSplit = 128;
@@ -343,6 +303,32 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
+// Adds to columns [c, c + 32) of a row's output the values that are not finite
+// of the listed keys that it sees: their weight is positive, so what matters is
+// their sign.  Bit b of list[q][u]: key u + 8 b of the part's key tile j + q.
+__device__ __forceinline__ void add_listed(const PromptArgs& a, const Item& x, const uint16_t (*list)[8], int j, int n,
+                                           int see, int c, float* y) {
+  for (int q = 0; j + q < n; ++q) {
+    for (int u = 0; u < 8; ++u) {
+      for (uint32_t bits = list[q][u]; bits; bits &= bits - 1) {
+        const int key = (x.j0 + j + q) * kTile + u + 8 * (__ffs(bits) - 1);
+        if (key >= see) continue;
+        const uint4* v = reinterpret_cast<const uint4*>(a.v + (x.k0 + key) * a.v_tok + x.head * a.v_head + c);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint4 w = v[i];
+          const uint32_t pair[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int h = 0; h < 8; ++h) {
+            const float f = __uint_as_float(h & 1 ? pair[h / 2] & 0xffff0000u : pair[h / 2] << 16);
+            if (f - f != 0.f) y[i * 8 + h] += f;
+          }
+        }
+      }
+    }
+  }
+}
+
 __device__ int g_no_status;  // where flags go when the caller gives no status word
 
 template <int D, bool kSplit>
@@ -368,9 +354,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* next_full = o_full + 2;                // [2] next item known
   uint64_t* next_read = next_full + 2;             // [2] and read by every warp
   uint4* answer = reinterpret_cast<uint4*>((reinterpret_cast<uintptr_t>(next_read + 2) + 15) & ~uintptr_t(15));  // [2]
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(answer + 2);
+  uint16_t (*lists)[L::kPartly][8] = reinterpret_cast<uint16_t (*)[L::kPartly][8]>(answer + 2);  // [kLists], see add_listed
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(lists + L::kLists);
   int* abort = reinterpret_cast<int*>(tmem_slot + 1);
-  int* sick = abort + 1;                           // [kSick] by item: its number + 1 where a value is bad
   int* err = a.status ? a.status : &g_no_status;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -391,7 +377,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&v_clean[s], 2);
     }
     *abort = 0;
-    for (int i = 0; i < L::kSick; ++i) sick[i] = 0;
     fence_mbar_init();
   }
   if (warp == 9) {
@@ -599,9 +584,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t r = 0;
       for (int64_t it = blockIdx.x; ok && it >= 0; it = next_item(r++)) {
         const Item x = item_at<kSplit>(a, sc, it);
-        const int n = x.n();
-        for (int j = 0; ok && j < n; ++j) {
-          if (!x.mixed(j)) continue;
+        const int n = x.n(), first = x.first_mixed();
+        for (int j = first; ok && j < n; ++j) {
           const uint32_t e = g + 2 * j + 1;
           const int s = e % kSlots;
           // (these warps have nothing to do until an item's last tiles: a long row's time)
@@ -609,7 +593,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) break;
           full ^= 1u << s;
           const int lo = max(0, x.see(0) - (x.j0 + j) * kTile), hi = min(kTile, x.lk - (x.j0 + j) * kTile);
-          uint32_t bad = 0;
+          uint32_t bad = 0;    // bit b: row t / 8 + 8 b
           // 16-byte unit u of the tile: row (u / 8) % 128; the swizzle stays within a row
           for (int u = t; u < L::kTileBytes / 16; u += 64) {
             const int row = (u >> 3) & (kTile - 1);
@@ -619,11 +603,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             } else if (row >= lo) {
               const uint4 w = *p;
               // the carry out of an exponent of ones: infinity or NaN
-              bad |= ((w.x & 0x7f807f80u) + 0x00800080u) | ((w.y & 0x7f807f80u) + 0x00800080u) |
-                     ((w.z & 0x7f807f80u) + 0x00800080u) | ((w.w & 0x7f807f80u) + 0x00800080u);
+              auto odd = [](uint32_t y) { return ((y & 0x7f807f80u) + 0x00800080u) & 0x80008000u; };
+              const uint4 o = make_uint4(odd(w.x), odd(w.y), odd(w.z), odd(w.w));
+              if (o.x | o.y | o.z | o.w) {
+                bad |= 1u << (row >> 3);
+                auto rest = [](uint32_t y, uint32_t z) { return y & ~((z >> 15) * 0xffffu); };
+                *p = make_uint4(rest(w.x, o.x), rest(w.y, o.y), rest(w.z, o.z), rest(w.w, o.w));
+              }
             }
           }
-          if (bad & 0x80008000u) reinterpret_cast<volatile int*>(sick)[item % L::kSick] = item + 1;
+          for (int i = 1; i < 8; i <<= 1) bad |= __shfl_xor_sync(0xffffffffu, bad, i);  // a row's units are eight lanes'
+          if ((t & 7) == 0) lists[item % L::kLists][j - first][t >> 3] = static_cast<uint16_t>(bad);
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(&v_clean[s]);
@@ -725,11 +715,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
       }
       const bool mine = used && tok < x.n_tok;
-      const bool again = reinterpret_cast<volatile int*>(sick)[item % L::kSick] == item + 1;
-      const bool redo = n > 0 && __any_sync(0xffffffffu, again);
+      // the tiles that this one's products have read, whose lists are written
+      const uint16_t (*list)[8] = lists[item % L::kLists];
+      const int first = x.first_mixed();
+      uint32_t listed = 0;
+      for (int q = 0; first + q < n; ++q) {
+        const uint4 w = *reinterpret_cast<const uint4*>(list[q]);
+        listed |= w.x | w.y | w.z | w.w;
+      }
       if (kSplit) {
         // this part's share of the rows, for the joining kernel
-        if (lane == 0) sc.sick[it * 8 + warp] = redo;
         const int64_t at = it * (2 * kTile) + i * kTile + row;
         if (mine) sc.ml[at] = make_float2(m, l);
 #pragma unroll
@@ -738,17 +733,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (n == 0) break;
           tmem_ld32(to + c * 32, v);
           tmem_ld_wait();
+          if (listed) add_listed(a, x, list, first, n, see, c * 32, v);
           if (mine && l != 0.f) {
 #pragma unroll
             for (int u = 0; u < 32; u += 4)
               *reinterpret_cast<float4*>(sc.o + at * D + c * 32 + u) = make_float4(v[u], v[u + 1], v[u + 2], v[u + 3]);
           }
-        }
-      } else if (redo) {
-        // each warp its own rows: the other tile's keys may be looked at meanwhile
-        for (int rr = (warp & 3) * 32; rr < min(sc.tpt * a.G, (warp & 3) * 32 + 32); ++rr) {
-          const int tt = i * sc.tpt + rr / a.G;
-          if (tt < x.n_tok) attend_row<D>(a, x.qtok + tt, x.head * a.G + rr % a.G, x.k0, x.see(tt));
         }
       } else {
         const float inv = l == 0.f ? 0.f : 1.f / l;
@@ -759,6 +749,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (n > 0) {
             tmem_ld32(to + c * 32, v);
             tmem_ld_wait();
+            if (listed) add_listed(a, x, list, first, n, see, c * 32, v);
           }
           if (mine) {
             // a row that sees nothing is zero even where its tile computed something
@@ -802,22 +793,14 @@ __global__ void __launch_bounds__(256) k_prompt_join(const PromptArgs a, const S
   const int64_t part0 = id * sc.n_split;
   float2 ml[kMaxSplit / 32];
   float m = -INFINITY, l = 0.f;
-  bool sick = false;
 #pragma unroll
   for (int u = 0; u < kMaxSplit / 32; ++u) {
     const int s = u * 32 + lane;
     ml[u] = make_float2(-INFINITY, 0.f);
-    if (s < sc.n_split) {
-      ml[u] = sc.ml[(part0 + s) * (2 * kTile) + r];
-      sick |= sc.sick[(part0 + s) * 8 + r / 32] != 0;
-    }
+    if (s < sc.n_split) ml[u] = sc.ml[(part0 + s) * (2 * kTile) + r];
     m = fmaxf(m, ml[u].x);
   }
   const int head = x.head * a.G + row % a.G;
-  if (__any_sync(0xffffffffu, sick)) {
-    attend_row<D>(a, x.qtok + tok, head, x.k0, x.see(tok));
-    return;
-  }
   for (int i = 16; i > 0; i >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, i));
   const float mz = m == -INFINITY ? 0.f : m;
   float o[D / 32];
@@ -874,7 +857,7 @@ int parts_of(int64_t n_slots, int64_t total_q, int64_t total_k, int64_t n_seqs, 
   return cost(best) < 0.9 * cost(1) ? static_cast<int>(best) : 1;
 }
 int64_t part_bytes(int64_t n_items, int n_split, int D) {
-  return n_split == 1 ? 0 : n_items * n_split * (8 * 4 + 2 * kTile * (8 + 4ll * D));
+  return n_split == 1 ? 0 : n_items * n_split * 2 * kTile * (8 + 4ll * D);
 }
 
 // Tensor map of [tokens, heads, D] bf16 with a box of 64 elements x
@@ -993,7 +976,6 @@ extern "C" int ai_attend_prompt(const void* q_dev, const int64_t* q_strides, con
   sc.n_items = slots * n_kv_heads;
   if (sc.n_items > 0x7fffffff) return fail(AI_ERR_ARG, "too many query blocks");
   sc.n_split = parts_of(slots, total_q, total_k, n_seqs, n_kv_heads);
-  sc.sick = nullptr;
   sc.ml = nullptr;
   sc.o = nullptr;
   if (sc.n_split > 1) {
@@ -1003,7 +985,6 @@ extern "C" int ai_attend_prompt(const void* q_dev, const int64_t* q_strides, con
     const int64_t parts = sc.n_items * sc.n_split;
     sc.o = static_cast<float*>(workspace_dev);
     sc.ml = reinterpret_cast<float2*>(sc.o + parts * 2 * kTile * head_dim);
-    sc.sick = reinterpret_cast<int*>(sc.ml + parts * 2 * kTile);
   }
   CUtensorMap mq, mk, mv;
   // without keys nothing is loaded, but a map needs a row

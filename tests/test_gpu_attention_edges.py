@@ -1,5 +1,7 @@
 """The attention and cache calls at their edges: what lists ask for, values that are not finite, shared pages, long rows,
 tensors that are dropped after the call."""
+import random
+
 import pytest
 import torch
 
@@ -10,8 +12,8 @@ pytestmark = pytest.mark.gpu
 if not torch.cuda.is_available():  # pragma: no cover
     pytest.skip("needs a GPU", allow_module_level=True)
 
-from ivf_top_key_b200 import AiError, PagedCache  # noqa: E402
-from tests.test_gpu_attention import _i32  # noqa: E402
+from ivf_top_key_b200 import AiError, C, PagedCache, attend_prompt  # noqa: E402
+from tests.test_gpu_attention import DEV, _i32, _prompt  # noqa: E402
 
 
 @pytest.mark.parametrize("asked", [0, 80, 96, 97, 112, 128, 129, 144, 256])
@@ -40,3 +42,73 @@ def test_extend_decode_steps_beside_one_request_beyond_the_cache():
         c.extend(_i32(list(seqs)), _i32(counts))
         ref.same_as(c)
     assert ref.lens[:5] == [0, 2, 2, 2, 2]
+
+
+def _spoiled(v, cu_q, cu_k, Hq, places):
+    """v with the values of `places` (sequence, key, key head, column, value), and what they make of the outputs
+    [total_q, Hq, D]: 0 where no row sees one, else the sum of those that it sees (of a place named twice the last)."""
+    v, G = v.clone(), Hq // v.shape[1]
+    add = torch.zeros(cu_q[-1], Hq, v.shape[2])
+    for (b, j, h, d), x in {tuple(p[:4]): p[4] for p in places}.items():
+        v[cu_k[b] + j, h, d] = x
+        lq, lk = cu_q[b + 1] - cu_q[b], cu_k[b + 1] - cu_k[b]
+        first = max(0, j - (lk - lq))   # query i sees the keys up to lk - lq + i
+        add[cu_q[b] + first:cu_q[b + 1], h * G:(h + 1) * G, d] += x
+    return v, add
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,ql,kl", [
+    (2, 2, 64, [300], [300]),
+    (1, 1, 128, [513], [700]),
+    (4, 2, 128, [40, 300, 50], [40, 300, 50]),
+    (8, 1, 64, [130, 3], [400, 140]),
+    (6, 2, 128, [150, 20], [90, 20]),        # the first rows see nothing
+    (128, 1, 128, [9], [140]),
+    (8, 2, 64, [40, 3], [3000, 5000]),       # keys divided among CTAs
+    (2, 1, 128, [5], [9000]),
+    (64, 1, 64, [70], [4000]),
+])
+def test_prompt_values_that_are_not_finite_reach_only_the_rows_that_see_them(Hq, Hkv, D, ql, kl):
+    """Bit for bit: every other output is what it is without them, and so it is in every run."""
+    q, k, v, cu_q, cu_k = _prompt(ql, kl, Hq, Hkv, D, seed=7 * sum(kl))
+    r = random.Random(sum(kl))
+    places = []
+    for b, (n_q, n_k) in enumerate(zip(ql, kl)):
+        near = [n_k - 1, max(0, n_k - n_q), max(0, n_k - n_q // 2), r.randrange(n_k), max(0, n_k - 1 - r.randrange(n_q))]
+        for j in near:
+            places.append((b, j, r.randrange(Hkv), r.randrange(D), r.choice([torch.nan, torch.inf, -torch.inf])))
+        j, h, d = near[2], r.randrange(Hkv), r.randrange(D)
+        places += [(b, j, h, d, torch.inf), (b, n_k - 1, h, d, -torch.inf)]
+    v2, add = _spoiled(v, cu_q, cu_k, Hq, places)
+    dq, dk, cq, ck = q.to(DEV), k.to(DEV), _i32(cu_q), _i32(cu_k)
+    lse, lse2 = (torch.empty(len(q), Hq, device=DEV) for _ in range(2))
+    status = _i32([0])
+    # the two runs differ in these values alone; a finite one has to be a finite one's bits
+    out = attend_prompt(dq, dk, v.to(DEV), cq, ck, out_lse=lse, status=status)
+    want = out.float() + add.to(DEV)
+    for _ in range(5):
+        got = attend_prompt(dq, dk, v2.to(DEV), cq, ck, out_lse=lse2, status=status).float()
+        assert torch.equal(lse, lse2)
+        seen = want.isnan() | want.isinf()
+        assert torch.equal(got.where(~seen, 0), want.where(~seen, 0))
+        assert torch.equal(got.isnan(), want.isnan()) and torch.equal(got.isinf(), want.isinf())
+        assert (got[want.isinf()] == want[want.isinf()]).all()
+    assert status.item() == 0
+
+
+def test_prompt_long_with_bad_values_beside_a_healthy_one():
+    """Blocks at the end of a long prompt whose last values are not finite, taken over by CTAs that have others to do."""
+    ql = [24000, 300]
+    Hq, Hkv, D = 16, 8, 128
+    assert C.ai_attend_prompt_workspace(2, sum(ql), sum(ql), Hq, Hkv, D) == 0   # undivided
+    q, k, v, cu, _ = _prompt(ql, ql, Hq, Hkv, D, seed=91)
+    v2, add = _spoiled(v, cu, cu, Hq, [(0, 23990, 3, 5, torch.nan), (0, 23901, 0, 127, torch.inf),
+                                       (0, 12001, 7, 64, torch.nan), (0, 0, 1, 1, -torch.inf)])
+    dq, dk, dcu = q.to(DEV), k.to(DEV), _i32(cu)
+    status = _i32([0])
+    want = attend_prompt(dq, dk, v.to(DEV), dcu, status=status).float() + add.to(DEV)
+    got = attend_prompt(dq, dk, v2.to(DEV), dcu, status=status).float()
+    assert status.item() == 0
+    good = want.isfinite()
+    assert torch.equal(got.isfinite(), good) and torch.equal(got[good], want[good])
+    assert good[24000:].all()
