@@ -347,7 +347,9 @@ int ai_refine_kernel_choice(ai_handle h, int32_t C, int32_t* kernel_out);
  *               the ai_cache_* calls use it; may be NULL for ai_attend_*)
  *   status      NULL, or an int32 that collects AI_DEVFLAG_* bits: RANGE for
  *               an id, sequence or page out of range (skipped, no access),
- *               CAPACITY where pages ran out (that sequence is unchanged)
+ *               CAPACITY where pages ran out (that sequence is unchanged),
+ *               TIMEOUT where a wait inside a kernel ran out (the call's
+ *               output is not valid)
  * n_pages at most 2^20; n_pages * page_size and max_pages * page_size below
  * 2^31.                                                                   */
 typedef struct ai_cache {
@@ -375,7 +377,8 @@ typedef struct ai_cache {
  * head_dim] bf16 and lse [total_q, n_heads] float32 (nullable) are dense;
  * rows that belong to no sequence stay as they were.  status_dev: NULL or an
  * int32 that collects AI_DEVFLAG_* bits (RANGE: cu_q / cu_k not as above,
- * nothing out of range is touched but the output is not valid).
+ * nothing out of range is touched but the output is not valid; TIMEOUT as
+ * for ai_cache).
  * Limit: n_heads / n_kv_heads at most 128.                                */
 int ai_attend_prompt(const void* q_dev, const int64_t* q_strides, const void* k_dev,
                      const int64_t* k_strides, const void* v_dev, const int64_t* v_strides,

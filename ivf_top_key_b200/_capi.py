@@ -22,6 +22,7 @@ ERRORS = {
     -5: "AI_ERR_TIMEOUT", -6: "AI_ERR_CUDA", -7: "AI_ERR_STATE",
 }
 AI_FP32, AI_BF16, AI_FP8E4M3 = 0, 1, 2
+AI_DEVFLAG_TIMEOUT, AI_DEVFLAG_RANGE, AI_DEVFLAG_CAPACITY = 1, 2, 4
 DTYPES = {"fp32": AI_FP32, "bf16": AI_BF16, "fp8": AI_FP8E4M3}
 
 EXPORTED = [

@@ -97,6 +97,16 @@ def _list(t, dev, what: str, n=None):
     return _dense(t, _INT, dev, what, None if n is None else (n,))
 
 
+def _refuse(bits: int):
+    """Raises for the AI_DEVFLAG_* bits of a status word; a wait that ran out says more than what was refused."""
+    if bits & C.AI_DEVFLAG_TIMEOUT:
+        raise C.AiError(-5, "a wait inside a kernel ran out: outputs since the last check are not valid")
+    if bits & C.AI_DEVFLAG_RANGE:
+        raise C.AiError(-4, "an id, sequence or page was out of range, or a sequence was listed twice")
+    if bits & C.AI_DEVFLAG_CAPACITY:
+        raise C.AiError(-2, "pages or table columns ran out")
+
+
 # ---------------------------------------------------------------- attention
 def attend_prompt(q, k, v, cu_q, cu_k=None, *, scale=None, out=None, out_lse=None, status=None, stream=None):
     """Causal attention over packed prompts (ai_attend_prompt).
@@ -309,7 +319,4 @@ class PagedCache:
         """Wait for the current stream and raise for what the calls refused since the last check."""
         bits = int(self.status.item())
         self.status.zero_()
-        if bits & 2:
-            raise C.AiError(-4, "an id, sequence or page was out of range, or a sequence was listed twice")
-        if bits:
-            raise C.AiError(-2, "pages or table columns ran out")
+        _refuse(bits)
