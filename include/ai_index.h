@@ -345,8 +345,9 @@ int ai_refine_kernel_choice(ai_handle h, int32_t C, int32_t* kernel_out);
  *   lens        [n_seqs] int32: tokens of each sequence
  *   refs        [n_pages] int32: sequences that hold the page, 0 = free (only
  *               the ai_cache_* calls use it; may be NULL for ai_attend_*)
- *   status      NULL, or an int32 that collects AI_DEVFLAG_* bits: RANGE for
- *               an id, sequence or page out of range (skipped, no access),
+ *   status      an int32 that collects AI_DEVFLAG_* bits, or NULL: the
+ *               device's own word, which ai_status_read reads.  RANGE for an
+ *               id, sequence or page out of range (skipped, no access),
  *               CAPACITY where pages ran out (that sequence is unchanged),
  *               TIMEOUT where a wait inside a kernel ran out (the call's
  *               output is not valid)
@@ -375,8 +376,8 @@ typedef struct ai_cache {
  * strides (in elements) of the first two are given as {token, head} pairs
  * and are positive multiples of 8, bases 16-byte aligned.  out [total_q, n_heads,
  * head_dim] bf16 and lse [total_q, n_heads] float32 (nullable) are dense;
- * rows that belong to no sequence stay as they were.  status_dev: NULL or an
- * int32 that collects AI_DEVFLAG_* bits (RANGE: cu_q / cu_k not as above,
+ * rows that belong to no sequence stay as they were.  status_dev: an int32
+ * that collects AI_DEVFLAG_* bits, or NULL as in ai_cache (RANGE: cu_q / cu_k not as above,
  * nothing out of range is touched but the output is not valid; TIMEOUT as
  * for ai_cache).
  * Limit: n_heads / n_kv_heads at most 128.                                */
@@ -456,6 +457,13 @@ int ai_cache_free(const ai_cache* cache, const int32_t* seqs_dev, int32_t n, voi
  * tables and refs follow.                                                 */
 int ai_cache_compact(const ai_cache* cache, void* workspace_dev, int64_t workspace_bytes,
                      void* cuda_stream);
+
+/* The AI_DEVFLAG_* bits that attention and cache calls without a status word
+ * have raised on the current device since the last read (of the calls whose
+ * work cuda_stream is behind: it waits for that stream), and clears them.
+ * Not to be called while a stream is captured.  AI_ERR_ARG for a null
+ * output, AI_ERR_CUDA on a CUDA error.                                    */
+int ai_status_read(int32_t* bits_out, void* cuda_stream);
 
 /* ------------------------------------------------- failure-path test hook */
 /* Runs the library's bounded wait against a barrier that nothing completes

@@ -14,12 +14,12 @@ import torch
 
 from . import _capi as C
 from ._capi import AiError  # noqa: F401
-from .attention import (PagedCache, attend_cached, attend_prompt, attend_selected, cache_compact, cache_extend,
-                        cache_fork, cache_free, cache_write)
+from .attention import (PagedCache, attend_cached, attend_check, attend_prompt, attend_selected, cache_compact,
+                        cache_extend, cache_fork, cache_free, cache_write)
 
 __all__ = ["AttentionIndex", "AiError", "quantize_fp8", "merge_topk", "C", "PagedCache", "attend_prompt",
-           "attend_cached", "attend_selected", "cache_extend", "cache_write", "cache_fork", "cache_free",
-           "cache_compact"]
+           "attend_cached", "attend_selected", "attend_check", "cache_extend", "cache_write", "cache_fork",
+           "cache_free", "cache_compact"]
 
 
 class AttentionIndex:

@@ -35,7 +35,7 @@ EXPORTED = [
     "ai_debug_refine_kernel", "ai_refine_kernel_choice", "ai_debug_refine_split",
     "ai_attend_prompt", "ai_attend_prompt_workspace", "ai_attend_workspace", "ai_attend_cached", "ai_attend_selected",
     "ai_cache_workspace", "ai_cache_extend", "ai_cache_write", "ai_cache_fork", "ai_cache_free",
-    "ai_cache_compact",
+    "ai_cache_compact", "ai_status_read",
 ]
 PHASES = ["route", "refine", "seal", "refit", "publish", "exh_scores", "exh_topk", "order"]
 
@@ -118,6 +118,7 @@ def _load():
         "ai_cache_fork": [vp, vp, vp, i32, vp, i64, vp],
         "ai_cache_free": [vp, vp, i32, vp],
         "ai_cache_compact": [vp, vp, i64, vp],
+        "ai_status_read": [ctypes.POINTER(i32), vp],
     }
     for name, args in sig.items():
         f = getattr(lib, name)
@@ -383,6 +384,12 @@ def ai_cache_free(cache: AiCache, seqs, n: int, stream: int):
 
 def ai_cache_compact(cache: AiCache, workspace, workspace_bytes: int, stream: int):
     _check(_lib.ai_cache_compact(ctypes.byref(cache), workspace, workspace_bytes, stream))
+
+
+def ai_status_read(stream: int) -> int:
+    v = ctypes.c_int32()
+    _check(_lib.ai_status_read(ctypes.byref(v), stream))
+    return v.value
 
 
 def ai_last_error() -> str:

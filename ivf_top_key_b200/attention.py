@@ -10,7 +10,9 @@ stream order; `PagedCache` holds such tensors for a program that has none.
 A call checks its tensors on the host, allocates its output and workspace
 with torch on the stream it runs on (so captured graphs and streams never
 share a workspace) and waits for nothing.  `stream` is a torch stream on the
-tensors' device; by default the current one of that device.
+tensors' device; by default the current one of that device.  What the device
+refuses, or an output that is not valid, shows in the call's `status` word, or
+without one in `attend_check()`.
 """
 from __future__ import annotations
 
@@ -105,6 +107,14 @@ def _refuse(bits: int):
         raise C.AiError(-4, "an id, sequence or page was out of range, or a sequence was listed twice")
     if bits & C.AI_DEVFLAG_CAPACITY:
         raise C.AiError(-2, "pages or table columns ran out")
+
+
+def attend_check(device=None):
+    """Wait for the device's current stream and raise for what calls without a status word refused since the last
+    check (ai_status_read)."""
+    device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+    with torch.cuda.device(device):
+        _refuse(C.ai_status_read(torch.cuda.current_stream().cuda_stream))
 
 
 # ---------------------------------------------------------------- attention

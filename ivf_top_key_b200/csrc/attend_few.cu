@@ -82,7 +82,7 @@ __global__ void __launch_bounds__(Few<D, FP8>::kThreads, 1) k_attend_few(const R
   uint64_t* st_free = st_full + 2;                                             // [2] states read
   uint32_t* reals = reinterpret_cast<uint32_t*>(st_free + 2);                  // [S] bit i: key i of the tile is there
   int* abort = reinterpret_cast<int*>(reals + S);
-  int* err = a.status ? a.status : &g_no_status;
+  int* err = a.status;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int cta = blockIdx.x;

@@ -87,7 +87,7 @@ __device__ __forceinline__ bool seq_rows(const PromptArgs& a, int b, int* q0, in
   *lq = q1 - *q0;
   *lk = k1 - *k0;
   const bool ok = *q0 >= 0 && q1 >= *q0 && q1 <= a.total_q && *k0 >= 0 && k1 >= *k0 && k1 <= a.total_k;
-  if (!ok && a.status) atomicOr(a.status, AI_DEVFLAG_RANGE);
+  if (!ok) atomicOr(a.status, AI_DEVFLAG_RANGE);
   return ok;
 }
 
@@ -329,8 +329,6 @@ __device__ __forceinline__ void add_listed(const PromptArgs& a, const Item& x, c
   }
 }
 
-__device__ int g_no_status;  // where flags go when the caller gives no status word
-
 template <int D, bool kSplit>
 __global__ void __launch_bounds__(kThreads, 1)
     k_prompt_tc(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
@@ -357,7 +355,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint16_t (*lists)[L::kPartly][8] = reinterpret_cast<uint16_t (*)[L::kPartly][8]>(answer + 2);  // [kLists], see add_listed
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(lists + L::kLists);
   int* abort = reinterpret_cast<int*>(tmem_slot + 1);
-  int* err = a.status ? a.status : &g_no_status;
+  int* err = a.status;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -966,7 +964,6 @@ extern "C" int ai_attend_prompt(const void* q_dev, const int64_t* q_strides, con
   a.c2 = scale == 0.f ? 1e-30f : scale * kLog2e;
   a.out = static_cast<uint16_t*>(out_dev);
   a.lse = lse_dev;
-  a.status = status_dev;
   Schedule sc;
   sc.tpt = kTile / a.G;
   sc.qb = 2 * sc.tpt;
@@ -986,6 +983,8 @@ extern "C" int ai_attend_prompt(const void* q_dev, const int64_t* q_strides, con
     sc.o = static_cast<float*>(workspace_dev);
     sc.ml = reinterpret_cast<float2*>(sc.o + parts * 2 * kTile * head_dim);
   }
+  a.status = status_dev ? status_dev : default_status();
+  if (!a.status) return fail(AI_ERR_CUDA, "the device's status word was not found");
   CUtensorMap mq, mk, mv;
   // without keys nothing is loaded, but a map needs a row
   const bool none = total_k == 0;

@@ -105,7 +105,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* q_empty = q_full + 2;                               // [2] queries read
   uint64_t* joined = q_empty + 2;                               // [2] states written / read
   int* abort = reinterpret_cast<int*>(joined + 2);
-  int* err = a.status ? a.status : &g_no_status;
+  int* err = a.status;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int n_heads = a.n_heads;
@@ -818,7 +818,8 @@ int run_rows(const ai_cache* c, int32_t layer, const void* q, int32_t R, int32_t
   a.c2 = scale * kLog2e;
   a.out = static_cast<uint16_t*>(out);
   a.lse = lse;
-  a.status = c->status;
+  a.status = c->status ? c->status : default_status();
+  if (!a.status) return fail(AI_ERR_CUDA, "the device's status word was not found");
   const int64_t most = ids ? n_ids : static_cast<int64_t>(c->max_pages) * c->page_size;
   const int64_t tiles = static_cast<int64_t>(R) * a.Hkv * n_mb * ((most + a.tile - 1) / a.tile);
   const int grid = static_cast<int>(tiles < 1 ? 1 : (tiles < max_grid() ? tiles : max_grid()));

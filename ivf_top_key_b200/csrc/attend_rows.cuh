@@ -35,7 +35,7 @@ struct RowsArgs {
   float* lse;               // [R, Hq] or nullptr
   float* part;              // partial results: [2 * grid][16 MT][D + 4]
   int32_t* meta;            // [grid][4]
-  int32_t* status;          // or nullptr
+  int32_t* status;
 };
 
 namespace {
@@ -93,8 +93,6 @@ __device__ __forceinline__ void cp4z(uint32_t dst, const void* src, bool real) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(real ? 4 : 0) : "memory");
 }
 
-__device__ int g_no_status;  // where flags go when the caller gives no status word
-
 // ----------------------------------------------------------- division of work
 // Division of a token (< 2^31) by the page size: with s = ceil(log2 d),
 // m = ceil(2^(31 + s) / d) < 2^32 the quotient is exactly n m >> (31 + s)
@@ -110,7 +108,7 @@ __device__ __forceinline__ int len_of(const RowsArgs& a, int row) {
   if (s < 0 || s >= a.n_seqs) return 0;
   const int64_t most = static_cast<int64_t>(a.width) * a.page_size;
   const int n = a.lens[s];
-  if ((n < 0 || n > most) && a.status) atomicOr(a.status, AI_DEVFLAG_RANGE);
+  if (n < 0 || n > most) atomicOr(a.status, AI_DEVFLAG_RANGE);
   return n < 0 ? 0 : (n > most ? static_cast<int>(most) : n);
 }
 __device__ __forceinline__ int tiles_of(const RowsArgs& a, int row) {

@@ -12,6 +12,8 @@
 // What bounds them: a call is one CTA that plans (reads the reference counts;
 // about 4 us) and a grid that moves pages at the copy rate of HBM: 256 pages of
 // 4 layers (474 MB read and written) 80 us, 5.9 TB/s.
+#include <mutex>
+
 #include "../../include/ai_index.h"
 #include "common.cuh"
 #include "kernels.h"
@@ -44,7 +46,7 @@ struct View {
 };
 
 __device__ __forceinline__ void flag(const View& c, int bit) {
-  if (c.status) atomicOr(c.status, bit);
+  atomicOr(c.status, bit);
 }
 __device__ __forceinline__ bool listed_before(const int32_t* list, int i) {
   for (int j = 0; j < i; ++j)
@@ -425,6 +427,15 @@ __global__ void __launch_bounds__(kMoveThreads) k_compact_move(View c, const int
   }
 }
 
+// Where flags go when the caller gives no status word, and what the last read
+// took from there.
+__device__ int32_t g_status[2];
+
+__global__ void k_take_status() {
+  dependency_wait();
+  g_status[1] = atomicExch(&g_status[0], 0);
+}
+
 View view_of(const ai_cache* c) {
   View v{};
   const int es = c->dtype == AI_BF16 ? 2 : 1;
@@ -443,10 +454,11 @@ View view_of(const ai_cache* c) {
   v.refs = c->refs;
   v.n_seqs = c->n_seqs;
   v.width = c->max_pages;
-  v.status = c->status;
+  v.status = c->status ? c->status : default_status();
   return v;
 }
 
+int no_status() { return fail(AI_ERR_CUDA, "the device's status word was not found"); }
 int done(cudaError_t e) { return e == cudaSuccess ? AI_OK : fail(AI_ERR_CUDA, cudaGetErrorString(e)); }
 
 int check_tables(const ai_cache* c) {
@@ -479,6 +491,20 @@ int device_sms() {
     known[dev].store(sms, std::memory_order_relaxed);
   }
   return sms;
+}
+
+int32_t* default_status() {
+  static std::atomic<int32_t*> known[kMaxDevices] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return nullptr;
+  int32_t* p = known[dev].load(std::memory_order_relaxed);
+  if (!p) {
+    void* at = nullptr;
+    if (cudaGetSymbolAddress(&at, g_status) != cudaSuccess) return nullptr;
+    p = static_cast<int32_t*>(at);
+    known[dev].store(p, std::memory_order_relaxed);
+  }
+  return p;
 }
 
 cudaError_t ReadyOnce::allow(const void* kernel, int bytes) {
@@ -532,8 +558,10 @@ extern "C" int ai_cache_extend(const ai_cache* c, const int32_t* seqs_dev, const
   if (!rc && n > 0 && !counts_dev) rc = fail(AI_ERR_ARG, "null counts");
   if (!rc) rc = check_ws(c, n, workspace_dev, workspace_bytes);
   if (rc || n == 0) return rc;
-  return done(launch_after(k_extend, dim3(1), dim3(kPlan), 0, static_cast<cudaStream_t>(cuda_stream), view_of(c), seqs_dev,
-                           counts_dev, n, static_cast<int32_t*>(workspace_dev)));
+  const View v = view_of(c);
+  if (!v.status) return no_status();
+  return done(launch_after(k_extend, dim3(1), dim3(kPlan), 0, static_cast<cudaStream_t>(cuda_stream), v, seqs_dev, counts_dev,
+                           n, static_cast<int32_t*>(workspace_dev)));
 }
 
 extern "C" int ai_cache_write(const ai_cache* c, int32_t layer, const void* k_dev, const void* v_dev,
@@ -555,11 +583,13 @@ extern "C" int ai_cache_write(const ai_cache* c, int32_t layer, const void* k_de
   const uint16_t* kn = static_cast<const uint16_t*>(k_dev);
   const uint16_t* vn = static_cast<const uint16_t*>(v_dev);
   const dim3 grid(static_cast<unsigned>(blocks));
+  const View v = view_of(c);
+  if (!v.status) return no_status();
   return done(c->dtype == AI_BF16
-                  ? launch_after(k_write<false>, grid, dim3(256), 0, st, view_of(c), slots, layer, kn, vn, seqs_dev, cu_dev,
-                                 n, n_tokens, c->n_kv_heads, c->head_dim)
-                  : launch_after(k_write<true>, grid, dim3(256), 0, st, view_of(c), slots, layer, kn, vn, seqs_dev, cu_dev,
-                                 n, n_tokens, c->n_kv_heads, c->head_dim));
+                  ? launch_after(k_write<false>, grid, dim3(256), 0, st, v, slots, layer, kn, vn, seqs_dev, cu_dev, n,
+                                 n_tokens, c->n_kv_heads, c->head_dim)
+                  : launch_after(k_write<true>, grid, dim3(256), 0, st, v, slots, layer, kn, vn, seqs_dev, cu_dev, n,
+                                 n_tokens, c->n_kv_heads, c->head_dim));
 }
 
 extern "C" int ai_cache_fork(const ai_cache* c, const int32_t* src_dev, const int32_t* dst_dev, int32_t n,
@@ -571,6 +601,7 @@ extern "C" int ai_cache_fork(const ai_cache* c, const int32_t* src_dev, const in
   if (!rc) rc = check_ws(c, n, workspace_dev, workspace_bytes);
   if (rc || n == 0) return rc;
   const View v = view_of(c);
+  if (!v.status) return no_status();
   cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
   int32_t* plan = static_cast<int32_t*>(workspace_dev);
   int32_t* length = plan + n;
@@ -588,8 +619,10 @@ extern "C" int ai_cache_free(const ai_cache* c, const int32_t* seqs_dev, int32_t
   int rc = check_tables(c);
   if (!rc) rc = check_list(c, seqs_dev, n);
   if (rc || n == 0) return rc;
-  return done(launch_after(k_free, dim3(n < 4096 ? n : 4096), dim3(256), 0, static_cast<cudaStream_t>(cuda_stream),
-                           view_of(c), seqs_dev, n));
+  const View v = view_of(c);
+  if (!v.status) return no_status();
+  return done(launch_after(k_free, dim3(n < 4096 ? n : 4096), dim3(256), 0, static_cast<cudaStream_t>(cuda_stream), v,
+                           seqs_dev, n));
 }
 
 extern "C" int ai_cache_compact(const ai_cache* c, void* workspace_dev, int64_t workspace_bytes, void* cuda_stream) {
@@ -599,6 +632,7 @@ extern "C" int ai_cache_compact(const ai_cache* c, void* workspace_dev, int64_t 
   if (!rc) rc = check_ws(c, 0, workspace_dev, workspace_bytes);
   if (rc) return rc;
   const View v = view_of(c);
+  if (!v.status) return no_status();
   cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
   int32_t* map = static_cast<int32_t*>(workspace_dev);
   int32_t* from = map + c->n_pages;
@@ -607,4 +641,18 @@ extern "C" int ai_cache_compact(const ai_cache* c, void* workspace_dev, int64_t 
   rc = done(launch_after(k_compact_plan, dim3(1), dim3(kPlan), 0, st, v, map, from, to, count));
   if (rc) return rc;
   return done(launch_after(k_compact_move, dim3(16 * device_sms()), dim3(kMoveThreads), 0, st, v, map, from, to, count));
+}
+
+extern "C" int ai_status_read(int32_t* bits_out, void* cuda_stream) {
+  using namespace aiidx;
+  if (!bits_out) return fail(AI_ERR_ARG, "null output");
+  static std::mutex one;   // g_status[1] is one reader's at a time
+  std::lock_guard<std::mutex> lock(one);
+  const int32_t* word = default_status();
+  if (!word) return no_status();
+  cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
+  cudaError_t e = launch_after(k_take_status, dim3(1), dim3(1), 0, st);
+  if (e == cudaSuccess) e = cudaMemcpyAsync(bits_out, word + 1, sizeof(int32_t), cudaMemcpyDeviceToHost, st);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+  return done(e);
 }

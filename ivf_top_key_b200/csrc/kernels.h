@@ -261,6 +261,9 @@ cudaError_t launch_after(void (*kernel)(P...), dim3 grid, dim3 block, size_t sme
 // ------------------------------------------------------------- per device
 constexpr int kMaxDevices = 128;
 int device_sms();   // of the current device (looked up once)
+// The current device's word for flags of calls that bring none (looked up
+// once), nullptr where it is not found.
+int32_t* default_status();
 // A kernel's shared-memory limit, raised once per device.
 struct ReadyOnce {
   std::atomic<bool> done[kMaxDevices] = {};

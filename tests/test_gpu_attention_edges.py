@@ -1,6 +1,9 @@
 """The attention and cache calls at their edges: what lists ask for, values that are not finite, shared pages, long rows,
 tensors that are dropped after the call."""
+import os
 import random
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -12,8 +15,9 @@ pytestmark = pytest.mark.gpu
 if not torch.cuda.is_available():  # pragma: no cover
     pytest.skip("needs a GPU", allow_module_level=True)
 
-from ivf_top_key_b200 import AiError, C, PagedCache, attend_prompt  # noqa: E402
-from tests.test_gpu_attention import DEV, _i32, _prompt  # noqa: E402
+from ivf_top_key_b200 import (AiError, C, PagedCache, attend_cached, attend_check, attend_prompt,  # noqa: E402
+                              attend_selected, cache_extend)
+from tests.test_gpu_attention import DEV, _cache, _i32, _prompt, _q  # noqa: E402
 
 
 @pytest.mark.parametrize("asked", [0, 80, 96, 97, 112, 128, 129, 144, 256])
@@ -112,3 +116,62 @@ def test_prompt_long_with_bad_values_beside_a_healthy_one():
     good = want.isfinite()
     assert torch.equal(got.isfinite(), good) and torch.equal(got[good], want[good])
     assert good[24000:].all()
+
+
+def test_calls_without_a_status_word_are_checked_by_device():
+    args, _, _ = _cache([40, 50], 16, 1, 64, "bf16", seed=5)
+    q = _q(2, 2, 64, 8).to(DEV)
+    x = _q(30, 2, 64, 9).to(DEV)
+    attend_check()
+    ok = [lambda: attend_cached(q, **args), lambda: attend_prompt(x, x, x, _i32([0, 10, 30]))]
+    bad = [lambda: attend_cached(q, seqs=_i32([7, -1]), **args), lambda: attend_selected(q, _i32([[1], [50]]), **args),
+           lambda: attend_prompt(x, x, x, _i32([0, 40, 30])), lambda: attend_prompt(x, x, x, _i32([0, 10, 31]))]
+    lens = args["lens"]
+    for wrong in (-1, 10 ** 9):
+        def call(n=wrong):
+            args["lens"] = _i32([n, 50])
+            attend_cached(q, **args)
+            args["lens"] = lens
+        bad.append(call)
+    for call in bad:
+        ok[0](), call(), ok[1]()
+        with pytest.raises(AiError, match="DEVICE_CHECK"):
+            attend_check(DEV)
+        attend_check()   # once
+    status = _i32([0])   # with a word of its own a call says it there
+    attend_cached(q, seqs=_i32([7, -1]), status=status, **args)
+    attend_check(torch.device("cuda", 0))
+    assert status.item() == 2
+    c = PagedCache(n_pages=2, page_size=4, n_kv_heads=1, head_dim=64, n_seqs=2, max_pages=3)
+    cache_extend(c.k, c.v, c.tables, c.lens, c.refs, _i32([0]), _i32([9]))
+    with pytest.raises(AiError, match="OOM"):
+        attend_check()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    seqs = _i32([7, -1])
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        attend_cached(q, seqs=seqs, **args)
+    attend_check()
+    g.replay()
+    with pytest.raises(AiError, match="DEVICE_CHECK"):
+        attend_check()
+
+
+def test_the_first_call_of_a_process_may_be_a_captured_one():
+    code = """
+import torch
+from ivf_top_key_b200 import PagedCache, attend_cached, attend_check, attend_prompt
+c = PagedCache(n_pages=2, page_size=4, n_kv_heads=1, head_dim=64, n_seqs=1, max_pages=2)
+q, cu = torch.ones(1, 2, 64, dtype=torch.bfloat16, device="cuda"), torch.tensor([0, 1], dtype=torch.int32, device="cuda")
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    a = attend_cached(q, c.k, c.v, c.tables, c.lens)
+    b = attend_prompt(q, q[:, :1], q[:, :1], cu)
+g.replay()
+attend_check()
+assert (a == 0).all() and (b == 1).all()
+"""
+    subprocess.run([sys.executable, "-c", code], check=True, timeout=200,
+                   cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
