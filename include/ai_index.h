@@ -344,7 +344,8 @@ int ai_refine_kernel_choice(ai_handle h, int32_t C, int32_t* kernel_out);
  *               tokens [p * page_size, (p + 1) * page_size)
  *   lens        [n_seqs] int32: tokens of each sequence
  *   refs        [n_pages] int32: sequences that hold the page, 0 = free (only
- *               the ai_cache_* calls use it; may be NULL for ai_attend_*)
+ *               the ai_cache_* calls use it; may be NULL for ai_attend_* and
+ *               ai_cache_write)
  *   status      an int32 that collects AI_DEVFLAG_* bits, or NULL: the
  *               device's own word, which ai_status_read reads.  RANGE for an
  *               id, sequence or page out of range (skipped, no access),
@@ -437,7 +438,10 @@ int ai_cache_extend(const ai_cache* cache, const int32_t* seqs_dev, const int32_
 /* Write the keys and values [n_tokens, n_kv_heads, head_dim] bf16 (dense) of
  * one layer: rows [cu[i], cu[i+1]) become the last cu[i+1] - cu[i] tokens of
  * sequence seqs[i] (fp8: quantised as by ai_quantize_fp8, per token and
- * head).  cu_dev int32 [n + 1], ascending; rows outside are not read.     */
+ * head).  cu_dev int32 [n + 1], ascending; rows outside are not read.  Where
+ * cache->refs is given, a sequence whose rows reach a page that another one
+ * holds too is refused (RANGE); without it such a write changes them all.
+ * Write a sequence's tokens in every layer before it is forked.           */
 int ai_cache_write(const ai_cache* cache, int32_t layer, const void* k_dev, const void* v_dev,
                    const int32_t* seqs_dev, const int32_t* cu_dev, int32_t n, int32_t n_tokens,
                    void* cuda_stream);

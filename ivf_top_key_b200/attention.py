@@ -104,7 +104,8 @@ def _refuse(bits: int):
     if bits & C.AI_DEVFLAG_TIMEOUT:
         raise C.AiError(-5, "a wait inside a kernel ran out: outputs since the last check are not valid")
     if bits & C.AI_DEVFLAG_RANGE:
-        raise C.AiError(-4, "an id, sequence or page was out of range, or a sequence was listed twice")
+        raise C.AiError(-4, "an id, sequence or page was out of range, a sequence was listed twice, or a write reached "
+                            "a page of several sequences")
     if bits & C.AI_DEVFLAG_CAPACITY:
         raise C.AiError(-2, "pages or table columns ran out")
 
@@ -229,10 +230,12 @@ def cache_extend(k, v, tables, lens, refs, seqs, counts, *, k_scale=None, v_scal
         C.ai_cache_extend(c, ps, pc, n, ws.data_ptr(), need, st)
 
 
-def cache_write(k, v, tables, lens, seqs, cu, new_k, new_v, *, layer: int = 0, k_scale=None, v_scale=None,
+def cache_write(k, v, tables, lens, seqs, cu, new_k, new_v, *, refs=None, layer: int = 0, k_scale=None, v_scale=None,
                 status=None, stream=None):
-    """Rows [cu[i], cu[i+1]) of new_k, new_v become the last tokens of sequence seqs[i] (ai_cache_write)."""
-    c, dev = _view(k, v, tables, lens, None, k_scale, v_scale, status)
+    """Rows [cu[i], cu[i+1]) of new_k, new_v become the last tokens of sequence seqs[i] (ai_cache_write).
+
+    refs: as for cache_extend; with it, rows that reach a page of several sequences are refused."""
+    c, dev = _view(k, v, tables, lens, refs, k_scale, v_scale, status)
     ps, n = _list(seqs, dev, "seqs"), seqs.shape[0]
     pc = _list(cu, dev, "cu", n + 1)
     shape = (new_k.shape[0], c.n_kv_heads, c.head_dim)
@@ -304,8 +307,8 @@ class PagedCache:
         cache_extend(self.k, self.v, self.tables, self.lens, self.refs, seqs, counts, stream=stream, **self._scales())
 
     def write(self, seqs, cu, new_k, new_v, layer: int = 0, stream=None):
-        cache_write(self.k, self.v, self.tables, self.lens, seqs, cu, new_k, new_v, layer=layer, stream=stream,
-                    **self._scales())
+        cache_write(self.k, self.v, self.tables, self.lens, seqs, cu, new_k, new_v, refs=self.refs, layer=layer,
+                    stream=stream, **self._scales())
 
     def fork(self, src, dst, stream=None):
         cache_fork(self.k, self.v, self.tables, self.lens, self.refs, src, dst, stream=stream, **self._scales())

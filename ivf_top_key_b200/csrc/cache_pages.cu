@@ -7,7 +7,8 @@
 // order of the call's list.
 //
 // Pages that hold more than one sequence's tokens are full (a fork copies the
-// part page), so a page is written only while one sequence owns it.
+// part page), and a write that would reach one is refused, so a page is written
+// only while one sequence owns it.
 //
 // What bounds them: a call is one CTA that plans (reads the reference counts;
 // about 4 us) and a grid that moves pages at the copy rate of HBM: 256 pages of
@@ -164,7 +165,10 @@ __global__ void __launch_bounds__(kPlan) k_extend(View c, const int32_t* seqs, c
 }
 
 // -------------------------------------------------------------------- write
-// One warp per (token, head) row of K and of V.
+// One warp per (token, head) row of K and of V.  Pages that several sequences
+// hold are the first ones of their rows (a fork shares all full pages), so a
+// segment whose first page is one sequence's reaches no shared one; the token's
+// own page is looked at too, for tables that were made otherwise.
 template <bool FP8>
 __global__ void k_write(View c, int64_t layer_slots, int layer, const uint16_t* kn, const uint16_t* vn,
                         const int32_t* seqs, const int32_t* cu, int n, int n_tokens, int Hkv, int D) {
@@ -189,33 +193,51 @@ __global__ void k_write(View c, int64_t layer_slots, int layer, const uint16_t* 
   }
   const int len = c.lens[s];
   const int64_t pos = static_cast<int64_t>(len) - (cu[lo + 1] - tok);
+  const int64_t first = static_cast<int64_t>(len) - (cu[lo + 1] - cu[lo]);
+  // lane 0 looks up the token's page, lane 1 the segment's first one
+  const int64_t at = lane == 1 ? max(first, static_cast<int64_t>(0)) : pos;
   int page = -1;
-  if (pos >= 0 && pos < static_cast<int64_t>(c.width) * c.page_size)
-    page = c.tables[static_cast<int64_t>(s) * c.width + pos / c.page_size];
-  if (page < 0 || page >= c.n_pages) {
+  bool shared = false;
+  if (lane < 2 && at >= 0 && at < static_cast<int64_t>(c.width) * c.page_size) {
+    page = c.tables[static_cast<int64_t>(s) * c.width + static_cast<uint32_t>(at) / static_cast<uint32_t>(c.page_size)];
+    if (page < 0 || page >= c.n_pages) page = -1;
+    else if (c.refs) shared = c.refs[page] > 1;
+  }
+  page = __shfl_sync(0xffffffffu, page, 0);
+  if (__any_sync(0xffffffffu, shared) || page < 0) {
     if (lane == 0) flag(c, AI_DEVFLAG_RANGE);
     return;
   }
-  const int64_t row = (layer * layer_slots + static_cast<int64_t>(page) * c.page_size + pos % c.page_size) * Hkv + h;
+  // a lane's first words of both rows at once
   const int64_t src = (static_cast<int64_t>(tok) * Hkv + h) * D;
+  uint32_t head[2][2];
+#pragma unroll
+  for (int which = 0; which < 2; ++which)
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+      head[which][u] = lane + 32 * u < D / 2 ? reinterpret_cast<const uint32_t*>((which ? vn : kn) + src)[lane + 32 * u] : 0;
+  const int slot = static_cast<int>(static_cast<uint32_t>(pos) % static_cast<uint32_t>(c.page_size));
+  const int64_t row = (layer * layer_slots + static_cast<int64_t>(page) * c.page_size + slot) * Hkv + h;
+#pragma unroll
   for (int which = 0; which < 2; ++which) {
     const uint32_t* x = reinterpret_cast<const uint32_t*>((which ? vn : kn) + src);
+    auto word = [&](int i) { return i < 32 ? head[which][0] : (i < 64 ? head[which][1] : x[i]); };
     uint8_t* dst = which ? c.v : c.k;
     if constexpr (!FP8) {
       uint32_t* y = reinterpret_cast<uint32_t*>(dst + row * D * 2);
-      for (int i = lane; i < D / 2; i += 32) y[i] = x[i];
+      for (int i = lane; i < D / 2; i += 32) y[i] = word(i);
     } else {
       // scale amax / 448 and e4m3 codes of the row, as for fp8 key stores
       float amax = 0.f;
       for (int i = lane; i < D / 2; i += 32) {
-        const uint32_t u = x[i];
+        const uint32_t u = word(i);
         amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(u << 16)), fabsf(__uint_as_float(u & 0xffff0000u))));
       }
       for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
       const float scale = amax > 0.f ? __fdiv_rn(amax, 448.f) : 1.f;
       uint16_t* y = reinterpret_cast<uint16_t*>(dst + row * D);
       for (int i = lane; i < D / 2; i += 32) {
-        const uint32_t u = x[i];
+        const uint32_t u = word(i);
         const uint16_t a = __nv_cvt_float_to_fp8(__fdiv_rn(__uint_as_float(u << 16), scale), __NV_SATFINITE, __NV_E4M3);
         const uint16_t b =
             __nv_cvt_float_to_fp8(__fdiv_rn(__uint_as_float(u & 0xffff0000u), scale), __NV_SATFINITE, __NV_E4M3);

@@ -17,7 +17,7 @@ if not torch.cuda.is_available():  # pragma: no cover
 
 from ivf_top_key_b200 import (AiError, C, PagedCache, attend_cached, attend_check, attend_prompt,  # noqa: E402
                               attend_selected, cache_extend)
-from tests.test_gpu_attention import DEV, _cache, _i32, _prompt, _q  # noqa: E402
+from tests.test_gpu_attention import DEV, _cache, _gen, _i32, _prompt, _q  # noqa: E402
 
 
 @pytest.mark.parametrize("asked", [0, 80, 96, 97, 112, 128, 129, 144, 256])
@@ -175,3 +175,31 @@ assert (a == 0).all() and (b == 1).all()
 """
     subprocess.run([sys.executable, "-c", code], check=True, timeout=200,
                    cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp8"])
+def test_write_leaves_pages_alone_that_another_sequence_holds(dtype):
+    c = PagedCache(n_pages=8, page_size=4, n_kv_heads=2, head_dim=64, n_seqs=3, max_pages=4, dtype=dtype)
+    x = torch.randn(16, 2, 64, generator=_gen(1)).bfloat16().to(DEV)
+    c.extend(_i32([0]), _i32([8]))
+    c.write(_i32([0]), _i32([0, 8]), x[:8], x[:8])
+    c.fork(_i32([0]), _i32([1]))          # two full pages, held by both
+    c.extend(_i32([1, 0]), _i32([2, 6]))
+    c.check()
+    before = [t.clone() for t in (c.k, c.v)]
+    # sequence 1's last five tokens: three of them lie in a page that sequence 0 holds too; sequence 0's own are written
+    c.write(_i32([1, 0]), _i32([0, 5, 11]), x[:11], x[:11])
+    with pytest.raises(AiError, match="DEVICE_CHECK"):
+        c.check()
+    own = c.tables[0, 2:4].tolist()
+    for t, b in zip((c.k, c.v), before):
+        rest = [p for p in range(8) if p not in own]
+        assert torch.equal(t[:, rest], b[:, rest]) and not torch.equal(t[:, own], b[:, own])
+    c.write(_i32([1]), _i32([0, 2]), x[:2], x[:2])   # what it owns alone
+    c.check()
+    c.free(_i32([0]))
+    c.write(_i32([1]), _i32([0, 10]), x[:10], x[:10])   # now it owns all of it
+    c.check()
+    if dtype == "bf16":
+        pages = c.tables[1, :3].tolist()
+        assert torch.equal(c.k[0, pages].reshape(12, 2, 64)[:10], x[:10])
