@@ -423,7 +423,8 @@ int ai_attend_selected(const ai_cache* cache, int32_t layer, const void* q_dev,
  * these calls may be captured too.  New pages are the lowest free ones, in
  * the order of the list.  A sequence with lens = 0 is empty.  What a call
  * refuses (bad index, a sequence listed twice, pages exhausted) is flagged in
- * cache->status and left unchanged; the rest of the list is done.         */
+ * cache->status and left unchanged; the rest of the list is done.  (Released
+ * twice is not refused: the second time the sequence is empty.)           */
 
 /* Bytes of workspace for a call with an n-entry list (ai_cache_compact: 0). */
 int ai_cache_workspace(const ai_cache* cache, int32_t n, int64_t* bytes_out);
@@ -438,9 +439,11 @@ int ai_cache_extend(const ai_cache* cache, const int32_t* seqs_dev, const int32_
 /* Write the keys and values [n_tokens, n_kv_heads, head_dim] bf16 (dense) of
  * one layer: rows [cu[i], cu[i+1]) become the last cu[i+1] - cu[i] tokens of
  * sequence seqs[i] (fp8: quantised as by ai_quantize_fp8, per token and
- * head).  cu_dev int32 [n + 1], ascending; rows outside are not read.  Where
- * cache->refs is given, a sequence whose rows reach a page that another one
- * holds too is refused (RANGE); without it such a write changes them all.
+ * head).  cu_dev int32 [n + 1], ascending; rows outside are not read.  Rows
+ * before a sequence's first token (cu asks for more than it has) are left out
+ * and flagged (RANGE).  Where cache->refs is given, a sequence whose rows
+ * reach a page that another one holds too is refused as a whole (RANGE);
+ * without it such a write changes them all.
  * Write a sequence's tokens in every layer before it is forked.           */
 int ai_cache_write(const ai_cache* cache, int32_t layer, const void* k_dev, const void* v_dev,
                    const int32_t* seqs_dev, const int32_t* cu_dev, int32_t n, int32_t n_tokens,

@@ -16,7 +16,7 @@ if not torch.cuda.is_available():  # pragma: no cover
     pytest.skip("needs a GPU", allow_module_level=True)
 
 from ivf_top_key_b200 import (AiError, C, PagedCache, attend_cached, attend_check, attend_prompt,  # noqa: E402
-                              attend_selected, cache_extend)
+                              attend_selected, cache_extend, cache_write)
 from tests.test_gpu_attention import DEV, _cache, _gen, _i32, _prompt, _q  # noqa: E402
 
 
@@ -203,3 +203,14 @@ def test_write_leaves_pages_alone_that_another_sequence_holds(dtype):
     if dtype == "bf16":
         pages = c.tables[1, :3].tolist()
         assert torch.equal(c.k[0, pages].reshape(12, 2, 64)[:10], x[:10])
+
+
+@pytest.mark.parametrize("refs", [False, True])
+def test_write_of_more_tokens_than_a_sequence_has_writes_the_last_ones(refs):
+    c = PagedCache(n_pages=4, page_size=4, n_kv_heads=1, head_dim=64, n_seqs=2, max_pages=2)
+    c.extend(_i32([0, 1]), _i32([3, 2]))
+    x = torch.randn(9, 1, 64, generator=_gen(2)).bfloat16().to(DEV)
+    status = _i32([0])
+    cache_write(c.k, c.v, c.tables, c.lens, _i32([0, 1]), _i32([0, 7, 9]), x, x, refs=c.refs if refs else None, status=status)
+    assert status.item() == 2
+    assert torch.equal(c.k[0, 0, :3], x[4:7]) and torch.equal(c.k[0, 1, :2], x[7:]) and (c.k[0, :2, 3] == 0).all()
