@@ -559,7 +559,8 @@ __global__ void __launch_bounds__(Few<D, FP8>::kThreads, 1) k_attend_few(const R
             uint16_t* to = a.out + (out_row + h) * D;
 #pragma unroll
             for (int dd = 0; dd < D / 16; ++dd) {
-              const uint32_t y = begun ? pack_bf16(o[dd][i] * inv, o[dd][2 + i] * inv) : 0;
+              // (a head whose scores are all -inf is zero whatever the values hold)
+              const uint32_t y = begun && l_run[i] != 0.f ? pack_bf16(o[dd][i] * inv, o[dd][2 + i] * inv) : 0;
               if constexpr (!FP8) {
                 to[dd * 16 + g] = static_cast<uint16_t>(y & 0xffff);
                 to[dd * 16 + 8 + g] = static_cast<uint16_t>(y >> 16);

@@ -612,6 +612,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             y.z = fmaf(z.z, wgt[i], y.z);
             y.w = fmaf(z.w, wgt[i], y.w);
           }
+          // a head that saw nothing, or whose scores are all -inf, is zero whatever the values hold
+          if (x.slot < 0 && l == 0.f) y = make_float4(0.f, 0.f, 0.f, 0.f);
           if (used) {
             if (x.slot < 0)
               *reinterpret_cast<uint2*>(a.out + (static_cast<int64_t>(x.row) * a.Hq + h0 + r) * D + c0 + c) =

@@ -214,3 +214,33 @@ def test_write_of_more_tokens_than_a_sequence_has_writes_the_last_ones(refs):
     cache_write(c.k, c.v, c.tables, c.lens, _i32([0, 1]), _i32([0, 7, 9]), x, x, refs=c.refs if refs else None, status=status)
     assert status.item() == 2
     assert torch.equal(c.k[0, 0, :3], x[4:7]) and torch.equal(c.k[0, 1, :2], x[7:]) and (c.k[0, :2, 3] == 0).all()
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+@pytest.mark.parametrize("Hq,Hkv,n", [(1, 1, 5), (8, 1, 31), (8, 2, 300), (24, 1, 20), (40, 1, 200), (4, 1, 30000),
+                                      (16, 1, 30000)])
+def test_rows_whose_scores_are_all_minus_infinity_are_zero(Hq, Hkv, n, kv):
+    """Whatever the values hold; the heads beside them are as they would be."""
+    D = 64
+    args, _, _ = _cache([n], 64, Hkv, D, kv, seed=n, layers=1, layer=0)
+    page = args["tables"][0].long()
+    k, v = args["k"], args["v"]
+    if kv == "bf16":
+        k[0, :, :, :, 0] = 1
+        v[0, :, :, :, 1] = torch.nan
+        v[0, :, :, :, 2] = torch.inf
+    else:
+        k[0, :, :, :, 0] = 0x38            # 1.0
+        v[0, :, :, :, 1] = 0x7F            # NaN
+    q = torch.zeros(1, Hq, D, dtype=torch.bfloat16, device=DEV)
+    q[0, 0, 0] = -torch.inf
+    lse = torch.empty(1, Hq, device=DEV)
+    ids = _i32([list(range(n))])
+    for out in (attend_cached(q, out_lse=lse, **args), attend_selected(q, ids, out_lse=lse, **args)):
+        assert (out[0, 0] == 0).all() and lse[0, 0] == -torch.inf
+        assert out[0, 1:, 1].isnan().all() and lse[0, 1:].isfinite().all()
+    if kv == "bf16":
+        at = (page[:, None] * 64 + torch.arange(64, device=DEV)).flatten()[:n]
+        kk, vv = (t[0].flatten(0, 1)[at].contiguous() for t in (k, v))
+        out = attend_prompt(q, kk, vv, _i32([0, 1]), _i32([0, n]), out_lse=lse)
+        assert (out[0, 0] == 0).all() and lse[0, 0] == -torch.inf and out[0, 1:, 1].isnan().all()
