@@ -381,7 +381,8 @@ typedef struct ai_cache {
  * that collects AI_DEVFLAG_* bits, or NULL as in ai_cache (RANGE: cu_q / cu_k not as above,
  * nothing out of range is touched but the output is not valid; TIMEOUT as
  * for ai_cache).
- * Limit: n_heads / n_kv_heads at most 128.                                */
+ * Limits: n_heads / n_kv_heads at most 128; total_q and total_k at most
+ * 2^31 - 257.                                                             */
 int ai_attend_prompt(const void* q_dev, const int64_t* q_strides, const void* k_dev,
                      const int64_t* k_strides, const void* v_dev, const int64_t* v_strides,
                      const int32_t* cu_q_dev, const int32_t* cu_k_dev, int32_t n_seqs,

@@ -137,6 +137,7 @@ struct Schedule {
   float* o;                   //              [n_items][n_split][256][D] output before the division
 };
 constexpr int kMaxSplit = 128;
+constexpr int kMaxTokens = 0x7fffffff - 2 * kTile;
 
 // Slot s belongs to the last sequence b with cu_q[b] / qb + b <= s: each
 // sequence has at least as many slots as blocks.
@@ -352,7 +353,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* next_full = o_full + 2;                // [2] next item known
   uint64_t* next_read = next_full + 2;             // [2] and read by every warp
   uint4* answer = reinterpret_cast<uint4*>((reinterpret_cast<uintptr_t>(next_read + 2) + 15) & ~uintptr_t(15));  // [2]
-  uint16_t (*lists)[L::kPartly][8] = reinterpret_cast<uint16_t (*)[L::kPartly][8]>(answer + 2);  // [kLists], see add_listed
+  // [kLists][kPartly][8], see add_listed
+  uint16_t (*lists)[L::kPartly][8] = reinterpret_cast<uint16_t (*)[L::kPartly][8]>(answer + 2);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(lists + L::kLists);
   int* abort = reinterpret_cast<int*>(tmem_slot + 1);
   int* err = a.status;
@@ -610,7 +612,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
           }
-          for (int i = 1; i < 8; i <<= 1) bad |= __shfl_xor_sync(0xffffffffu, bad, i);  // a row's units are eight lanes'
+          // a row's units are eight lanes'
+          for (int i = 1; i < 8; i <<= 1) bad |= __shfl_xor_sync(0xffffffffu, bad, i);
           if ((t & 7) == 0) lists[item % L::kLists][j - first][t >> 3] = static_cast<uint16_t>(bad);
           fence_proxy_async_smem();
           __syncwarp();
@@ -923,6 +926,8 @@ extern "C" int ai_attend_prompt(const void* q_dev, const int64_t* q_strides, con
   using namespace aiidx;
   if (!q_strides || !k_strides || !v_strides || !cu_q_dev || !cu_k_dev) return fail(AI_ERR_ARG, "null pointer argument");
   if (n_seqs < 0 || total_q < 0 || total_k < 0) return fail(AI_ERR_ARG, "negative sequence or token count");
+  // the end of the last tile behind the last token stays below 2^31
+  if (total_q > kMaxTokens || total_k > kMaxTokens) return fail(AI_ERR_ARG, "more than 2^31 - 257 tokens");
   if ((total_q > 0 && (!q_dev || !out_dev)) || (total_k > 0 && (!k_dev || !v_dev)))
     return fail(AI_ERR_ARG, "null pointer argument");
   if (head_dim != 64 && head_dim != 128) return fail(AI_ERR_ARG, "head_dim must be 64 or 128");

@@ -816,7 +816,7 @@ int run_rows(const ai_cache* c, int32_t layer, const void* q, int32_t R, int32_t
   // measured: about 1.5 us an item; 0.2 us a tile of 32 keys, 0.4 to 0.7 us a
   // larger one
   a.over = a.mb_rows <= kFewHeads ? 7 : 3;
-  a.nt_ids = (n_ids + a.tile - 1) / a.tile;
+  a.nt_ids = static_cast<int>((static_cast<int64_t>(n_ids) + a.tile - 1) / a.tile);
   a.c2 = scale * kLog2e;
   a.out = static_cast<uint16_t*>(out);
   a.lse = lse;

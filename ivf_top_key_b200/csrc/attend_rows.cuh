@@ -112,7 +112,7 @@ __device__ __forceinline__ int len_of(const RowsArgs& a, int row) {
   return n < 0 ? 0 : (n > most ? static_cast<int>(most) : n);
 }
 __device__ __forceinline__ int tiles_of(const RowsArgs& a, int row) {
-  return (len_of(a, row) + a.tile - 1) / a.tile;
+  return static_cast<int>((static_cast<uint32_t>(len_of(a, row)) + a.tile - 1) / a.tile);  // (past 2^31)
 }
 
 // A share of one item: tiles [t0, t1) of a row and a (key head, row block).

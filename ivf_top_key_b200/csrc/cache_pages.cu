@@ -149,8 +149,9 @@ __global__ void __launch_bounds__(kPlan) k_extend(View c, const int32_t* seqs, c
   for (int i = threadIdx.x; i < n; i += kPlan) {
     if (rank[i] == -1) continue;
     const int s = seqs[i];
-    const int len = c.lens[s], end = len + counts[i];
-    const int p0 = (len + c.page_size - 1) / c.page_size, p1 = (end + c.page_size - 1) / c.page_size;
+    const int64_t len = c.lens[s], end = len + counts[i];   // (below 2^31, rounded up maybe not)
+    const int p0 = static_cast<int>((len + c.page_size - 1) / c.page_size);
+    const int p1 = static_cast<int>((end + c.page_size - 1) / c.page_size);
     if (rank[i] < 0 || (p1 > p0 && rank[i] + (p1 - p0) > have)) {
       flag(c, AI_DEVFLAG_CAPACITY);
       continue;
@@ -160,7 +161,7 @@ __global__ void __launch_bounds__(kPlan) k_extend(View c, const int32_t* seqs, c
       c.tables[static_cast<int64_t>(s) * c.width + p] = page;
       c.refs[page] = 1;
     }
-    c.lens[s] = end;
+    c.lens[s] = static_cast<int>(end);
   }
 }
 
@@ -322,7 +323,7 @@ __device__ __forceinline__ void copy_chunk(const View& c, int layer, int from, i
   }
   if (chunk == 0 && c.scale_floats) {
     const int64_t ps = static_cast<int64_t>(c.page_size) * c.scale_floats;
-    for (int i = threadIdx.x; i < slots * c.scale_floats; i += kMoveThreads) {
+    for (int64_t i = threadIdx.x; i < static_cast<int64_t>(slots) * c.scale_floats; i += kMoveThreads) {
       c.ks[(l + to) * ps + i] = c.ks[(l + from) * ps + i];
       c.vs[(l + to) * ps + i] = c.vs[(l + from) * ps + i];
     }

@@ -1,5 +1,6 @@
 """The attention and cache calls at their edges: what lists ask for, values that are not finite, shared pages, long rows,
 tensors that are dropped after the call."""
+import math
 import os
 import random
 import subprocess
@@ -211,7 +212,8 @@ def test_write_of_more_tokens_than_a_sequence_has_writes_the_last_ones(refs):
     c.extend(_i32([0, 1]), _i32([3, 2]))
     x = torch.randn(9, 1, 64, generator=_gen(2)).bfloat16().to(DEV)
     status = _i32([0])
-    cache_write(c.k, c.v, c.tables, c.lens, _i32([0, 1]), _i32([0, 7, 9]), x, x, refs=c.refs if refs else None, status=status)
+    cache_write(c.k, c.v, c.tables, c.lens, _i32([0, 1]), _i32([0, 7, 9]), x, x, refs=c.refs if refs else None,
+                status=status)
     assert status.item() == 2
     assert torch.equal(c.k[0, 0, :3], x[4:7]) and torch.equal(c.k[0, 1, :2], x[7:]) and (c.k[0, :2, 3] == 0).all()
 
@@ -244,3 +246,37 @@ def test_rows_whose_scores_are_all_minus_infinity_are_zero(Hq, Hkv, n, kv):
         kk, vv = (t[0].flatten(0, 1)[at].contiguous() for t in (k, v))
         out = attend_prompt(q, kk, vv, _i32([0, 1]), _i32([0, n]), out_lse=lse)
         assert (out[0, 0] == 0).all() and lse[0, 0] == -torch.inf and out[0, 1:, 1].isnan().all()
+
+
+@pytest.mark.parametrize("Hq", [2, 16])
+def test_a_row_of_almost_2_31_keys(Hq):
+    """49981 times the same page of 42966 tokens, 2^31 - 2 in all: the last tile's end is past 2^31.  All weights are 1
+    and the values small whole numbers, so sums are exact where a warp adds up (2^31 / (148 * 8) keys, below 2^24)."""
+    page, width = 42966, 49981
+    n = page * width
+    assert n == 2 ** 31 - 2
+    k = torch.ones(1, page, 1, 64, dtype=torch.bfloat16, device=DEV)
+    v = (torch.arange(64, device=DEV) % 5 - 2).to(torch.bfloat16).expand(1, page, 1, 64).contiguous()
+    tables = torch.zeros(1, width, dtype=torch.int32, device=DEV)
+    q = torch.zeros(1, Hq, 64, dtype=torch.bfloat16, device=DEV)
+    lse, status = torch.empty(1, Hq, device=DEV), _i32([0])
+    out = attend_cached(q, k, v, tables, _i32([n]), out_lse=lse, status=status)
+    assert status.item() == 0
+    assert torch.equal(out, v[:, 0].expand_as(out))
+    # the joined parts' sum: at most 300 roundings; then a step of the logarithm, and the product's
+    assert (lse.double() - math.log(n)).abs().max() < 300 * 2.0 ** -24 + 4 * 22 * 2.0 ** -24
+
+
+def test_extend_to_almost_2_31_tokens():
+    page, width = 42966, 49981
+    tables = torch.full((2, width), -1, dtype=torch.int32, device=DEV)
+    lens, refs, status = _i32([0, 0]), torch.zeros(width, dtype=torch.int32, device=DEV), _i32([0])
+    c = C.AiCache(tables=tables.data_ptr(), lens=lens.data_ptr(), refs=refs.data_ptr(), status=status.data_ptr(),
+                  n_pages=width, page_size=page, n_seqs=2, max_pages=width)
+    n = C.ai_cache_workspace(c, 1)
+    ws, seqs = torch.empty(n, dtype=torch.uint8, device=DEV), _i32([1])
+    for more in (2 ** 31 - 2 - page - 5, page, 5):
+        C.ai_cache_extend(c, seqs.data_ptr(), _i32([more]).data_ptr(), 1, ws.data_ptr(), n, 0)
+    torch.cuda.synchronize()
+    assert status.item() == 0 and lens.tolist() == [0, 2 ** 31 - 2] and (refs == 1).all()
+    assert torch.equal(tables[1], torch.arange(width, dtype=torch.int32, device=DEV)) and (tables[0] == -1).all()
