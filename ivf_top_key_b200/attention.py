@@ -10,9 +10,11 @@ stream order; `PagedCache` holds such tensors for a program that has none.
 A call checks its tensors on the host, allocates its output and workspace
 with torch on the stream it runs on (so captured graphs and streams never
 share a workspace) and waits for nothing.  `stream` is a torch stream on the
-tensors' device; by default the current one of that device.  What the device
-refuses, or an output that is not valid, shows in the call's `status` word, or
-without one in `attend_check()`.
+tensors' device; by default the current one of that device.  The caller orders
+it behind what writes the tensors and before what reads the output; all of
+them may be dropped right after.  What the device refuses, or an output that
+is not valid, shows in the call's `status` word, or without one in
+`attend_check()`.
 """
 from __future__ import annotations
 
@@ -55,6 +57,18 @@ def _on(device: torch.device, stream):
         return handle, None if device.index == torch._C._cuda_getDevice() else torch.cuda.device(device)
     _need(stream.device == device, "the stream must be on the tensors' device")
     return stream.cuda_stream, _entered(device, stream)
+
+
+def _kept(stream, out, *tensors):
+    """After a call on a stream of the caller's: its tensors may be dropped now, their memory is not given to others
+    before the stream has come this far.  The output, which may be new memory of that stream, is used on the current
+    one."""
+    if stream is not None:
+        for t in (out, *tensors):
+            if t is not None:
+                t.record_stream(stream)
+        if out is not None:
+            out.record_stream(torch.cuda.current_stream(stream.device))
 
 
 @functools.lru_cache(maxsize=None)
@@ -153,6 +167,7 @@ def attend_prompt(q, k, v, cu_q, cu_k=None, *, scale=None, out=None, out_lse=Non
         C.ai_attend_prompt(q.data_ptr(), q.stride()[:2], k.data_ptr(), k.stride()[:2], v.data_ptr(), v.stride()[:2],
                            pq, pk, B, T, Tk, Hq, Hkv, D, D ** -0.5 if scale is None else scale, po, pl,
                            ps, ws.data_ptr() if n else None, n, st)
+    _kept(stream, out, q, k, v, cu_q, cu_k, out_lse, status)
     return out
 
 
@@ -199,7 +214,9 @@ def attend_cached(q, k, v, tables, lens, seqs=None, *, layer: int = 0, k_scale=N
     shape without D); tables [n_seqs, max_pages], lens [n_seqs] int32.  Row r
     reads sequence seqs[r] (None: r).  Returns out [rows, Hq, D]."""
     c, dev = _view(k, v, tables, lens, None, k_scale, v_scale, status)
-    return _rows(q, None, c, dev, seqs, layer, scale, out, out_lse, stream)
+    out = _rows(q, None, c, dev, seqs, layer, scale, out, out_lse, stream)
+    _kept(stream, out, q, k, v, tables, lens, seqs, k_scale, v_scale, out_lse, status)
+    return out
 
 
 def attend_selected(q, ids, k, v, tables, lens, seqs=None, *, layer: int = 0, k_scale=None, v_scale=None, scale=None,
@@ -210,7 +227,9 @@ def attend_selected(q, ids, k, v, tables, lens, seqs=None, *, layer: int = 0, k_
     (negative: no key); the rest as for attend_cached.  seqs None: every row
     is the only sequence of the tables, or row t is sequence t."""
     c, dev = _view(k, v, tables, lens, None, k_scale, v_scale, status)
-    return _rows(q, ids, c, dev, seqs, layer, scale, out, out_lse, stream)
+    out = _rows(q, ids, c, dev, seqs, layer, scale, out, out_lse, stream)
+    _kept(stream, out, q, ids, k, v, tables, lens, seqs, k_scale, v_scale, out_lse, status)
+    return out
 
 
 # -------------------------------------------------------------------- pages
@@ -228,6 +247,7 @@ def cache_extend(k, v, tables, lens, refs, seqs, counts, *, k_scale=None, v_scal
     with ctx or _HERE:
         ws, need = _workspace(c, n, dev)
         C.ai_cache_extend(c, ps, pc, n, ws.data_ptr(), need, st)
+    _kept(stream, None, k, v, tables, lens, refs, seqs, counts, k_scale, v_scale, status)
 
 
 def cache_write(k, v, tables, lens, seqs, cu, new_k, new_v, *, refs=None, layer: int = 0, k_scale=None, v_scale=None,
@@ -243,6 +263,7 @@ def cache_write(k, v, tables, lens, seqs, cu, new_k, new_v, *, refs=None, layer:
     st, ctx = _on(dev, stream)
     with ctx or _HERE:
         C.ai_cache_write(c, layer, pk, pv, ps, pc, n, shape[0], st)
+    _kept(stream, None, k, v, tables, lens, refs, seqs, cu, new_k, new_v, k_scale, v_scale, status)
 
 
 def cache_fork(k, v, tables, lens, refs, src, dst, *, k_scale=None, v_scale=None, status=None, stream=None):
@@ -254,6 +275,7 @@ def cache_fork(k, v, tables, lens, refs, src, dst, *, k_scale=None, v_scale=None
     with ctx or _HERE:
         ws, need = _workspace(c, n, dev)
         C.ai_cache_fork(c, ps, pd, n, ws.data_ptr(), need, st)
+    _kept(stream, None, k, v, tables, lens, refs, src, dst, k_scale, v_scale, status)
 
 
 def cache_free(tables, lens, refs, seqs, *, page_size: int, status=None, stream=None):
@@ -268,6 +290,7 @@ def cache_free(tables, lens, refs, seqs, *, page_size: int, status=None, stream=
     st, ctx = _on(dev, stream)
     with ctx or _HERE:
         C.ai_cache_free(c, ps, seqs.shape[0], st)
+    _kept(stream, None, tables, lens, refs, seqs, status)
 
 
 def cache_compact(k, v, tables, lens, refs, *, k_scale=None, v_scale=None, status=None, stream=None):
@@ -277,6 +300,7 @@ def cache_compact(k, v, tables, lens, refs, *, k_scale=None, v_scale=None, statu
     with ctx or _HERE:
         ws, need = _workspace(c, 0, dev)
         C.ai_cache_compact(c, ws.data_ptr(), need, st)
+    _kept(stream, None, k, v, tables, lens, refs, k_scale, v_scale, status)
 
 
 class PagedCache:

@@ -18,7 +18,7 @@ if not torch.cuda.is_available():  # pragma: no cover
 
 from ivf_top_key_b200 import (AiError, C, PagedCache, attend_cached, attend_check, attend_prompt,  # noqa: E402
                               attend_selected, cache_extend, cache_write)
-from tests.test_gpu_attention import DEV, _cache, _gen, _i32, _prompt, _q  # noqa: E402
+from tests.test_gpu_attention import DEV, _cache, _gen, _i32, _ids, _prompt, _q  # noqa: E402
 
 
 @pytest.mark.parametrize("asked", [0, 80, 96, 97, 112, 128, 129, 144, 256])
@@ -280,3 +280,59 @@ def test_extend_to_almost_2_31_tokens():
     torch.cuda.synchronize()
     assert status.item() == 0 and lens.tolist() == [0, 2 ** 31 - 2] and (refs == 1).all()
     assert torch.equal(tables[1], torch.arange(width, dtype=torch.int32, device=DEV)) and (tables[0] == -1).all()
+
+
+def test_inputs_of_a_call_on_another_stream_may_be_dropped_after_it():
+    args, _, _ = _cache([700, 65], 64, 2, 64, "bf16", seed=71, layers=1, layer=0)
+    q = _q(2, 8, 64, 72).to(DEV)
+    ids = _i32(_ids(2, 65, 60, 73))
+    k, v = (torch.randn(2, 2, 64, generator=_gen(s)).bfloat16().to(DEV) for s in (74, 75))
+    cu = _i32([0, 1, 2])
+    c = PagedCache(n_pages=4, page_size=4, n_kv_heads=2, head_dim=64, n_seqs=2, max_pages=2)
+    s = torch.cuda.Stream()
+
+    def dropped(call, *inputs):
+        held = [x.clone() for x in inputs]
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            torch.cuda._sleep(40_000_000)
+        out = call(*[held.pop(0) for _ in inputs], stream=s)
+        junk = [torch.full_like(x, 3) for x in inputs for _ in range(4)]   # where the inputs were, if that is free
+        torch.cuda.synchronize()
+        del junk
+        return out
+
+    assert torch.equal(dropped(lambda x, stream: attend_cached(x, stream=stream, **args), q), attend_cached(q, **args))
+    assert torch.equal(dropped(lambda x, i, stream: attend_selected(x, i, stream=stream, **args), q, ids),
+                       attend_selected(q, ids, **args))
+    assert torch.equal(dropped(attend_prompt, q, k, v, cu), attend_prompt(q, k, v, cu))
+    seqs, ones = _i32([1, 0]), _i32([1, 1])
+    dropped(c.extend, seqs, ones)
+    assert c.lens.tolist() == [1, 1] and c.tables[:, 0].tolist() == [1, 0]
+    dropped(c.write, seqs, cu, k, v)
+    assert torch.equal(c.k[0, :2, 0], k) and torch.equal(c.v[0, :2, 0], v)
+    dropped(c.fork, _i32([0]), _i32([1]))
+    dropped(c.free, _i32([0]))
+    assert c.lens.tolist() == [0, 1]
+
+
+def test_an_output_of_another_stream_may_be_dropped_while_it_is_read():
+    args, _, _ = _cache([700, 65], 64, 2, 64, "bf16", seed=76, layers=1, layer=0)
+    q = _q(2, 8, 64, 77).to(DEV)
+    k, cu = q[:, :2].contiguous(), _i32([0, 1, 2])
+    s = torch.cuda.Stream()
+    minus = -q
+    for call in (lambda x: attend_cached(x, stream=s, **args), lambda x: attend_prompt(x, k, k, cu, stream=s)):
+        s.wait_stream(torch.cuda.current_stream())
+        want = call(q)
+        torch.cuda.synchronize()
+        want + 0   # (the kernel's first launch may wait for the device)
+        out = call(q)
+        torch.cuda.current_stream().wait_stream(s)
+        torch.cuda._sleep(40_000_000)
+        got = out + 0
+        del out
+        others = [call(minus) for _ in range(4)]   # on s, which does not wait for the copy
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
+        del others
