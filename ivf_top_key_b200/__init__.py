@@ -14,8 +14,8 @@ import torch
 
 from . import _capi as C
 from ._capi import AiError  # noqa: F401
-from .attention import (PagedCache, attend_cached, attend_check, attend_prompt, attend_selected, cache_compact,
-                        cache_extend, cache_fork, cache_free, cache_write)
+from .attention import (PagedCache, _kept, attend_cached, attend_check, attend_prompt, attend_selected,
+                        cache_compact, cache_extend, cache_fork, cache_free, cache_write)
 
 __all__ = ["AttentionIndex", "AiError", "quantize_fp8", "merge_topk", "C", "PagedCache", "attend_prompt",
            "attend_cached", "attend_selected", "attend_check", "cache_extend", "cache_write", "cache_fork",
@@ -103,9 +103,13 @@ class AttentionIndex:
         cache.write before it belong there too.  Returns the attention output [T, Hq, D]."""
         with torch.cuda.stream(self.stream):
             ids = self.route_refine(q_index, w, pos0, k, C_budget, out=out_ids)
-            return attend_selected(q, ids, cache.k, cache.v, cache.tables[seq:seq + 1], cache.lens[seq:seq + 1],
-                                   layer=layer, k_scale=cache.k_scale, v_scale=cache.v_scale, scale=scale, out=out,
-                                   out_lse=out_lse, status=cache.status)
+            out = attend_selected(q, ids, cache.k, cache.v, cache.tables[seq:seq + 1], cache.lens[seq:seq + 1],
+                                  layer=layer, k_scale=cache.k_scale, v_scale=cache.v_scale, scale=scale, out=out,
+                                  out_lse=out_lse, status=cache.status)
+        if torch.cuda.current_stream(self.device) != self.stream:
+            _kept(self.stream, out, q_index, w, q, out_ids, out_lse, cache.k, cache.v, cache.tables, cache.lens,
+                  cache.k_scale, cache.v_scale, cache.status)
+        return out
 
     def select_exhaustive(self, q, w, pos0: int, k: int, out=None, out_scores=None):
         if out is None:

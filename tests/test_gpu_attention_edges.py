@@ -16,8 +16,8 @@ pytestmark = pytest.mark.gpu
 if not torch.cuda.is_available():  # pragma: no cover
     pytest.skip("needs a GPU", allow_module_level=True)
 
-from ivf_top_key_b200 import (AiError, C, PagedCache, attend_cached, attend_check, attend_prompt,  # noqa: E402
-                              attend_selected, cache_extend, cache_write)
+from ivf_top_key_b200 import (AiError, AttentionIndex, C, PagedCache, attend_cached, attend_check,  # noqa: E402
+                              attend_prompt, attend_selected, cache_extend, cache_write)
 from tests.test_gpu_attention import DEV, _cache, _gen, _i32, _ids, _prompt, _q  # noqa: E402
 
 
@@ -336,3 +336,49 @@ def test_an_output_of_another_stream_may_be_dropped_while_it_is_read():
         torch.cuda.synchronize()
         assert torch.equal(got, want)
         del others
+
+
+def test_attend_of_an_index_with_its_own_stream():
+    """The queries may be dropped after the call, the output while the current stream still reads it."""
+    d, H, D, n, T, k = 128, 32, 64, 512, 64, 40
+    ik, iq = (torch.randn(m, *t, d, generator=_gen(80 + m)).bfloat16().to(DEV) for m, t in ((n, ()), (T, (H,))))
+    w, q = torch.randn(T, H, generator=_gen(81)).to(DEV), _q(T, 4, D, 82).to(DEV)
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        idx = AttentionIndex(d=d, H=H, window=128, clusters_per_window=4, refit_period=0, max_query_chunk=T, max_budget=256,
+                             max_k=k, max_keys=n)
+    c = PagedCache(n_pages=40, page_size=16, n_kv_heads=2, head_dim=D, n_seqs=1, max_pages=32)
+    c.extend(_i32([0]), _i32([n]))
+    kv = torch.randn(n, 2, D, generator=_gen(83)).bfloat16().to(DEV)
+    c.write(_i32([0]), _i32([0, n]), kv, kv)
+    torch.cuda.synchronize()
+    idx.append_keys(ik)
+    idx.seal()
+    want = idx.attend(iq, w, n - T, k, 256, q, c)
+    minus = -q
+    idx.sync()
+    torch.cuda.synchronize()
+    assert want.isfinite().all() and want.abs().max() > 0
+    want + 0   # (the kernel's first launch may wait for the device)
+    # inputs
+    held = [iq.clone(), w.clone(), q.clone()]
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(40_000_000)
+    out = idx.attend(held.pop(0), held.pop(0), n - T, k, 256, held.pop(0), c)
+    junk = [torch.full_like(x, 3) for x in (iq, w, q) for _ in range(4)]
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+    del junk, out
+    # the output
+    out = idx.attend(iq, w, n - T, k, 256, q, c)
+    torch.cuda.current_stream().wait_stream(s)
+    torch.cuda._sleep(40_000_000)
+    got = out + 0
+    del out
+    others = [idx.attend(iq, w, n - T, k, 256, minus, c) for _ in range(4)]
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
+    del others
+    c.check()
+    idx.close()
