@@ -857,7 +857,7 @@ extern "C" int ai_attend_selected(const ai_cache* cache, int32_t layer, const vo
                                   void* out_dev, float* lse_dev, void* workspace_dev, int64_t workspace_bytes,
                                   void* cuda_stream) {
   using namespace aiidx;
-  if (!ids_dev) return fail(AI_ERR_ARG, "null pointer argument");
+  if (T > 0 && !ids_dev) return fail(AI_ERR_ARG, "null pointer argument");
   if (k <= 0) return fail(AI_ERR_ARG, "k must be positive");
   return run_rows(cache, layer, q_dev, T, n_heads, ids_dev, k, seqs_dev, scale, out_dev, lse_dev, workspace_dev,
                   workspace_bytes, cuda_stream);

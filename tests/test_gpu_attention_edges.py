@@ -382,3 +382,38 @@ def test_attend_of_an_index_with_its_own_stream():
     del others
     c.check()
     idx.close()
+
+
+def test_no_rows_and_empty_lists_of_ids():
+    c = PagedCache(n_pages=2, page_size=4, n_kv_heads=1, head_dim=64, n_seqs=1, max_pages=2)
+    q = torch.empty(0, 2, 64, dtype=torch.bfloat16, device=DEV)
+    assert c.attend_selected(q, torch.empty(0, 5, dtype=torch.int32, device=DEV)).shape == (0, 2, 64)
+    assert c.attend(q, _i32([])).shape == (0, 2, 64)
+    c.check()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp8"])
+def test_compact_moves_all_layers_and_scales(dtype):
+    page, n = 8, [13, 30, 8, 21]
+    c = PagedCache(n_pages=16, page_size=page, n_kv_heads=2, head_dim=64, n_seqs=5, max_pages=4, dtype=dtype, n_layers=3)
+    c.extend(_i32(list(range(4))), _i32(n))
+    cu = _i32([0, 13, 43, 51, 72])
+    for layer in range(3):
+        x = torch.randn(72, 2, 64, generator=_gen(layer)).bfloat16().to(DEV)
+        c.write(_i32(list(range(4))), cu, x, x * 2, layer=layer)
+    c.fork(_i32([1]), _i32([4]))
+    c.free(_i32([0, 2]))
+    c.check()
+    parts = [t for t in (c.k, c.v, c.k_scale, c.v_scale) if t is not None]
+
+    def tokens(s, length):
+        at = c.tables[s, :-(-length // page)].long()
+        return [t[:, at].flatten(1, 2)[:, :length].clone() for t in parts]
+
+    before = {s: tokens(s, m) for s, m in ((1, 30), (3, 21), (4, 30))}
+    c.compact()
+    c.check()
+    assert c.refs.tolist() == [1, 1, 2, 2, 2, 1, 1, 1] + [0] * 8
+    for s, want in before.items():
+        for a, b in zip(tokens(s, 21 if s == 3 else 30), want):
+            assert torch.equal(a, b)
