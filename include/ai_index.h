@@ -330,7 +330,9 @@ int ai_refine_kernel_choice(ai_handle h, int32_t C, int32_t* kernel_out);
  * n_heads query heads share n_kv_heads key heads in groups of
  * n_heads / n_kv_heads consecutive heads.  Queries and outputs are bf16,
  * sums and statistics float32, weights rounded to bf16 for the product with
- * v; head_dim is 64 or 128, scale finite and not negative.
+ * v (fp8 caches: to f16, 11 bits down to 2^-15 of a row's largest weight and
+ * below that to within 2^-26 of it); head_dim is 64 or 128, scale finite and
+ * not negative.
  * The calls are enqueued on cuda_stream, allocate nothing and may be captured;
  * they need no handle.  Calls whose work may overlap (two streams, two graphs)
  * need a workspace each.                                                  */

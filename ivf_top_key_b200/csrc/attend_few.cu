@@ -309,9 +309,8 @@ __global__ void __launch_bounds__(Few<D, FP8>::kThreads, 1) k_attend_few(const R
     };
     // The maximum moves only when it grows by more than 2^kGrow: the weights
     // stay in range and most tiles leave o as it is.  fp8: weights are
-    // 2^kLift e^(s - m) * (value scale / largest value scale so far), in f16:
-    // 11 bits down to 2^-25 of the largest, smaller ones to within 2^-36 of
-    // it, and at most 2^15.
+    // 2^kLift e^(s - m) * (value scale / 2^base), in f16: 11 bits down to 2^-25
+    // of the largest, smaller ones to within 2^-36 of it, and at most 2^15.
     constexpr float kGrow = FP8 ? 4.f : 8.f, kLift = 11.f;
     uint32_t n0 = 0, share = 0;
     // this warp's first tile of a share whose first tile is the CTA's n-th
@@ -339,7 +338,7 @@ __global__ void __launch_bounds__(Few<D, FP8>::kThreads, 1) k_attend_few(const R
       const bool mine = own < t1;
       float c2[2] = {a.c2, a.c2};        // by head 2 t, 2 t + 1
       float o[D / 16][4], m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
-      float e_run = -INFINITY;           // fp8: log2 of the largest value scale so far
+      float base = -INFINITY, top = -INFINITY;   // fp8: see scale_base
       if (mine) {
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
@@ -371,13 +370,15 @@ __global__ void __launch_bounds__(Few<D, FP8>::kThreads, 1) k_attend_few(const R
         }
       }
       bool begun = false;
-      for (int at = own; at < t1; at += kComp) {
+      float far = INFINITY;              // fp8: the tile's keys of this log2 scale and more are done
+      for (int at = own; at < t1;) {
         const uint32_t n = n0 + (at - t0), st = n % S;
         if (!__all_sync(0xffffffffu, mbar_wait(&full[st], (n / S) & 1, err, abort))) {
           ok = false;
           break;
         }
         const uint32_t real = reals[st];
+        bool again = false;
         if (real) {
           const uint8_t* stage = stages + st * 2 * L::kKV;
           const uint32_t sk = smem_u32(stage), sv = sk + L::kKV;
@@ -418,7 +419,7 @@ __global__ void __launch_bounds__(Few<D, FP8>::kThreads, 1) k_attend_few(const R
           // scale, mask and the running maximum; rows g and g + 8 of block j are
           // keys 16 j + key(g) and 8 behind it
           const float* ksc = scales + st * 2 * kTile + L::key(g);
-          float lv[4], e_max = e_run;
+          float lv[4];
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             float f0 = 1.f, f1 = 1.f;
@@ -427,7 +428,6 @@ __global__ void __launch_bounds__(Few<D, FP8>::kThreads, 1) k_attend_few(const R
               f1 = ksc[j * 16 + 8];
               lv[2 * j] = __log2f(ksc[kTile + j * 16]);
               lv[2 * j + 1] = __log2f(ksc[kTile + j * 16 + 8]);
-              e_max = fmaxf(e_max, fmaxf(lv[2 * j], lv[2 * j + 1]));
             }
             s[j][0] *= c2[0] * f0;
             s[j][1] *= c2[1] * f0;
@@ -452,21 +452,45 @@ __global__ void __launch_bounds__(Few<D, FP8>::kThreads, 1) k_attend_few(const R
 #pragma unroll
             for (int d = 4; d < 32; d *= 2) mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], d));
           }
-          if constexpr (FP8) {
-#pragma unroll
-            for (int d = 4; d < 32; d *= 2) e_max = fmaxf(e_max, __shfl_xor_sync(0xffffffffu, e_max, d));
-          }
           const bool move0 = mx[0] > -INFINITY && (m_run[0] == -INFINITY || mx[0] > m_run[0] + kGrow);
           const bool move1 = mx[1] > -INFINITY && (m_run[1] == -INFINITY || mx[1] > m_run[1] + kGrow);
-          if (__any_sync(0xffffffffu, move0 || move1) || (FP8 && e_max > e_run)) {
+          bool move = move0 || move1;
+          float first = 1.f;              // the sum takes a tile's weights once
+          if constexpr (FP8) {
+            if (far != INFINITY) {
+              first = 0.f;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) lv[i] = lv[i] < far ? lv[i] : -INFINITY;
+            }
+            move |= fmaxf(fmaxf(lv[0], lv[1]), fmaxf(lv[2], lv[3])) > base;
+            move |= fminf(fminf(lv[0], lv[1]), fminf(lv[2], lv[3])) < base - kSpan;
+          }
+          if (__any_sync(0xffffffffu, move)) {
             const float m0 = move0 ? mx[0] : m_run[0], m1 = move1 ? mx[1] : m_run[1];
             const float f0 = move0 ? exp2_approx(m_run[0] - m0) : 1.f, f1 = move1 ? exp2_approx(m_run[1] - m1) : 1.f;
             m_run[0] = m0;
             m_run[1] = m1;
+            float fe = 1.f;
+            if constexpr (FP8) {
+              float e = fmaxf(fmaxf(lv[0], lv[1]), fmaxf(lv[2], lv[3]));
+#pragma unroll
+              for (int d = 4; d < 32; d *= 2) e = fmaxf(e, __shfl_xor_sync(0xffffffffu, e, d));
+              e = ceilf(e);
+              const float b = scale_base(e, base, far == INFINITY, &top);
+              if (b != base) fe = pow2(base - b);
+              base = b;
+              far = fminf(b - kSpan, e - 1.f);
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                if (lv[i] < far) {      // another pass
+                  again |= lv[i] != -INFINITY;
+                  lv[i] = -INFINITY;
+                }
+              again = __any_sync(0xffffffffu, again);
+            }
             if (begun) {
               l_run[0] *= f0;
               l_run[1] *= f1;
-              const float fe = FP8 && e_max > e_run ? exp2_approx(e_run - e_max) : 1.f;
               const float g0 = f0 * fe, g1 = f1 * fe;
 #pragma unroll
               for (int i = 0; i < D / 16; ++i) {
@@ -476,7 +500,6 @@ __global__ void __launch_bounds__(Few<D, FP8>::kThreads, 1) k_attend_few(const R
                 o[i][3] *= g1;
               }
             }
-            e_run = e_max;
           }
           begun = true;
           // a head without a finite score so far: exponents against 0 (all e^-inf = 0)
@@ -484,7 +507,7 @@ __global__ void __launch_bounds__(Few<D, FP8>::kThreads, 1) k_attend_few(const R
           // the weights for the product with v, as two bf16 terms (16 bits; the
           // products have time left: reading bounds) or, fp8, as one f16 (11
           // bits); their sum is taken before that rounding
-          const float lift = kLift - (e_run == -INFINITY ? 0.f : e_run);
+          const float lift = kLift - (base == -INFINITY ? 0.f : base);
           uint32_t p[2][2], rest[2][2];
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
@@ -492,8 +515,8 @@ __global__ void __launch_bounds__(Few<D, FP8>::kThreads, 1) k_attend_few(const R
             for (int i = 0; i < 2; ++i) {
               const float x0 = s[j][2 * i] - mu[0], x1 = s[j][2 * i + 1] - mu[1];
               const float e0 = exp2_approx(x0), e1 = exp2_approx(x1);
-              l_run[0] += e0;
-              l_run[1] += e1;
+              l_run[0] = FP8 ? fmaf(e0, first, l_run[0]) : l_run[0] + e0;
+              l_run[1] = FP8 ? fmaf(e1, first, l_run[1]) : l_run[1] + e1;
               if constexpr (FP8) {
                 const float v0 = lv[2 * j + i] + lift;
                 p[j][i] = transposed(pack_f16(exp2_approx(x0 + v0), exp2_approx(x1 + v0)));
@@ -537,8 +560,11 @@ __global__ void __launch_bounds__(Few<D, FP8>::kThreads, 1) k_attend_few(const R
               }
           }
         }
+        if (FP8 && again) continue;
+        far = INFINITY;
         __syncwarp();
         if (lane == 0) mbar_arrive(&empty[st]);
+        at += kComp;
       }
       if (!ok) break;
       n0 += t1 - t0;
@@ -548,7 +574,7 @@ __global__ void __launch_bounds__(Few<D, FP8>::kThreads, 1) k_attend_few(const R
 #pragma unroll
           for (int d = 4; d < 32; d *= 2) l_run[i] += __shfl_xor_sync(0xffffffffu, l_run[i], d);
       }
-      const float unlift = !FP8 ? 1.f : (e_run == -INFINITY ? 0.f : exp2_approx(e_run - kLift));
+      const float unlift = !FP8 ? 1.f : (base == -INFINITY ? 0.f : exp2_approx(base - kLift));
       if (alone) {
         if (mine) {
 #pragma unroll

@@ -292,13 +292,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     float o[D / 8][4];
     float m_run[2], l_run[2];
     float c2[2] = {a.c2, a.c2};                    // by row: scale * log2 e (fp8: and the queries' power of two)
-    float e_run = -INFINITY;                       // fp8: log2 of the largest value scale so far
+    float base = -INFINITY, top = -INFINITY;       // fp8: see scale_base
     bool begun = false;
     // The maximum moves only when it grows by more than 2^kGrow: the weights
     // stay in range and most tiles leave o as it is.  fp8: weights are
-    // 2^kLift e^(s - m) * (value scale / largest value scale so far), in f16:
-    // 11 bits down to 2^-25 of the largest, smaller ones to within 2^-36 of
-    // it, and at most 2^15.
+    // 2^kLift e^(s - m) * (value scale / 2^base), in f16: 11 bits down to 2^-25
+    // of the largest, smaller ones to within 2^-36 of it, and at most 2^15.
     constexpr float kGrow = FP8 ? 4.f : 8.f, kLift = 11.f;
 
     uint32_t n = 0, n_shares = 0;
@@ -349,7 +348,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int j = i; j < 4; j += 2)
                 qf[kk][j] = pack_f16(__uint_as_float(qf[kk][j] << 16) * f, __uint_as_float(qf[kk][j] & 0xffff0000u) * f);
           }
-          e_run = -INFINITY;
+          base = top = -INFINITY;
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&q_empty[qs]);
@@ -359,7 +358,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         l_run[0] = l_run[1] = 0.f;
         begun = false;
       }
-      for (int tile = x.t0; tile < x.t1; ++tile, ++n) {
+      // fp8, by block of a tile's keys: those of this log2 scale and more are done
+      float far[NK / NB];
+#pragma unroll
+      for (int i = 0; i < NK / NB; ++i) far[i] = INFINITY;
+      for (int tile = x.t0; tile < x.t1;) {
         const uint32_t st = n % S;
         if (!__all_sync(0xffffffffu, mbar_wait(&full[st], (n / S) & 1, err, abort))) {
           ok = false;
@@ -367,13 +370,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const uint8_t* stage = stages + st * 2 * L::kKV;
         const uint32_t sk = smem_u32(stage), sv = sk + L::kKV;
+        bool again = false;
         if ((n & 1) == group) {
 #pragma unroll
           for (int blk = 0; blk < NK / NB; ++blk) {
             const int k0 = wk * NK + blk * NB;      // first key of the block
             constexpr uint32_t kAll = NB == 32 ? 0xffffffffu : (1u << (NB % 32)) - 1;
             const uint32_t real = (reals[st * 4 + k0 / 32] >> (k0 % 32)) & kAll;  // its keys, one bit each
-            if (real == 0) continue;
+            if (real == 0 || (FP8 && far[blk] == -INFINITY)) continue;
+            float left = -INFINITY;                 // fp8: keys below it need another pass
             float s[NB / 8][4];
 #pragma unroll
             for (int j = 0; j < NB / 8; ++j) s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
@@ -415,7 +420,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // scale, mask and the running maximum
             const float* ksc = scales + st * 2 * kTile + k0;
             float mx[2] = {-INFINITY, -INFINITY};
-            float lv[FP8 ? NB / 4 : 1], e_max = e_run;
+            float lv[FP8 ? NB / 4 : 1], hi = -INFINITY, lo = INFINITY;   // fp8: log2 of the value scales
 #pragma unroll
             for (int j = 0; j < NB / 8; ++j) {
               if constexpr (FP8) {
@@ -427,7 +432,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 s[j][3] *= c2[1] * f1;
                 lv[2 * j] = __log2f(ksc[kTile + i0]);
                 lv[2 * j + 1] = __log2f(ksc[kTile + i1]);
-                e_max = fmaxf(e_max, fmaxf(lv[2 * j], lv[2 * j + 1]));
+                hi = fmaxf(hi, fmaxf(lv[2 * j], lv[2 * j + 1]));
+                lo = fminf(lo, fminf(lv[2 * j], lv[2 * j + 1]));
               } else {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) s[j][i] *= a.c2;
@@ -454,21 +460,46 @@ __global__ void __launch_bounds__(kThreads, 1)
               mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 1));
               mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 2));
             }
-            if constexpr (FP8) {
-              e_max = fmaxf(e_max, __shfl_xor_sync(0xffffffffu, e_max, 1));
-              e_max = fmaxf(e_max, __shfl_xor_sync(0xffffffffu, e_max, 2));
-            }
             const bool move0 = !begun ? mx[0] > -INFINITY : mx[0] > m_run[0] + kGrow || (m_run[0] == -INFINITY && mx[0] > -INFINITY);
             const bool move1 = !begun ? mx[1] > -INFINITY : mx[1] > m_run[1] + kGrow || (m_run[1] == -INFINITY && mx[1] > -INFINITY);
-            if (__any_sync(0xffffffffu, move0 || move1) || (FP8 && e_max > e_run)) {
+            float first = 1.f;                      // the sum takes a block's weights once
+            if (FP8 && far[blk] != INFINITY) {
+              first = 0.f;
+              hi = lo = -INFINITY;
+#pragma unroll
+              for (int i = 0; i < NB / 4; ++i) {
+                lv[i] = lv[i] < far[blk] ? lv[i] : -INFINITY;
+                hi = fmaxf(hi, lv[i]);
+              }
+            }
+            if (__any_sync(0xffffffffu, move0 || move1 || (FP8 && (hi > base || lo < base - kSpan)))) {
               const float m0 = move0 ? mx[0] : m_run[0], m1 = move1 ? mx[1] : m_run[1];
               const float f0 = move0 ? exp2_approx(m_run[0] - m0) : 1.f, f1 = move1 ? exp2_approx(m_run[1] - m1) : 1.f;
               m_run[0] = m0;
               m_run[1] = m1;
+              float fe = 1.f;
+              if constexpr (FP8) {
+                float e = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, 1));
+                e = ceilf(fmaxf(e, __shfl_xor_sync(0xffffffffu, e, 2)));
+                const float b = scale_base(e, base, far[blk] == INFINITY, &top);
+                if (b != base) fe = pow2(base - b);
+                base = b;
+                const float low = fminf(b - kSpan, e - 1.f);
+                bool more = false;
+#pragma unroll
+                for (int i = 0; i < NB / 4; ++i)
+                  if (lv[i] < low) {
+                    more |= lv[i] != -INFINITY;
+                    lv[i] = -INFINITY;
+                  }
+                if (__any_sync(0xffffffffu, more)) {
+                  left = low;
+                  again = true;
+                }
+              }
               if (begun) {
                 l_run[0] *= f0;
                 l_run[1] *= f1;
-                const float fe = FP8 && e_max > e_run ? exp2_approx(e_run - e_max) : 1.f;
                 const float g0 = f0 * fe, g1 = f1 * fe;
 #pragma unroll
                 for (int i = 0; i < D / 8; ++i) {
@@ -478,7 +509,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                   o[i][3] *= g1;
                 }
               }
-              e_run = e_max;
             }
             begun = true;
             // a row without a finite score so far: exponents against 0 (all e^-inf = 0)
@@ -486,13 +516,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             // the weights, rounded once (bf16; fp8: f16) for the product with v;
             // their sum is taken before that rounding
             uint32_t p[NB / 16][4];
-            const float lift = kLift - (e_run == -INFINITY ? 0.f : e_run);
+            const float lift = kLift - (base == -INFINITY ? 0.f : base);
 #pragma unroll
             for (int j = 0; j < NB / 8; ++j) {
               const float x0 = s[j][0] - mu[0], x1 = s[j][1] - mu[0], x2 = s[j][2] - mu[1], x3 = s[j][3] - mu[1];
               const float e0 = exp2_approx(x0), e1 = exp2_approx(x1), e2 = exp2_approx(x2), e3 = exp2_approx(x3);
-              l_run[0] += e0 + e1;
-              l_run[1] += e2 + e3;
+              l_run[0] = FP8 ? fmaf(e0 + e1, first, l_run[0]) : l_run[0] + (e0 + e1);
+              l_run[1] = FP8 ? fmaf(e2 + e3, first, l_run[1]) : l_run[1] + (e2 + e3);
               if constexpr (FP8) {
                 const float v0 = lv[2 * j] + lift, v1 = lv[2 * j + 1] + lift;
                 p[j / 2][(j & 1) * 2 + 0] = pack_f16(exp2_approx(x0 + v0), exp2_approx(x1 + v1));
@@ -539,10 +569,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
               }
             }
+            far[blk] = left;
           }
         }
+        if (FP8 && again) continue;
+#pragma unroll
+        for (int i = 0; i < NK / NB; ++i) far[i] = INFINITY;
         __syncwarp();
         if (lane == 0) mbar_arrive(&empty[st]);
+        ++tile;
+        ++n;
       }
       if (!ok) break;
       {
@@ -553,7 +589,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           l_run[i] += __shfl_xor_sync(0xffffffffu, l_run[i], 2);
         }
         if constexpr (FP8) {
-          const float f = e_run == -INFINITY ? 0.f : exp2_approx(e_run - kLift);
+          const float f = base == -INFINITY ? 0.f : exp2_approx(base - kLift);
 #pragma unroll
           for (int i = 0; i < D / 8; ++i) {
             o[i][0] *= f;

@@ -93,6 +93,22 @@ __device__ __forceinline__ void cp4z(uint32_t dst, const void* src, bool real) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(real ? 4 : 0) : "memory");
 }
 
+// fp8: weights times value scales are f16 for the product with v, held against
+// 2^base, which follows the tiles' largest value scales: up at once, down where a
+// tile's is 2^kFall lower, so that a few keys of far larger scales (or zeros, whose
+// scale is 1) do not take the others' bits.  Keys whose scales are more than
+// 2^kSpan below it have a pass of their own over the tile.  The output so far,
+// fp32, is rescaled with base, exactly, and stays in range: base keeps within 60
+// of its largest (top).  e: log2 of the largest scale of a tile, rounded up.
+constexpr float kFall = 6.f, kSpan = 10.f;
+__device__ __forceinline__ float scale_base(float e, float base, bool first_pass, float* top) {
+  *top = fmaxf(*top, e);
+  if (e > base) return e;
+  return e != -INFINITY && (!first_pass || e < base - kFall) ? fmaxf(e, *top - 60.f) : base;
+}
+// 2^x for a whole x up to 127; 0 below -126
+__device__ __forceinline__ float pow2(float x) { return __int_as_float(max(0, static_cast<int>(x) + 127) << 23); }
+
 // ----------------------------------------------------------- division of work
 // Division of a token (< 2^31) by the page size: with s = ceil(log2 d),
 // m = ceil(2^(31 + s) / d) < 2^32 the quotient is exactly n m >> (31 + s)

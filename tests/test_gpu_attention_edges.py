@@ -417,3 +417,38 @@ def test_compact_moves_all_layers_and_scales(dtype):
     for s, want in before.items():
         for a, b in zip(tokens(s, 21 if s == 3 else 30), want):
             assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("Hq,Hkv", [(1, 1), (16, 2), (24, 1), (64, 1)])
+@pytest.mark.parametrize("what", ["zero", "every fourth zero", "outlier"])
+def test_fp8_values_beside_far_larger_scales_keep_their_weights(Hq, Hkv, what):
+    """Values 2^-30 of ordinary ones beside some that are zero (scale 1, as quantize_fp8 makes it), and ordinary values
+    beside some of 2^30 that weigh nothing (a score 100 below the others): what the others give is as exact as ever."""
+    D, n = 64, 3000
+    args, kd, vd = _cache([n], 64, Hkv, D, "fp8", seed=90, layers=1, layer=0)
+    page = args["tables"][0].tolist()
+    q = _q(1, Hq, D, 91)
+    q[:, :, 0] = 8
+    if what != "outlier":
+        args["v_scale"] *= 2.0 ** -30
+        vd[0] *= 2.0 ** -30
+    for j in range(0, n, 4) if what == "every fourth zero" else (0, 700, 701, 1500, n - 1):
+        at = 0, page[j // 64], j % 64
+        if what != "outlier":
+            args["v"][at] = 0
+            args["v_scale"][at] = 1
+            vd[0][j] = 0
+        else:
+            args["k"][at] = 0
+            args["k"][at][:, 0] = 0xFE    # -448
+            args["k_scale"][at] = 0.25
+            kd[0][j] = 0
+            kd[0][j, :, 0] = -112
+            args["v_scale"][at] *= 2.0 ** 30
+            vd[0][j] *= 2.0 ** 30
+    lse, status = torch.empty(1, Hq, device=DEV), _i32([0])
+    want = [R.attend(q[0].double(), kd[0], vd[0], D ** -0.5)]
+    for out in (attend_cached(q.to(DEV), out_lse=lse, status=status, **args),
+                attend_selected(q.to(DEV), _i32([list(range(n))]), out_lse=lse, status=status, **args)):
+        R.check(out, lse, want)
+    assert status.item() == 0
