@@ -16,10 +16,10 @@
 // hand over their states in two buffers that joining warps read, so that
 // no row waits for the one before it.
 //
-// Measured: 4 x 131072 tokens of 8 key heads, bf16: 317 us, 6.8 TB/s (a plain
-// read of the same bytes); 48 sequences of up to 8192 tokens, fp8: 109 us, 4.2
-// TB/s.  What bounds fp8 is the widening: half of the issue slots and 46 % of the
-// ALU slots (tiles of 64 keys and ten computing warps measured the same).
+// Measured: 4 x 131072 tokens of 8 key heads, bf16: 320 us, 6.7 TB/s (a plain
+// read of the same bytes); 48 sequences of up to 8192 tokens, fp8: 98 to 102 us,
+// 4.5 TB/s.  What bounds fp8 is the widening: half of the issue slots and 46 % of
+// the ALU slots (tiles of 64 keys and ten computing warps measured the same).
 #include "attend_rows.cuh"
 
 namespace aiidx {

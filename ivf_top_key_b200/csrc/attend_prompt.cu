@@ -33,7 +33,8 @@
 // Rows behind the sequence's end are zeroed there, and so are values that are
 // not finite, whose keys are listed; the rows that see such a key add its
 // infinity or NaN to their outputs at the end.  So the bits of every other
-// output are what they would be without it.
+// output are what they would be without it (16384 tokens, all values NaN: 1.26 ms,
+// one key in a thousand infinite: as without).
 //
 // Measured: 16384 tokens, 16 heads on 2, D = 128: 0.89 ms in a short run (1230
 // TFLOP/s, 0.75 of the measured bf16 product), 1.02 ms in a long one; a chunk of

@@ -15,7 +15,7 @@
 // attend_few.cu: 4 x 131072 tokens of 8 key heads 317 us there, 356 us here.
 //
 // Measured: 8192 rows of 2048 of 131072 keys, one key head of 32 query heads:
-// 1.35 ms, 8.6 GB of rows from L2 (6.4 TB/s) and 204 TFLOP/s.  It is the
+// 1.30 ms, 8.6 GB of rows from L2 (6.6 TB/s) and 211 TFLOP/s.  It is the
 // computing warps' latency that bounds it (two an SM quarter, what their
 // registers leave): without the products the same copies take 1.06 ms.
 //
@@ -513,8 +513,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             begun = true;
             // a row without a finite score so far: exponents against 0 (all e^-inf = 0)
             const float mu[2] = {m_run[0] == -INFINITY ? 0.f : m_run[0], m_run[1] == -INFINITY ? 0.f : m_run[1]};
-            // the weights, rounded once (bf16; fp8: f16) for the product with v;
-            // their sum is taken before that rounding
+            // the weights, rounded once (bf16; fp8: f16) for the product with v; their
+            // sum is taken before that rounding.  (A second bf16 term, as for few heads,
+            // would double the product where the computing warps are the bound.)
             uint32_t p[NB / 16][4];
             const float lift = kLift - (base == -INFINITY ? 0.f : base);
 #pragma unroll
