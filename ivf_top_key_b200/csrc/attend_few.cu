@@ -479,7 +479,7 @@ __global__ void __launch_bounds__(Few<D, FP8>::kThreads, 1) k_attend_few(const R
               const float b = scale_base(e, base, far == INFINITY, &top);
               if (b != base) fe = pow2(base - b);
               base = b;
-              far = fminf(b - kSpan, e - 1.f);
+              far = scale_rest(e, b);
 #pragma unroll
               for (int i = 0; i < 4; ++i)
                 if (lv[i] < far) {      // another pass

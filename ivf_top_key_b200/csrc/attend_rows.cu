@@ -484,7 +484,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float b = scale_base(e, base, far[blk] == INFINITY, &top);
                 if (b != base) fe = pow2(base - b);
                 base = b;
-                const float low = fminf(b - kSpan, e - 1.f);
+                const float low = scale_rest(e, b);
                 bool more = false;
 #pragma unroll
                 for (int i = 0; i < NB / 4; ++i)

@@ -106,6 +106,10 @@ __device__ __forceinline__ float scale_base(float e, float base, bool first_pass
   if (e > base) return e;
   return e != -INFINITY && (!first_pass || e < base - kFall) ? fmaxf(e, *top - 60.f) : base;
 }
+// The log2 scale below which a tile's keys are left for another pass.  Every pass
+// takes the largest left, so there are at most as many as keys; finite, also
+// where a scale is infinite, as infinity stands for a first pass.
+__device__ __forceinline__ float scale_rest(float e, float base) { return fminf(fminf(base - kSpan, e - 1.f), 1e30f); }
 // 2^x for a whole x up to 127; 0 below -126
 __device__ __forceinline__ float pow2(float x) { return __int_as_float(max(0, static_cast<int>(x) + 127) << 23); }
 

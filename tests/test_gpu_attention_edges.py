@@ -452,3 +452,28 @@ def test_fp8_values_beside_far_larger_scales_keep_their_weights(Hq, Hkv, what):
                 attend_selected(q.to(DEV), _i32([list(range(n))]), out_lse=lse, status=status, **args)):
         R.check(out, lse, want)
     assert status.item() == 0
+
+
+@pytest.mark.parametrize("Hq,Hkv", [(2, 1), (24, 1), (64, 1)])
+def test_fp8_value_scales_of_every_size_end_and_reach_only_their_rows(Hq, Hkv):
+    """Scales over all of fp32's exponents, zero and infinity among them: rows of infinite ones are not finite, the other
+    sequence's rows are as exact as ever."""
+    D, n = 64, 700
+    args, kd, vd = _cache([n, n], 64, Hkv, D, "fp8", seed=95, layers=1, layer=0)
+    r = random.Random(96)
+    for s in range(2):
+        page = args["tables"][s].tolist()
+        for j in range(n):
+            at = 0, page[j // 64], j % 64
+            x = r.choice([0.0, 2.0 ** r.randint(-140, 90), 2.0 ** r.randint(-140, -100), 1.0, torch.inf if s == 0 else 3.0])
+            args["v_scale"][at] = x
+            vd[s][j] = args["v"][at].view(torch.float8_e4m3fn).double().cpu() * x
+    q = _q(2, Hq, D, 97)
+    lse, status = torch.empty(2, Hq, device=DEV), _i32([0])
+    want = R.attend(q[1].double(), kd[1], vd[1], D ** -0.5)
+    ids = _i32([list(range(n))] * 2)
+    for out in (attend_cached(q.to(DEV), out_lse=lse, status=status, **args),
+                attend_selected(q.to(DEV), ids, out_lse=lse, status=status, **args)):
+        assert not out[0].isfinite().any()
+        R.check(out[1:], lse[1:], [want])
+    assert status.item() == 0
